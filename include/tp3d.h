@@ -58,9 +58,12 @@ typedef enum {
   TP3D_ETIMEOUT = 6,     /* a bounded device-side wait ran out                    */
   TP3D_EUNSUPPORTED = 7, /* valid request outside what the kernels implement      */
   TP3D_EOVERLAP = 8,     /* output buffer overlaps an input buffer               */
-  TP3D_ERANGE = 9        /* a value on the layer's fp16 score path (LN1 output,
+  TP3D_ERANGE = 9,       /* a value on the layer's fp16 score path (LN1 output,
                             Q, K) beyond fp16's finite range; raised by a kernel
                             and reported by tp3d_sync_status                     */
+  TP3D_EPAGES = 10       /* a length, page or slot of the paged cache that does
+                            not fit (tp3d_paged.h); raised by a kernel and
+                            reported by tp3d_sync_status                        */
 } tp3d_status;
 
 typedef enum { TP3D_F32 = 0, TP3D_BF16 = 1 } tp3d_dtype;
@@ -109,8 +112,9 @@ const char* tp3d_status_string(tp3d_status s);
 
 /* Synchronises `stream`, then reads and clears the device error word:
  * TP3D_ETIMEOUT if a bounded wait ran out since the last call, TP3D_ERANGE
- * if a layer call met a value its fp16 score path cannot hold, TP3D_ECUDA if
- * the stream reported an error, else TP3D_OK.                               */
+ * if a layer call met a value its fp16 score path cannot hold, TP3D_EPAGES if
+ * a paged-cache call met a length, page or slot that does not fit, TP3D_ECUDA
+ * if the stream reported an error, else TP3D_OK.                            */
 tp3d_status tp3d_sync_status(tp3d_ctx* ctx, void* stream);
 
 /* Failure detection (no counterpart on the pages; the bounded waits are this

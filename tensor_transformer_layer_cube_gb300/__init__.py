@@ -7,7 +7,9 @@ in one GB300's memory, plus bit-exact resharding between row, column, 2-D
 block, cube and replicated layouts ("On Optimizing the Communication of Model
 Parallelism", §2), in hand-written sm_103a kernels; and (``include/tp3d_plan.h``)
 the host-side planners: the cross-mesh resharding planner of that page's
-§3.2 and a pipeline-bubble simulator.
+§3.2 and a pipeline-bubble simulator; and (``include/tp3d_paged.h``) the paged
+key/value cache that serves the layer: block tables and slot maps from request
+lengths, the cache write, and attention of new tokens over the cache.
 
 This module only marshals arguments: every function has the name of the C
 entry point it calls and returns its status code (0 = TP3D_OK).  Tensor
@@ -37,11 +39,13 @@ __all__ = [
     "tp3d_pipeline_simulate", "tp3d_mlp_layout", "TP3D_SCHEME_1D", "TP3D_SCHEME_2D", "TP3D_SCHEME_3D", "TP3D_SPEC_R", "TP3D_SPEC_S0", "TP3D_SPEC_S1", "TP3D_SPEC_S01", "TP3D_CMR_NAIVE",
     "TP3D_CMR_LOAD_BALANCE", "TP3D_CMR_DFS", "TP3D_CMR_RANDOM_GREEDY", "TP3D_PIPE_GPIPE", "TP3D_PIPE_1F1B",
     "TP3D_PIPE_INTERLEAVED",
+    "tp3d_kv_cache", "tp3d_paged_batch", "tp3d_row_strides", "kv_cache", "paged_batch", "tp3d_paged_plan",
+    "tp3d_paged_store", "tp3d_paged_attn", "tp3d_paged_attn_workspace_bytes",
 ]
 
 STATUS = {0: "TP3D_OK", 1: "TP3D_EINVAL", 2: "TP3D_ESHAPE", 3: "TP3D_EALIGN", 4: "TP3D_EDTYPE",
           5: "TP3D_ECUDA", 6: "TP3D_ETIMEOUT", 7: "TP3D_EUNSUPPORTED", 8: "TP3D_EOVERLAP",
-          9: "TP3D_ERANGE"}
+          9: "TP3D_ERANGE", 10: "TP3D_EPAGES"}
 TP3D_F32, TP3D_BF16 = 0, 1
 CUBE_A, CUBE_B, CUBE_C, CUBE_B_SWAP, ROW, COL, BLOCK2D, REPLICATED = range(8)
 TP3D_SPEC_R, TP3D_SPEC_S0, TP3D_SPEC_S1, TP3D_SPEC_S01 = range(4)
@@ -69,6 +73,23 @@ class tp3d_layer_params(ctypes.Structure):
 
 class tp3d_layer_grads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in PARAM_NAMES]
+
+
+class tp3d_kv_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p)]
+
+
+class tp3d_paged_batch(ctypes.Structure):
+    _fields_ = [("requests", ctypes.c_int32), ("max_new", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("table_width", ctypes.c_int64)]
+
+
+class tp3d_row_strides(ctypes.Structure):
+    _fields_ = [("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class tp3d_rect(ctypes.Structure):
@@ -156,6 +177,18 @@ _SIGS = {
                                       ctypes.POINTER(tp3d_layer_params), ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(tp3d_layer_grads),
                                       ctypes.c_void_p]),
+    "tp3d_paged_plan": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int64] +
+                        [ctypes.c_void_p] * 3 + [ctypes.c_int64] + [ctypes.c_void_p] * 2 + [ctypes.c_int64] +
+                        [ctypes.c_void_p] * 6),
+    "tp3d_paged_store": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_kv_cache), ctypes.c_int64,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                        ctypes.c_void_p, ctypes.c_void_p]),
+    "tp3d_paged_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_kv_cache),
+                                       ctypes.POINTER(tp3d_paged_batch), ctypes.c_int, ctypes.c_float,
+                                       ctypes.c_void_p, tp3d_row_strides, ctypes.c_void_p, tp3d_row_strides,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "tp3d_paged_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.POINTER(tp3d_kv_cache),
+                                                          ctypes.c_int]),
     "tp3d_layout_rects": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, tp3d_layout, ctypes.POINTER(tp3d_rect),
                                          ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)]),
     "tp3d_mesh_rects": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, tp3d_mesh_spec, ctypes.POINTER(tp3d_rect),
@@ -289,6 +322,82 @@ def tp3d_layer_bwd(ctx, cfg: tp3d_layer_cfg, params: dict, X, workspace, dY, dX,
     g = _params(tp3d_layer_grads, grads)
     return lib().tp3d_layer_bwd(ctx, ctypes.byref(cfg), ctypes.byref(p), _p(X), _p(workspace), _p(dY), _p(dX),
                                 ctypes.byref(g), _s(stream))
+
+
+# ---------------------------------------------------------------------------
+# Paged key/value cache (include/tp3d_paged.h).  Strided arguments are torch
+# tensors here: their shapes and strides are what the C call takes.
+# ---------------------------------------------------------------------------
+
+def _dtype_of(x):
+    import torch
+    return {torch.float32: TP3D_F32, torch.bfloat16: TP3D_BF16}.get(x.dtype, -1)
+
+
+def _rows(x, what):
+    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
+        raise ValueError(f"{what}: a (token, head, column) tensor with contiguous columns")
+    return tp3d_row_strides(x.stride(0), x.stride(1))
+
+
+def kv_cache(k, v) -> tp3d_kv_cache:
+    """The descriptor of two pools seen as (page, token, head, column) with
+    contiguous columns (any page, token and head strides, the same for both).
+    It holds their addresses: keep the tensors."""
+    if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype or \
+            (k.stride(3) != 1 and k.shape[3] > 1):
+        raise ValueError("kv_cache: two (page, token, head, column) pools of one shape, type and strides")
+    return tp3d_kv_cache(_dtype_of(k), k.shape[2], k.shape[3], k.shape[1], k.shape[0], k.stride(0), k.stride(1),
+                         k.stride(2), k.data_ptr(), v.data_ptr())
+
+
+def paged_batch(q_start, kv_len, block_table, tokens: int, max_new: int = 0) -> tp3d_paged_batch:
+    """The descriptor of one step's requests (int32 device tensors; the table
+    as dense rows).  It holds their addresses: keep the tensors."""
+    import torch
+    for x in (q_start, kv_len, block_table):
+        if x.dtype != torch.int32 or not x.is_contiguous():
+            raise ValueError("paged_batch: contiguous int32 tensors")
+    if block_table.dim() != 2 or block_table.shape[0] != kv_len.numel() or q_start.numel() != kv_len.numel() + 1:
+        raise ValueError("paged_batch: q_start (requests + 1), kv_len (requests), block_table (requests, width)")
+    return tp3d_paged_batch(kv_len.numel(), max_new, tokens, q_start.data_ptr(), kv_len.data_ptr(),
+                            block_table.data_ptr(), block_table.shape[1])
+
+
+def tp3d_paged_plan(ctx, page, requests, tokens, cached, fresh, free_pages, free_cap, free_count, block_table,
+                    table_width, q_start, kv_len, slots, positions, free_left, stream=None) -> int:
+    return lib().tp3d_paged_plan(ctx, page, requests, tokens, _p(cached), _p(fresh), _p(free_pages), free_cap,
+                                 _p(free_count), _p(block_table), table_width, _p(q_start), _p(kv_len), _p(slots),
+                                 _p(positions), _p(free_left), _s(stream))
+
+
+def tp3d_paged_store(ctx, cache: tp3d_kv_cache, K, V, slots, stream=None) -> int:
+    """K, V: (token, head, column) tensors of the same strides."""
+    st = _rows(K, "tp3d_paged_store")
+    if V.shape != K.shape or V.stride() != K.stride() or tuple(K.shape[1:]) != (cache.kv_heads, cache.head_dim):
+        raise ValueError("tp3d_paged_store: K and V (tokens, kv_heads, head_dim) of the same strides")
+    if _dtype_of(K) != cache.dtype or _dtype_of(V) != cache.dtype or slots.numel() < K.shape[0] or \
+            slots.element_size() != 8 or not slots.is_contiguous():
+        raise ValueError("tp3d_paged_store: K and V of the cache's type, an int64 slot for each token")
+    return lib().tp3d_paged_store(ctx, ctypes.byref(cache), K.shape[0], _p(K), _p(V), st.token_stride,
+                                  st.head_stride, _p(slots), _s(stream))
+
+
+def tp3d_paged_attn(ctx, cache: tp3d_kv_cache, batch: tp3d_paged_batch, Q, O, lse, scale, workspace,
+                    stream=None) -> int:
+    """Q, O: (token, head, column) tensors; lse: dense (token, head) float32 or None."""
+    qs, os_ = _rows(Q, "tp3d_paged_attn"), _rows(O, "tp3d_paged_attn")
+    if lse is not None and (not lse.is_contiguous() or tuple(lse.shape) != tuple(Q.shape[:2]) or lse.element_size() != 4):
+        raise ValueError("tp3d_paged_attn: lse dense (tokens, heads) float32")
+    if O.shape != Q.shape or Q.shape[0] < batch.tokens or Q.shape[2] != cache.head_dim or \
+            _dtype_of(Q) != cache.dtype or _dtype_of(O) != cache.dtype:
+        raise ValueError("tp3d_paged_attn: Q and O (tokens, heads, head_dim) of the cache's type")
+    return lib().tp3d_paged_attn(ctx, ctypes.byref(cache), ctypes.byref(batch), Q.shape[1], scale, _p(Q), qs, _p(O),
+                                 os_, _p(lse), _p(workspace), _s(stream))
+
+
+def tp3d_paged_attn_workspace_bytes(ctx, cache: tp3d_kv_cache, heads: int) -> int:
+    return lib().tp3d_paged_attn_workspace_bytes(ctx, ctypes.byref(cache), heads)
 
 
 # ---------------------------------------------------------------------------

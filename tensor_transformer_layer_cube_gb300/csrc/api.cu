@@ -177,6 +177,7 @@ const char* tp3d_status_string(tp3d_status s) {
     case TP3D_EUNSUPPORTED: return "unsupported configuration";
     case TP3D_EOVERLAP: return "output overlaps an input";
     case TP3D_ERANGE: return "a value on the fp16 score path beyond fp16's range";
+    case TP3D_EPAGES: return "a length, page or slot of the paged cache that does not fit";
   }
   return "unknown status";
 }

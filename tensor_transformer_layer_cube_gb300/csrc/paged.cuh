@@ -1,0 +1,53 @@
+// paged.cuh - the paged key/value cache: what its kernels share.
+#pragma once
+
+#include "common.cuh"
+#include "tp3d_paged.h"
+
+namespace tp3d {
+
+// One call of tp3d_paged_attn, as its kernels take it (element strides).
+struct PagedAttn {
+  tp3d_kv_cache c;
+  int32_t page_log2;
+  int32_t requests, group;  // group: query heads per key/value head
+  int64_t tokens;
+  const int32_t *q_start, *kv_len, *table;
+  int64_t width;  // block table columns
+  float scale;
+  const __nv_bfloat16* q;
+  int64_t q_token, q_head;
+  __nv_bfloat16* o;
+  int64_t o_token, o_head;
+  float* lse;  // or null
+  int* err;
+};
+
+tp3d_status launch_paged_attn(tp3d_ctx* ctx, const PagedAttn& A, int max_new, void* workspace, cudaStream_t s);
+size_t paged_attn_workspace(const tp3d_ctx* ctx, int head_dim);
+
+#if defined(__CUDACC__)
+
+// A request as the attention kernels see it: rows [q0, q0 + n) of Q, kv keys.
+// Lengths that do not fit are clamped, so that whatever the buffers hold, no
+// access leaves them; a request that was clamped raises TP3D_EPAGES.
+struct PagedRequest {
+  int64_t q0;
+  int32_t n, kv;
+};
+__device__ __forceinline__ PagedRequest paged_request(const PagedAttn& A, int b) {
+  const int32_t s0 = __ldg(A.q_start + b), s1 = __ldg(A.q_start + b + 1), len = __ldg(A.kv_len + b);
+  const int64_t cap = A.width << A.page_log2;
+  PagedRequest r;
+  const int64_t q0 = s0 < 0 ? 0 : s0 > A.tokens ? A.tokens : s0;
+  const int64_t q1 = s1 < q0 ? q0 : s1 > A.tokens ? A.tokens : s1;
+  r.q0 = q0;
+  r.n = (int32_t)(q1 - q0);
+  r.kv = (int32_t)(len < 0 ? 0 : len > cap ? cap : len);
+  if (q0 != s0 || q1 != s1 || r.kv != len) raise_error(A.err, TP3D_EPAGES);
+  return r;
+}
+
+#endif
+
+}  // namespace tp3d
