@@ -21,7 +21,8 @@
  *
  * Ownership.  The caller allocates every tensor and workspace (PyTorch in the
  * bundled binding).  The library allocates only its context: one device
- * error word, two side streams with three events, and host-side caches.  All
+ * error word, 16 KiB of device counters, two side streams with three events,
+ * and host-side caches.  All
  * compute calls are asynchronous on the given CUDA stream (a cudaStream_t
  * passed as void*; NULL = the legacy default stream).  A call that runs
  * independent launches on the context's side streams (tp3d_layer_fwd,

@@ -126,8 +126,11 @@ tp3d_status tp3d_create(int device, tp3d_ctx** out) {
   memcpy(init + 2, &lim, sizeof(lim));
   if (cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
       cudaMalloc(&c->d_err, sizeof(init)) != cudaSuccess ||
-      cudaMemcpy(c->d_err, init, sizeof(init), cudaMemcpyHostToDevice) != cudaSuccess) {
+      cudaMemcpy(c->d_err, init, sizeof(init), cudaMemcpyHostToDevice) != cudaSuccess ||
+      cudaMalloc(&c->d_paged, kPagedCounters * sizeof(unsigned)) != cudaSuccess ||
+      cudaMemset(c->d_paged, 0, kPagedCounters * sizeof(unsigned)) != cudaSuccess) {
     if (c->d_err) cudaFree(c->d_err);
+    if (c->d_paged) cudaFree(c->d_paged);
     free(c);
     return TP3D_ECUDA;
   }
@@ -151,6 +154,7 @@ tp3d_status tp3d_create(int device, tp3d_ctx** out) {
 void tp3d_destroy(tp3d_ctx* ctx) {
   if (!ctx) return;
   if (ctx->d_err) cudaFree(ctx->d_err);
+  if (ctx->d_paged) cudaFree(ctx->d_paged);
   for (int k = 0; k < 2; ++k) {
     if (ctx->side[k]) cudaStreamDestroy(ctx->side[k]);
     if (ctx->ev_join[k]) cudaEventDestroy(ctx->ev_join[k]);

@@ -29,6 +29,8 @@ struct tp3d_ctx {
   // between calls
   void* scratch;
   size_t scratch_bytes;
+  // arrival counters of the paged attention's split items (zero between calls)
+  unsigned* d_paged;
   // CUDA graphs of whole layer calls keyed by their arguments (graph.cu), the
   // stream they run on, and the events that order it with the caller's stream
   void* graphs;
@@ -47,6 +49,7 @@ void graph_cache_free(tp3d_ctx* ctx);
 // the context sets another limit (tp3d_set_wait_limit_ns); the drains of an
 // aborting CTA always allow this long.
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;
+constexpr int kPagedCounters = 4096;
 constexpr int kErrWords = 4;  // ints of the device error area (error code, pad, 64-bit limit)
 
 #define TP3D_CUDA_TRY(expr)                       \
