@@ -5,81 +5,15 @@
 //   s_k = scale q . k_k,  m = max s_k,  l = sum exp(s_k - m),
 //   O = sum exp(s_k - m) v_k / l,  lse = m + log l,
 // in one pass over the keys with a running m, l and O.
+#include <cudaTypedefs.h>
 #include <math.h>
 
+#include "attn_tile.cuh"
 #include "paged.cuh"
 
 namespace tp3d {
 
 namespace {
-
-using bf16 = __nv_bfloat16;
-
-constexpr int kRowWarps = 4;
-
-// One CTA per (row, query head); its warps take every kRowWarps-th key, each
-// with its own running maximum and sums, joined at the end.  Lane l holds
-// columns l * D/32 .. of the row.
-template <int D>
-__global__ void __launch_bounds__(kRowWarps * 32) paged_attn_row_kernel(const PagedAttn A) {
-  constexpr int E = D / 32;
-  __shared__ float so[kRowWarps][D], sm[kRowWarps], sl[kRowWarps];
-  __shared__ int s_req;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = blockIdx.y, h = i / A.group;
-  const int64_t t = blockIdx.x;
-  if (threadIdx.x == 0) s_req = -1;
-  __syncthreads();
-  for (int b = threadIdx.x; b < A.requests; b += kRowWarps * 32) {
-    const PagedRequest r = paged_request(A, b);
-    if (t >= r.q0 && t < r.q0 + r.n) s_req = b;
-  }
-  __syncthreads();
-  const int b = s_req;
-  if (b < 0) return;
-  const PagedRequest r = paged_request(A, b);
-  if (r.n * A.group <= 64) return;
-  const int64_t last = (int64_t)r.kv - r.n + (t - r.q0);
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(A.q[t * A.q_token + i * A.q_head + lane * E + e]) * A.scale;
-    o[e] = 0.0f;
-  }
-  for (int64_t k = warp; k <= last; k += kRowWarps) {
-    const int32_t page = __ldg(A.table + (int64_t)b * A.width + (k >> A.page_log2));
-    const bool in = page >= 0 && page < A.c.pages;
-    if (!in) raise_error(A.err, TP3D_EPAGES);
-    const int64_t at = (int64_t)page * A.c.page_stride + (k & (A.c.page - 1)) * A.c.token_stride +
-                       h * A.c.head_stride + lane * E;
-    const bf16* kp = static_cast<const bf16*>(A.c.k) + at;
-    const bf16* vp = static_cast<const bf16*>(A.c.v) + at;
-    float s = 0.0f;
-    for (int e = 0; e < E; ++e) s += in ? q[e] * __bfloat162float(kp[e]) : 0.0f;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.0f : mn;
-    const float f = expf(m - base), p = expf(s - base);
-    l = l * f + p;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + (in ? p * __bfloat162float(vp[e]) : 0.0f);
-    m = mn;
-  }
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  float mm = -INFINITY, ll = 0.0f;
-  for (int w = 0; w < kRowWarps; ++w) mm = fmaxf(mm, sm[w]);
-  const float base = mm == -INFINITY ? 0.0f : mm;
-  for (int w = 0; w < kRowWarps; ++w) ll += sl[w] * expf(sm[w] - base);
-  for (int c = threadIdx.x; c < D; c += kRowWarps * 32) {
-    float x = 0.0f;
-    for (int w = 0; w < kRowWarps; ++w) x += so[w][c] * expf(sm[w] - base);
-    A.o[t * A.o_token + i * A.o_head + c] = __float2bfloat16(ll == 0.0f ? 0.0f : x / ll);
-  }
-  if (threadIdx.x == 0 && A.lse) A.lse[t * (int64_t)gridDim.y + i] = ll == 0.0f ? -INFINITY : base + logf(ll);
-}
 
 // ------------------------------------------------------------------ few rows
 // Requests with at most kFewRows rows (new tokens x query heads) per key/value
@@ -113,8 +47,6 @@ constexpr int kFewStages = 3;
 constexpr int kFewPerSm = 2;
 constexpr uint32_t kFewStageBytes = 32768;  // a tile's keys, then its values
 constexpr float kMoveLog2 = 8.0f;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 TP3D_HD constexpr int few_tile_keys() { return (int)kFewStageBytes / (4 * D); }
@@ -599,14 +531,698 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
   cp_wait<0>();
 }
 
-}  // namespace
+// ------------------------------------------------------------------ many rows
+// Requests with more than kFewRows rows per key/value head: prompts and their
+// chunks.  4 D FLOP per (row, key) pair against 4 D bytes per key: tensor
+// work bounds it.  One CTA per SM takes pairs of 128-row query tiles (rows are
+// new token x query head of the group, so grouped heads fill a tile with few
+// tokens and share its keys) and streams 128-key tiles by TMA, one box per
+// page and 64 columns.  As in the layer's forward: S = Q K^T in tensor memory,
+// an online softmax per row (one thread each), P written back over S, and
+// O += P V with P read from tensor memory.  Differences:
+//  * P is kept as two bf16 terms (P = hi + lo up to 2^-17 P): over its 32
+//    score columns a chunk leaves 16 columns of hi pairs and 16 of lo pairs,
+//    and O += hi V + lo V.  One bf16 term alone has an error as large as the
+//    output's own rounding.
+//  * The tile sequence (request, head, pair, key tile) is cut into equal
+//    contiguous ranges as in the kernel above, so lengths need no plan on the
+//    host and every SM gets the same number of tiles.
+//  * Key tiles that some row of the pair does not see whole are masked by
+//    comparison with each row's last key.  Their values are looked at by two
+//    otherwise idle warps before P V: rows past the request become zero, and a
+//    value that is not finite becomes zero and is noted with its key and
+//    column, since a probability of 0 would not silence it.
+//
+// warps: 0 TMA producer, 1 MMA issuer + TMEM owner, 2-3 value check
+// (warpgroup 0); 4-7 slot 0 rows; 8-11 slot 1 rows.
+// smem: Q0 | Q1 | R0 .. R4 (a ring of K_j V_j ...), 32 KiB each | barriers | notes
+// TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [256+D,256+2D)
+constexpr int kManyThreads = 384;
+constexpr int kManyRegsLow = 120, kManyRegsHigh = 192;  // 128 x 120 + 256 x 192 <= 384 x 168; no spills
+constexpr uint32_t kManyRing = 5;
+constexpr int kNotes = 4;  // items whose values may be under check or in use at once
+struct ManyShared {
+  unsigned notes[kNotes][64];    // per column (16 bits): first non-finite masked key - first row's last key
+  int noted[kNotes][2];          // by value-check warp
+  int last;
+  long long scan[kManyThreads / 32];
+  long long before;
+  int b0;
+};
+constexpr int kManySmem = 7 * (int)kTile + 512 + (int)sizeof(ManyShared) + 1024;
+static_assert(kManySmem <= 232448, "shared memory of one CTA");
+TP3D_HD constexpr size_t many_part_floats(int d) { return (size_t)2 * TR * (d + 2); }
 
-size_t paged_attn_workspace(const tp3d_ctx* ctx, int d) {
-  return (size_t)ctx->num_sms * kFewPerSm * 2 * few_part_floats(d) * sizeof(float);
+// sum of floor((a i + b) / m) for i < n, all non-negative (the Euclidean recursion)
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t s = 0;
+  while (n > 0) {
+    s += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+    a %= m;
+    b %= m;
+    const int64_t top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const int64_t t = a;
+    a = m;
+    m = t;
+  }
+  return s;
+}
+
+// The pairs of query tiles of a request: pair k holds tokens [2 k tt, +2 tt).
+struct ManyRequest {
+  int64_t q0;
+  int n, kv, tt;  // tt: tokens of a query tile
+  __device__ int pairs() const { return (n + 2 * tt - 1) / (2 * tt); }
+  // key tiles that tokens below `end` see (one at least: rows without keys are written too)
+  __device__ int tiles_upto(int64_t end) const {
+    const int64_t keys = (int64_t)kv - n + (end < n ? end : n);
+    return keys > 0 ? (int)((keys + TR - 1) / TR) : 1;
+  }
+  __device__ int tiles(int k) const { return tiles_upto((int64_t)(k + 1) * 2 * tt); }
+  // key tiles of the pairs before pair k (the last pair's are not among them)
+  __device__ int64_t before(int64_t k) const {
+    const int64_t w = 2 * tt, ctx = (int64_t)kv - n;
+    int64_t z = ctx < 0 ? -ctx / w : 0;  // pairs whose tokens all see nothing
+    if (z > k) z = k;
+    return z + floor_sum(k - z, TR, w, ctx + (z + 1) * w + TR - 1);
+  }
+  __device__ int64_t total() const {
+    const int p = pairs();
+    return before(p - 1) + tiles(p - 1);
+  }
+};
+
+__device__ __forceinline__ ManyRequest many_request(const PagedAttn& A, int b) {
+  const PagedRequest r = paged_request(A, b);
+  ManyRequest m;
+  m.q0 = r.q0;
+  m.n = (int64_t)r.n * A.group > kFewRows ? r.n : 0;  // the others are the kernel above's
+  m.kv = r.kv;
+  m.tt = TR / A.group;
+  return m;
+}
+
+// One piece of a CTA's range: key tiles [j0, j1) of pair k of (request b, head h).
+struct ManyCursor {
+  ManyRequest r;
+  int b, h, k, pairs;
+  int j0, j1, nkv;  // nkv: the pair's key tiles
+  int64_t u, u1;    // the piece's first unit, the range's end
+  __device__ void set(const PagedAttn&) {
+    nkv = r.tiles(k);
+    const int64_t left = u1 - u;
+    j1 = nkv - j0 <= left ? nkv : j0 + (int)left;
+  }
+  __device__ bool next(const PagedAttn& A) {
+    u += j1 - j0;
+    if (u >= u1) return false;
+    j0 = 0;
+    if (++k == pairs) {
+      k = 0;
+      if (++h == A.c.kv_heads) {
+        h = 0;
+        do r = many_request(A, ++b);
+        while (r.n == 0);
+        pairs = r.pairs();
+      }
+    }
+    set(A);
+    return true;
+  }
+  __device__ int64_t tok(int sl) const { return ((int64_t)2 * k + sl) * r.tt; }  // a slot's first token
+  __device__ bool two() const { return tok(1) < r.n; }
+  // key tiles of slot sl in this piece
+  __device__ int count(int sl) const {
+    if (sl) return two() ? j1 - j0 : 0;
+    const int n0 = r.tiles_upto(tok(1));
+    return n0 < j1 ? (n0 > j0 ? n0 - j0 : 0) : j1 - j0;
+  }
+  // key tile j holds keys that the pair's first row does not see
+  __device__ bool partial(int j) const { return ((int64_t)j + 1) * TR - 1 > (int64_t)r.kv - r.n + tok(0); }
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// 16-bit minimum in a word of two (a rare path: emulated on the word)
+__device__ __forceinline__ void note_min(unsigned* word, int half, unsigned v) {
+  unsigned old = *reinterpret_cast<volatile unsigned*>(word);
+  while (((old >> (16 * half)) & 0xffffu) > v) {
+    const unsigned want = half ? (old & 0x0000ffffu) | (v << 16) : (old & 0xffff0000u) | v;
+    const unsigned seen = atomicCAS(word, old, want);
+    if (seen == old) break;
+    old = seen;
+  }
 }
 
 template <int D>
-static tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool alone, void* workspace, cudaStream_t s) {
+__global__ void __launch_bounds__(kManyThreads, 1)
+    paged_attn_many_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                           const __grid_constant__ CUtensorMap mv, const PagedAttn A, float* __restrict__ parts,
+                           unsigned* __restrict__ counters) {
+  constexpr int NCH = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  const Ctx c = setup_smem(smem_raw);
+  ManyShared& sh = *reinterpret_cast<ManyShared*>(c.base_ptr + 7 * kTile + 512);
+  auto sQ = [&](int sl) { return c.base + (uint32_t)sl * kTile; };
+  auto sR = [&](uint32_t i) { return c.base + (2u + i) * kTile; };
+  auto bar = [&](int k) { return c.bar0 + 8u * k; };
+  const uint32_t q_full = bar(0), q_empty = bar(1), final_bar = bar(22), part_full = bar(28), part_last = bar(29);
+  auto r_full = [&](uint32_t i) { return bar(2 + (int)i); };
+  auto r_empty = [&](uint32_t i) { return bar(2 + (int)kManyRing + (int)i); };
+  auto s_full = [&](int sl) { return bar(12 + sl); };
+  auto p_full = [&](int sl) { return bar(14 + sl); };
+  auto p_empty = [&](int sl) { return bar(16 + sl); };
+  auto o_full = [&](int sl) { return bar(18 + sl); };
+  auto o_empty = [&](int sl) { return bar(20 + sl); };
+  auto v_checked = [&](uint32_t i) { return bar(23 + (int)i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- this CTA's range of the tile sequence (as in the kernel above)
+  int64_t units = 0;
+  ManyCursor cur;
+  {
+    long long carry = 0;
+    auto chunk = [&](int base, long long& mine, long long& tiles) {
+      const int b = base + (int)threadIdx.x;
+      tiles = 0;
+      if (b < A.requests) {
+        const ManyRequest r = many_request(A, b);
+        if (r.n > 0) tiles = r.total();
+      }
+      long long x = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) sh.scan[warp] = x;
+      __syncthreads();
+      mine = carry + x - tiles;
+      for (int w = 0; w < kManyThreads / 32; ++w) {
+        if (w < warp) mine += sh.scan[w];
+        carry += sh.scan[w];
+      }
+    };
+    long long mine = 0, tiles = 0;
+    for (int base = 0; base < A.requests; base += kManyThreads) chunk(base, mine, tiles);
+    units = carry * A.c.kv_heads;
+    const Ranges R(units, gridDim.x);
+    cur.u = R.begin(blockIdx.x);
+    cur.u1 = R.begin(blockIdx.x + 1);
+    if (cur.u >= cur.u1) return;
+    const bool one = A.requests <= kManyThreads;
+    carry = 0;
+    for (int base = 0; base < A.requests; base += kManyThreads) {
+      if (!one) chunk(base, mine, tiles);
+      const long long at = mine * A.c.kv_heads;
+      if (tiles > 0 && at <= cur.u && cur.u < at + tiles * A.c.kv_heads) {
+        sh.b0 = base + (int)threadIdx.x;
+        sh.before = at;
+      }
+      if (one || carry * A.c.kv_heads > cur.u) break;
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 30; ++k) {
+      // p_full, o_empty: one arrival per row warp of the slot; r_empty: the
+      // issuer and the two value-check warps (which follow every slot, so that
+      // no phase passes them by); v_checked: those two; part_full: all row warps
+      const bool four = k == 14 || k == 15 || k == 20 || k == 21, ring_empty = k >= 7 && k < 12;
+      mbar_init(bar(k), four ? 4 : ring_empty ? 3 : k >= 23 && k < 28 ? 2 : k == 28 ? 8 : 1);
+    }
+    *c.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&mq);
+    tma_prefetch_map(&mk);
+    tma_prefetch_map(&mv);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(c.tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *c.tmem_holder;
+  cur.b = sh.b0;
+  cur.r = many_request(A, cur.b);
+  cur.pairs = cur.r.pairs();
+  {
+    int64_t off = cur.u - sh.before;
+    const int64_t per_head = cur.r.total();
+    cur.h = (int)(off / per_head);
+    off -= cur.h * per_head;
+    int lo = 0, hi = cur.pairs;  // the last pair that begins at or before `off`
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cur.r.before(mid) <= off) lo = mid;
+      else hi = mid;
+    }
+    cur.k = lo;
+    cur.j0 = (int)(off - cur.r.before(lo));
+    cur.set(A);
+  }
+
+  if (warp < 4) {
+    // ---------------------------------------------------------- warpgroup 0
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyRegsLow));
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      // lane -> (page of the tile, 64-column chunk): one box each
+      const int bl2 = A.page_log2 < 7 ? A.page_log2 : 7;  // a box's keys
+      const int boxes = TR >> bl2;
+      const int pi = lane & (boxes - 1), ch = lane / boxes;
+      const bool mine = ch < NCH;
+      const uint32_t box_dst = (uint32_t)ch * kChunk + ((uint32_t)pi << bl2) * 128u;
+      const uint32_t kv_bytes = (uint32_t)TR * D * 2, q_bytes = (uint32_t)(cur.r.tt * A.group) * D * 2;
+      uint32_t n = 0, ic = 0;
+      bool ok = true;
+      do {
+        const bool two = cur.two();
+        if (!(ok = warp_wait(q_empty, (ic & 1) ^ 1, c, A.err, lane))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, q_bytes * (two ? 2u : 1u));
+          for (int sl = 0; sl < (two ? 2 : 1); ++sl)
+            for (int x = 0; x < NCH; ++x)
+              tma_load_3d(sQ(sl) + (uint32_t)x * kChunk, &mq, q_full, 64 * x, cur.h * A.group,
+                          (int)(cur.r.q0 + cur.tok(sl)));
+        }
+        ++ic;
+        for (int j = cur.j0; j < cur.j1 && ok; ++j) {
+          // a box outside the request or the pool starts past the last page: TMA fills it with zeros
+          const int64_t key = (int64_t)j * TR + ((int64_t)pi << bl2);
+          int32_t page = (int32_t)A.c.pages;
+          if (mine && key < cur.r.kv) {
+            page = __ldg(A.table + (int64_t)cur.b * A.width + (key >> A.page_log2));
+            if (page < 0 || page >= A.c.pages) {
+              raise_error(A.err, TP3D_EPAGES);
+              page = (int32_t)A.c.pages;
+            }
+          }
+          const int in_page = (int)(key & (A.c.page - 1));
+          for (int kvi = 0; kvi < 2; ++kvi, ++n) {
+            const uint32_t slot = n % kManyRing;
+            if (!(ok = warp_wait(r_empty(slot), ((n / kManyRing) & 1) ^ 1, c, A.err, lane))) break;
+            if (lane == 0) mbar_arrive_expect_tx(r_full(slot), kv_bytes);
+            __syncwarp();
+            if (mine) tma_load_4d(sR(slot) + box_dst, kvi ? &mv : &mk, r_full(slot), 64 * ch, in_page, cur.h, page);
+          }
+        }
+      } while (ok && cur.next(A));
+      if (!ok && lane == 0) {  // let what was issued land before the CTA's shared memory goes
+        if (ic) drain(q_full, (ic - 1) & 1);
+        for (uint32_t i = n > kManyRing ? n - kManyRing : 0; i < n; ++i)
+          drain(r_full(i % kManyRing), (i / kManyRing) & 1);
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint32_t id_s = idesc_bf16_f32(TR, TR, 0, 0);  // S = Q K^T
+      const uint32_t id_o = idesc_bf16_f32(TR, D, 0, 1);   // O += P V (P from TMEM, V MN-major)
+      uint32_t n = 0, ic = 0, vc = 0;  // vc: the next v_checked phase's parity, a bit per slot
+      uint32_t pc[2] = {0, 0}, oc[2] = {0, 0};  // P V products issued, pieces finished, per slot
+      bool ok = true;
+      auto ring = [&](uint32_t idx, uint32_t& slot) -> bool {
+        slot = idx % kManyRing;
+        return mbar_wait(r_full(slot), (idx / kManyRing) & 1, c.abort_flag, A.err);
+      };
+      auto issue_s = [&](int sl, uint32_t kslot) -> bool {
+        if (pc[sl] > 0 && !mbar_wait(p_empty(sl), (pc[sl] - 1) & 1, c.abort_flag, A.err)) return false;
+        tc_fence_after();
+        mma_tile(tmem + (uint32_t)(sl * TR), sQ(sl), false, sR(kslot), false, D / 16, id_s, false);
+        umma_commit(s_full(sl));
+        return true;
+      };
+      auto issue_pv = [&](int sl, uint32_t vslot, bool first) -> bool {
+        if (!mbar_wait(p_full(sl), pc[sl] & 1, c.abort_flag, A.err)) return false;
+        if (first && !mbar_wait(o_empty(sl), (oc[sl] & 1) ^ 1, c.abort_flag, A.err)) return false;
+        tc_fence_after();
+        const uint32_t pt = tmem + (uint32_t)(sl * TR), ot = tmem + 256u + (uint32_t)(sl * D);
+        for (int k = 0; k < TR / 16; ++k) {
+          const uint64_t vd = desc_mnmajor(sR(vslot), k);
+          const uint32_t hi = pt + 32u * (uint32_t)(k >> 1) + 8u * (uint32_t)(k & 1);
+          umma_ts(ot, hi, vd, id_o, (!first || k > 0) ? 1u : 0u);
+          umma_ts(ot, hi + 16u, vd, id_o, 1u);
+        }
+        umma_commit(p_empty(sl));
+        ++pc[sl];
+        return true;
+      };
+      do {
+        const int cnt[2] = {cur.count(0), cur.count(1)};
+        const int nmax = cur.j1 - cur.j0;
+        if (!(ok = mbar_wait(q_full, ic & 1, c.abort_flag, A.err))) break;
+        ++ic;
+        const uint32_t n0 = n;  // ring index of K_j0; K_(j0+i) = n0 + 2i, V_(j0+i) = n0 + 2i + 1
+        uint32_t ks = 0;
+        if (!(ok = ring(n0, ks) && (cnt[0] == 0 || issue_s(0, ks)) && (cnt[1] == 0 || issue_s(1, ks)))) break;
+        if (nmax == 1) umma_commit(q_empty);
+        umma_commit(r_empty(ks));
+        for (int i = 0; i < nmax && ok; ++i) {
+          uint32_t vs = 0, kn = 0;
+          const bool more = i + 1 < nmax;
+          if (!(ok = ring(n0 + 2 * i + 1, vs))) break;
+          if (cur.partial(cur.j0 + i)) {
+            if (!(ok = mbar_wait(v_checked(vs), (vc >> vs) & 1, c.abort_flag, A.err))) break;
+            vc ^= 1u << vs;
+          }
+          if (more && !(ok = ring(n0 + 2 * i + 2, kn))) break;
+          for (int sl = 0; sl < 2 && ok; ++sl)
+            if (i < cnt[sl]) ok = issue_pv(sl, vs, i == 0) && (i + 1 >= cnt[sl] || issue_s(sl, kn));
+          if (!ok) break;
+          umma_commit(r_empty(vs));
+          if (more) {
+            if (i + 2 == nmax) umma_commit(q_empty);  // the piece's last product with Q issued
+            umma_commit(r_empty(kn));
+          }
+        }
+        if (!ok) break;
+        for (int sl = 0; sl < 2; ++sl)
+          if (cnt[sl] > 0) {
+            umma_commit(o_full(sl));
+            ++oc[sl];
+          }
+        n = n0 + 2 * (uint32_t)nmax;
+      } while (cur.next(A));
+      umma_commit(final_bar);
+      drain(final_bar, 0);
+    } else if (warp >= 2) {
+      // ------------------------------------------------------------ value check
+      // warp w looks at half of the columns of each partly seen value tile:
+      // 16-byte vectors [w * NV, +NV) of the row's D / 8
+      constexpr int NV = D / 16;
+      const int w = warp - 2;
+      uint32_t n = 0, ic = 0;
+      bool ok = true;
+      do {
+        const int64_t seen = (int64_t)cur.r.kv - cur.r.n + cur.tok(0);  // the first row's last key
+        unsigned* const notes = sh.notes[ic % kNotes] + w * (NV * 4);
+        bool noting = false;
+        for (uint32_t i2 = 0; i2 < 2 * (uint32_t)(cur.j1 - cur.j0); ++i2, ++n) {
+          const int j = cur.j0 + (int)(i2 >> 1);
+          const uint32_t slot = n % kManyRing;
+          if (!(ok = warp_wait(r_full(slot), (n / kManyRing) & 1, c, A.err, lane))) break;
+          if (!(i2 & 1) || !cur.partial(j)) {
+            warp_arrive(r_empty(slot), lane);
+            continue;
+          }
+          if (!noting) {
+            noting = true;
+            for (int i = lane; i < NV * 4; i += 32) notes[i] = 0xffffffffu;
+            if (lane == 0) sh.noted[ic % kNotes][w] = 0;
+            __syncwarp();
+          }
+          uint8_t* const tile = c.base_ptr + (2 + slot) * kTile;
+          const int64_t k0 = (int64_t)j * TR;
+          const int from = seen + 1 > k0 ? (int)(seen + 1 - k0) : 0;
+          for (int i = from * NV + lane; i < TR * NV; i += 32) {
+            const int key = i / NV, v = w * NV + (i - key * NV);
+            uint4* const p = reinterpret_cast<uint4*>(tile + (v >> 3) * kChunk + key * 128 + (((v & 7) ^ (key & 7)) << 4));
+            if (k0 + key >= cur.r.kv) {
+              *p = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 x = *p;
+            uint32_t* const e = reinterpret_cast<uint32_t*>(&x);
+            bool bad = false;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              bad |= (e[q] & 0x7f80u) == 0x7f80u || (e[q] & 0x7f800000u) == 0x7f800000u;
+            if (bad) {
+              for (int q = 0; q < 8; ++q) {
+                const int half = q & 1;
+                if (((e[q >> 1] >> (16 * half)) & 0x7f80u) != 0x7f80u) continue;
+                e[q >> 1] &= half ? 0x0000ffffu : 0xffff0000u;
+                note_min(notes + (v - w * NV) * 4 + (q >> 1), half, (unsigned)(k0 + key - seen < 0xfffe ? k0 + key - seen : 0xfffe));
+              }
+              *p = x;
+              sh.noted[ic % kNotes][w] = 1;
+            }
+          }
+          fence_proxy_async_smem();  // the tensor core reads what was rewritten
+          warp_arrive(v_checked(slot), lane);
+          warp_arrive(r_empty(slot), lane);
+        }
+        ++ic;
+      } while (ok && cur.next(A));
+    }
+  } else {
+    // ------------------------------------------------------------ softmax rows (warpgroups 1, 2)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegsHigh));
+    const Ranges ranges(units, gridDim.x);
+    const int sl = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // the slot's row: token r / group, head r % group
+    const int tok = r / A.group, g = r - tok * A.group;
+    const float sl2 = A.scale * kLog2e;
+    const uint32_t s_col = (uint32_t)(sl * TR), o_col = 256u + (uint32_t)(sl * D);
+    const size_t pf = many_part_floats(D);
+    uint32_t sc = 0, oc = 0, ic = 0, xc = 0;  // score tiles, finished accumulators, pieces, split pieces
+    bool ok = true;
+    do {
+      const int cnt = cur.count(sl);
+      const int64_t token = cur.tok(sl) + tok;  // of the request
+      const bool live = tok < cur.r.tt && token < cur.r.n;
+      const int64_t lim = (int64_t)cur.r.kv - cur.r.n + token;  // the row's last key
+      float m = -INFINITY, l = 0.0f;
+      for (int j = cur.j0; j < cur.j0 + cnt && ok; ++j) {
+        // new scores; they also mean the slot's previous P V has finished
+        if (!(ok = warp_wait(s_full(sl), sc & 1, c, A.err, lane))) break;
+        ++sc;
+        tc_fence_after();
+        // columns of this tile that the row sees: [0, vis]
+        const int64_t left = lim - (int64_t)j * TR;
+        const int vis = left >= TR ? TR : (int)(left < -1 ? -1 : left);
+        const bool part = __any_sync(0xffffffffu, vis < TR - 1);
+        float ps[8], mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ps[i] = 0.0f;
+          mx[i] = -INFINITY;
+        }
+#pragma unroll 1
+        for (int cc = 0; cc < TR / 32; ++cc) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem_row(tmem, quarter, s_col + (uint32_t)(cc * 32)), v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!part || cc * 32 + e <= vis) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(v[e]));
+        }
+        float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        mt *= sl2;
+        const bool move = mt > m + kMoveLog2;
+        if (j > cur.j0 && __any_sync(0xffffffffu, move)) {
+          const float f = move ? ex2_approx(m - mt) : 1.0f;
+          l *= f;
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t ov[32];
+            tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+            tmem_st_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
+          }
+        }
+        if (move) m = mt;
+        const float mb = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+        for (int cc = 0; cc < TR / 32; ++cc) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem_row(tmem, quarter, s_col + (uint32_t)(cc * 32)), v);
+          tmem_ld_wait();
+          uint32_t pk[32];  // 16 columns of hi pairs, 16 of lo pairs
+#pragma unroll
+          for (int e2 = 0; e2 < 16; ++e2) {
+            const int col = cc * 32 + 2 * e2;
+            const float f0 = (!part || col <= vis) ? ex2_approx(fmaf(__uint_as_float(v[2 * e2]), sl2, -mb)) : 0.0f;
+            const float f1 = (!part || col + 1 <= vis) ? ex2_approx(fmaf(__uint_as_float(v[2 * e2 + 1]), sl2, -mb)) : 0.0f;
+            ps[(2 * e2) & 7] += f0;
+            ps[(2 * e2 + 1) & 7] += f1;
+            const uint32_t h = pack_bf16(f0, f1);
+            pk[e2] = h;
+            pk[16 + e2] = pack_bf16(f0 - __uint_as_float(h << 16), f1 - __uint_as_float(h & 0xffff0000u));
+          }
+          tmem_st_32x32b_x32(tmem_row(tmem, quarter, s_col + (uint32_t)(cc * 32)), pk);
+        }
+        tmem_st_wait();
+        l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+        tc_fence_before();
+        warp_arrive(p_full(sl), lane);
+      }
+      if (!ok) break;
+      if (cnt > 0) {
+        if (!(ok = warp_wait(o_full(sl), oc & 1, c, A.err, lane))) break;
+        ++oc;
+        tc_fence_after();
+      }
+      const bool whole = cur.j0 == 0 && cur.j1 == cur.nkv;
+      // columns whose notes say that this row sees a value that is not finite
+      const unsigned* const notes = sh.notes[ic % kNotes];
+      const unsigned rel = (unsigned)(token - cur.tok(0));  // the row's last key - the pair's first row's
+      const bool hurt = cnt > 0 && cur.partial(cur.j0 + cnt - 1) && (sh.noted[ic % kNotes][0] | sh.noted[ic % kNotes][1]) != 0;
+      const auto spoil = [&](uint32_t (&ov)[32], int cc) {
+        if (!hurt) return;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (((notes[(cc * 32 + e) >> 1] >> (16 * (e & 1))) & 0xffffu) <= rel) ov[e] = 0x7fffffffu;
+      };
+      const int head = cur.h * A.group + g;
+      const int64_t row = cur.r.q0 + token;
+      bf16* const dst = A.o + row * A.o_token + (int64_t)head * A.o_head;
+      const auto put_lse = [&](float top, float sum) {
+        if (A.lse)
+          A.lse[row * (int64_t)(A.group * A.c.kv_heads) + head] =
+              sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * kLn2;
+      };
+      if (whole) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if (cnt > 0)
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t ov[32];
+            tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
+            tmem_ld_wait();
+            spoil(ov, cc);
+            if (live) store_row32(dst + cc * 32, ov, inv);
+          }
+        if (cnt > 0) {
+          tc_fence_before();
+          warp_arrive(o_empty(sl), lane);
+        }
+        if (live) put_lse(m, l);
+      } else {
+        // element (column block of 4, row) of a part: rows consecutive, so that a warp's accesses are
+        float* const part = parts + ((size_t)blockIdx.x * 2 + (cur.j0 == 0 ? 1 : 0)) * pf;
+        const int prow = sl * TR + r;
+        if (cnt > 0) {
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t ov[32];
+            tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
+            tmem_ld_wait();
+            spoil(ov, cc);
+            if (live)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                __stcg(reinterpret_cast<uint4*>(part) + (size_t)(cc * 8 + e) * (2 * TR) + prow,
+                       make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]));
+          }
+          tc_fence_before();
+          warp_arrive(o_empty(sl), lane);
+        }
+        if (live) {
+          __stcg(part + (size_t)2 * TR * D + prow, m);
+          __stcg(part + (size_t)2 * TR * (D + 1) + prow, l);
+        }
+        __threadfence();
+        warp_arrive(part_full, lane);
+        const int64_t item0 = cur.u - cur.j0;
+        const int c0 = (int)ranges.owner(item0), pieces = (int)ranges.owner(item0 + cur.nkv - 1) - c0 + 1;
+        if (warp == 4 && lane == 0) {
+          if ((ok = mbar_wait(part_full, xc & 1, c.abort_flag, A.err))) {
+            __threadfence();
+            // the count returns to zero with the item's last arrival
+            sh.last = atomicInc(counters + c0, (unsigned)pieces - 1) == (unsigned)pieces - 1;
+            mbar_arrive(part_last);
+          }
+        }
+        if (!(ok = warp_wait(part_last, xc & 1, c, A.err, lane))) break;
+        ++xc;
+        if (*reinterpret_cast<volatile int*>(&sh.last)) {
+          __threadfence();
+          if (live) {
+            const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * pf; };
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
+            for (int p = 0; p < pieces; ++p) top = fmaxf(top, __ldcg(at(p) + (size_t)2 * TR * D + prow));
+            const float tb = top == -INFINITY ? 0.0f : top;
+            for (int cc = 0; cc < D / 32; ++cc) {
+              float acc[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) acc[e] = 0.0f;
+              sum = 0.0f;
+              for (int p = 0; p < pieces; ++p) {
+                const float lp = __ldcg(at(p) + (size_t)2 * TR * (D + 1) + prow);
+                if (lp == 0.0f) continue;  // no key of this row in the part, which may hold no O then
+                const float f = ex2_approx(__ldcg(at(p) + (size_t)2 * TR * D + prow) - tb);
+                sum += f * lp;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(at(p)) + (size_t)(cc * 8 + e) * (2 * TR) + prow);
+                  acc[4 * e] += f * v.x;
+                  acc[4 * e + 1] += f * v.y;
+                  acc[4 * e + 2] += f * v.z;
+                  acc[4 * e + 3] += f * v.w;
+                }
+              }
+              uint32_t ov[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(acc[e]);
+              store_row32(dst + cc * 32, ov, sum == 0.0f ? 0.0f : 1.0f / sum);
+            }
+            put_lse(top, sum);
+          }
+        }
+      }
+      ++ic;
+    } while (cur.next(A));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
+
+// a bf16 array of `rank` dimensions (columns first, strides in elements), boxes of 64 columns with the 128-byte swizzle
+tp3d_status row_map(CUtensorMap* m, const void* ptr, int rank, const int64_t* dims, const int64_t* strides,
+                    const uint32_t* box) {
+  auto fn = encode();
+  if (!fn) return TP3D_ECUDA;
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], es[4];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i > 0) {
+      // a tensor map's strides are below 2^40 bytes
+      if (strides[i - 1] >= ((int64_t)1 << 39)) return TP3D_EUNSUPPORTED;
+      st[i - 1] = (cuuint64_t)strides[i - 1] * 2;
+    }
+  }
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), d, st, bx, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TP3D_OK : TP3D_ECUDA;
+}
+
+template <int D>
+tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool alone, void* workspace, cudaStream_t s) {
   TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)few_smem<D>()));
   paged_attn_few_kernel<D><<<ctx->num_sms * kFewPerSm, kFewThreads, few_smem<D>(), s>>>(
@@ -614,21 +1230,42 @@ static tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool alone, voi
   return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
 }
 
+template <int D>
+tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, void* workspace, cudaStream_t s) {
+  CUtensorMap mq, mk, mv;
+  const int64_t qd[3] = {D, (int64_t)A.group * A.c.kv_heads, A.tokens}, qs[2] = {A.q_head, A.q_token};
+  const uint32_t qb[3] = {64, (uint32_t)A.group, (uint32_t)(TR / A.group)};
+  TP3D_TRY(row_map(&mq, A.q, 3, qd, qs, qb));
+  const int64_t cd[4] = {D, A.c.page, A.c.kv_heads, A.c.pages};
+  const int64_t cs[3] = {A.c.token_stride, A.c.head_stride, A.c.page_stride};
+  const uint32_t cb[4] = {64, (uint32_t)(A.c.page < TR ? A.c.page : TR), 1, 1};
+  TP3D_TRY(row_map(&mk, A.c.k, 4, cd, cs, cb));
+  TP3D_TRY(row_map(&mv, A.c.v, 4, cd, cs, cb));
+  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem));
+  // setmaxnreg.inc waits until the block's launch registers cover the split
+  cudaFuncAttributes fa;
+  TP3D_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_attn_many_kernel<D>));
+  if (fa.numRegs * kManyThreads < 128 * kManyRegsLow + 256 * kManyRegsHigh) return TP3D_EUNSUPPORTED;
+  paged_attn_many_kernel<D><<<ctx->num_sms, kManyThreads, kManySmem, s>>>(mq, mk, mv, A, static_cast<float*>(workspace),
+                                                                        ctx->d_paged);
+  return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
+}
+
+}  // namespace
+
+size_t paged_attn_workspace(const tp3d_ctx* ctx, int d) {
+  const size_t few = (size_t)ctx->num_sms * kFewPerSm * 2 * few_part_floats(d);
+  const size_t many = (size_t)ctx->num_sms * 2 * many_part_floats(d);
+  return (few > many ? few : many) * sizeof(float);
+}
+
 tp3d_status launch_paged_attn(tp3d_ctx* ctx, const PagedAttn& A, int max_new, void* workspace, cudaStream_t s) {
   if (ctx->num_sms * kFewPerSm > kPagedCounters) return TP3D_EUNSUPPORTED;
-  const int heads = A.group * A.c.kv_heads;
   const int64_t most = (max_new > 0 && max_new < A.tokens ? max_new : A.tokens) * A.group;
-  const bool alone = most <= kFewRows;
-  TP3D_TRY(A.c.head_dim == 128 ? launch_few<128>(ctx, A, alone, workspace, s)
-                               : launch_few<64>(ctx, A, alone, workspace, s));
+  const bool alone = most <= kFewRows, d128 = A.c.head_dim == 128;
+  TP3D_TRY(d128 ? launch_few<128>(ctx, A, alone, workspace, s) : launch_few<64>(ctx, A, alone, workspace, s));
   if (alone) return TP3D_OK;
-  if (heads > 65535) return TP3D_EUNSUPPORTED;
-  const dim3 grid((unsigned)A.tokens, (unsigned)heads);
-  if (A.c.head_dim == 128)
-    paged_attn_row_kernel<128><<<grid, kRowWarps * 32, 0, s>>>(A);
-  else
-    paged_attn_row_kernel<64><<<grid, kRowWarps * 32, 0, s>>>(A);
-  return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
+  return d128 ? launch_many<128>(ctx, A, workspace, s) : launch_many<64>(ctx, A, workspace, s);
 }
 
 }  // namespace tp3d
