@@ -88,7 +88,7 @@ typedef struct {
  * the top, request by request; *free_left is the count after the step.  The
  * counts are separate buffers (as kv_len and cached are), so a call can be
  * repeated or replayed.
- * A negative length, a request longer than table_width pages or 2^31 - 1
+ * A negative length, a request longer than table_width pages or 2^31 - 4097
  * tokens, a free_count outside [0, free_cap], or too few free pages or
  * `tokens` raise TP3D_EPAGES: tokens without a page then get slot -1, pages
  * not had are entered as -1, and a request whose own lengths are bad gets no

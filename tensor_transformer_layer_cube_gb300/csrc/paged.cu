@@ -51,10 +51,10 @@ struct Lengths {
 __device__ __forceinline__ Lengths plan_lengths(const PlanArgs& P, int b) {
   Lengths l{__ldg(P.cached + b), __ldg(P.fresh + b), false};
   const int64_t cap = P.width << P.page_log2, kv = (int64_t)l.cached + l.fresh;
-  if (l.cached < 0 || l.fresh < 0 || kv > cap || kv > INT32_MAX) {
+  if (l.cached < 0 || l.fresh < 0 || kv > cap || kv > kPagedMaxTokens) {
     l.bad = true;
     l.fresh = 0;
-    l.cached = l.cached < 0 ? 0 : l.cached > cap ? (int32_t)cap : l.cached;
+    l.cached = l.cached < 0 ? 0 : l.cached > cap ? (int32_t)(cap < kPagedMaxTokens ? cap : kPagedMaxTokens) : l.cached;
   }
   return l;
 }
@@ -339,7 +339,7 @@ tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3
   if (heads % cache->kv_heads) return TP3D_ESHAPE;
   if (heads / cache->kv_heads > 128) return TP3D_EUNSUPPORTED;
   if (batch->requests < 0 || batch->tokens < 0 || batch->table_width < 0) return TP3D_EINVAL;
-  if (batch->tokens > INT32_MAX || batch->table_width > INT32_MAX) return TP3D_EUNSUPPORTED;
+  if (batch->tokens > kPagedMaxTokens || batch->table_width > INT32_MAX) return TP3D_EUNSUPPORTED;
   if (batch->requests == 0 || batch->tokens == 0) return TP3D_OK;
   if (!batch->q_start || !batch->kv_len || (batch->table_width > 0 && !batch->block_table)) return TP3D_EINVAL;
   if (!Q || !O || !workspace) return TP3D_EINVAL;

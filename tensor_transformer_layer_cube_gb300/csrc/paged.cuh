@@ -6,6 +6,10 @@
 
 namespace tp3d {
 
+// the most tokens of one request, and rows of one call: sums of a position and
+// a few tiles' rows stay in 32 bits
+constexpr int64_t kPagedMaxTokens = INT32_MAX - 4096;
+
 // One call of tp3d_paged_attn, as its kernels take it (element strides).
 struct PagedAttn {
   tp3d_kv_cache c;
@@ -37,7 +41,7 @@ struct PagedRequest {
 };
 __device__ __forceinline__ PagedRequest paged_request(const PagedAttn& A, int b) {
   const int32_t s0 = __ldg(A.q_start + b), s1 = __ldg(A.q_start + b + 1), len = __ldg(A.kv_len + b);
-  const int64_t cap = A.width << A.page_log2;
+  const int64_t width = A.width << A.page_log2, cap = width < kPagedMaxTokens ? width : kPagedMaxTokens;
   PagedRequest r;
   const int64_t q0 = s0 < 0 ? 0 : s0 > A.tokens ? A.tokens : s0;
   const int64_t q1 = s1 < q0 ? q0 : s1 > A.tokens ? A.tokens : s1;

@@ -593,15 +593,14 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 
 // The pairs of query tiles of a request: pair k holds tokens [2 k tt, +2 tt).
 struct ManyRequest {
-  int64_t q0;
-  int n, kv, tt;  // tt: tokens of a query tile
+  int q0, n, kv, tt;  // tt: tokens of a query tile
   __device__ int pairs() const { return (n + 2 * tt - 1) / (2 * tt); }
   // key tiles that tokens below `end` see (one at least: rows without keys are written too)
-  __device__ int tiles_upto(int64_t end) const {
-    const int64_t keys = (int64_t)kv - n + (end < n ? end : n);
-    return keys > 0 ? (int)((keys + TR - 1) / TR) : 1;
+  __device__ int tiles_upto(int end) const {
+    const int keys = kv - n + (end < n ? end : n);
+    return keys > 0 ? (keys - 1) / TR + 1 : 1;
   }
-  __device__ int tiles(int k) const { return tiles_upto((int64_t)(k + 1) * 2 * tt); }
+  __device__ int tiles(int k) const { return tiles_upto((k + 1) * 2 * tt); }
   // key tiles of the pairs before pair k (the last pair's are not among them)
   __device__ int64_t before(int64_t k) const {
     const int64_t w = 2 * tt, ctx = (int64_t)kv - n;
@@ -618,7 +617,7 @@ struct ManyRequest {
 __device__ __forceinline__ ManyRequest many_request(const PagedAttn& A, int b) {
   const PagedRequest r = paged_request(A, b);
   ManyRequest m;
-  m.q0 = r.q0;
+  m.q0 = (int)r.q0;
   m.n = (int64_t)r.n * A.group > kFewRows ? r.n : 0;  // the others are the kernel above's
   m.kv = r.kv;
   m.tt = TR / A.group;
@@ -652,7 +651,7 @@ struct ManyCursor {
     set(A);
     return true;
   }
-  __device__ int64_t tok(int sl) const { return ((int64_t)2 * k + sl) * r.tt; }  // a slot's first token
+  __device__ int tok(int sl) const { return (2 * k + sl) * r.tt; }  // a slot's first token
   __device__ bool two() const { return tok(1) < r.n; }
   // key tiles of slot sl in this piece
   __device__ int count(int sl) const {
@@ -661,7 +660,7 @@ struct ManyCursor {
     return n0 < j1 ? (n0 > j0 ? n0 - j0 : 0) : j1 - j0;
   }
   // key tile j holds keys that the pair's first row does not see
-  __device__ bool partial(int j) const { return ((int64_t)j + 1) * TR - 1 > (int64_t)r.kv - r.n + tok(0); }
+  __device__ bool partial(int j) const { return (j + 1) * TR - 1 > r.kv - r.n + tok(0); }
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
@@ -684,6 +683,116 @@ __device__ __forceinline__ void note_min(unsigned* word, int half, unsigned v) {
   }
 }
 
+// A position in the ring: slot, and the parity of the slot's phase.
+struct RingPos {
+  uint32_t slot = 0, phase = 0;
+  __device__ void next() {
+    if (++slot == kManyRing) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// mbar_wait in fewer instructions (the clock and the abort flag are looked at
+// after each suspended try): the kernel's roles together fill the instruction
+// cache
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, const Ctx& c, int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*c.abort_flag) return false;
+  } while (globaltimer_ns() - t0 <= wait_limit_ns(err));
+  *c.abort_flag = 1;
+  raise_error(err, TP3D_ETIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, const Ctx& c, int* err, int lane) {
+  const bool ok = lane == 0 ? wait_on(bar, parity, c, err) : false;
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// One key tile of one row: its 128 scores at `s` in tensor memory become P
+// there (per 32 columns: 16 of hi pairs, 16 of lo pairs), the running maximum
+// m (base-2 units) and sum l are updated and, when some row of the warp has to
+// move its maximum, the row of O at `o` is rescaled.  The first 64 keys' P is
+// announced on `half`, so that its product starts while the rest is formed.
+// Both passes (maximum, then P) read the scores 32 columns at a time in rolled
+// loops: unrolled over the row, the code outgrows the instruction cache and
+// runs slower with half the instructions.  What has a paired fp32 form
+// (.f32x2) uses it.  PART: only columns up to `vis` are seen.
+template <int D, bool PART>
+__device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t half, int lane, float sl2, int vis,
+                                             bool first, float& m, float& l) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int cc = 0; cc < 4; ++cc) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(s + (uint32_t)(cc * 32), v);
+    tmem_ld_wait();
+    const int left = vis - cc * 32;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float x = !PART || e <= left ? __uint_as_float(v[e]) : -INFINITY;
+      const float y = !PART || e + 1 <= left ? __uint_as_float(v[e + 1]) : -INFINITY;
+      mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], x), y);
+    }
+  }
+  const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+  const bool move = mt > m + kMoveLog2;
+  if (__any_sync(0xffffffffu, move)) {
+    if (!first) {
+      const float f = move ? ex2_approx(m - mt) : 1.0f;
+      l *= f;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 16; ++cc) {
+        uint32_t ov[16];
+        tmem_ld_32x32b_x16(o + (uint32_t)(cc * 16), ov);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+        tmem_st_32x32b_x16(o + (uint32_t)(cc * 16), ov);
+      }
+    }
+    if (move) m = mt;
+  }
+  const float mb = m == -INFINITY ? 0.0f : m;
+  const f32x2 sc = splat2(sl2), nb = splat2(-mb), minus = splat2(-1.0f);
+  f32x2 sum[4] = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int cc = 0; cc < 4; ++cc) {
+    uint32_t v[32], pk[32];
+    tmem_ld_32x32b_x32(s + (uint32_t)(cc * 32), v);
+    tmem_ld_wait();
+    const int left = vis - cc * 32;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float p0, p1, t0, t1;
+      upk2(fma2(pk2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc, nb), p0, p1);
+      p0 = !PART || 2 * e <= left ? ex2_approx(p0) : 0.0f;
+      p1 = !PART || 2 * e + 1 <= left ? ex2_approx(p1) : 0.0f;
+      const f32x2 P = pk2(p0, p1);
+      sum[e & 3] = add2(sum[e & 3], P);
+      // hi: the upper halves as they are (truncated to bf16); lo: the exact rest, rounded
+      const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+      pk[e] = __byte_perm(b0, b1, 0x7632);
+      upk2(fma2(pk2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)), minus, P), t0, t1);
+      pk[16 + e] = pack_bf16(t0, t1);
+    }
+    tmem_st_32x32b_x32(s + (uint32_t)(cc * 32), pk);
+    if (cc == 1) {
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(half, lane);
+    }
+  }
+  tmem_st_wait();
+  float a0, a1;
+  upk2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
+  l += a0 + a1;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kManyThreads, 1)
     paged_attn_many_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -704,6 +813,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   auto p_empty = [&](int sl) { return bar(16 + sl); };
   auto o_full = [&](int sl) { return bar(18 + sl); };
   auto o_empty = [&](int sl) { return bar(20 + sl); };
+  auto p_half = [&](int sl) { return bar(30 + sl); };
   auto v_checked = [&](uint32_t i) { return bar(23 + (int)i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -754,11 +864,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
   }
   if (threadIdx.x == 0) {
-    for (int k = 0; k < 30; ++k) {
-      // p_full, o_empty: one arrival per row warp of the slot; r_empty: the
+    for (int k = 0; k < 32; ++k) {
+      // p_half, p_full, o_empty: one arrival per row warp of the slot; r_empty: the
       // issuer and the two value-check warps (which follow every slot, so that
       // no phase passes them by); v_checked: those two; part_full: all row warps
-      const bool four = k == 14 || k == 15 || k == 20 || k == 21, ring_empty = k >= 7 && k < 12;
+      const bool four = k == 14 || k == 15 || k == 20 || k == 21 || k >= 30, ring_empty = k >= 7 && k < 12;
       mbar_init(bar(k), four ? 4 : ring_empty ? 3 : k >= 23 && k < 28 ? 2 : k == 28 ? 8 : 1);
     }
     *c.abort_flag = 0;
@@ -808,22 +918,23 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const bool mine = ch < NCH;
       const uint32_t box_dst = (uint32_t)ch * kChunk + ((uint32_t)pi << bl2) * 128u;
       const uint32_t kv_bytes = (uint32_t)TR * D * 2, q_bytes = (uint32_t)(cur.r.tt * A.group) * D * 2;
+      RingPos pos;
       uint32_t n = 0, ic = 0;
       bool ok = true;
       do {
         const bool two = cur.two();
-        if (!(ok = warp_wait(q_empty, (ic & 1) ^ 1, c, A.err, lane))) break;
+        if (!(ok = warp_wait_on(q_empty, (ic & 1) ^ 1, c, A.err, lane))) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(q_full, q_bytes * (two ? 2u : 1u));
           for (int sl = 0; sl < (two ? 2 : 1); ++sl)
             for (int x = 0; x < NCH; ++x)
               tma_load_3d(sQ(sl) + (uint32_t)x * kChunk, &mq, q_full, 64 * x, cur.h * A.group,
-                          (int)(cur.r.q0 + cur.tok(sl)));
+                          cur.r.q0 + cur.tok(sl));
         }
         ++ic;
         for (int j = cur.j0; j < cur.j1 && ok; ++j) {
           // a box outside the request or the pool starts past the last page: TMA fills it with zeros
-          const int64_t key = (int64_t)j * TR + ((int64_t)pi << bl2);
+          const int key = j * TR + (pi << bl2);
           int32_t page = (int32_t)A.c.pages;
           if (mine && key < cur.r.kv) {
             page = __ldg(A.table + (int64_t)cur.b * A.width + (key >> A.page_log2));
@@ -833,9 +944,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             }
           }
           const int in_page = (int)(key & (A.c.page - 1));
-          for (int kvi = 0; kvi < 2; ++kvi, ++n) {
-            const uint32_t slot = n % kManyRing;
-            if (!(ok = warp_wait(r_empty(slot), ((n / kManyRing) & 1) ^ 1, c, A.err, lane))) break;
+          for (int kvi = 0; kvi < 2; ++kvi, ++n, pos.next()) {
+            const uint32_t slot = pos.slot;
+            if (!(ok = warp_wait_on(r_empty(slot), pos.phase ^ 1, c, A.err, lane))) break;
             if (lane == 0) mbar_arrive_expect_tx(r_full(slot), kv_bytes);
             __syncwarp();
             if (mine) tma_load_4d(sR(slot) + box_dst, kvi ? &mv : &mk, r_full(slot), 64 * ch, in_page, cur.h, page);
@@ -849,32 +960,46 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------------ MMA issuer
-      const uint32_t id_s = idesc_bf16_f32(TR, TR, 0, 0);  // S = Q K^T
-      const uint32_t id_o = idesc_bf16_f32(TR, D, 0, 1);   // O += P V (P from TMEM, V MN-major)
-      uint32_t n = 0, ic = 0, vc = 0;  // vc: the next v_checked phase's parity, a bit per slot
+      // This one thread keeps the tensor core fed, so what it does between
+      // products is kept short: descriptors by addition, ring slots by
+      // counting, and the next tiles' arrival looked at before the
+      // probabilities are waited for.
+      constexpr uint32_t id_s = idesc_bf16_f32(TR, TR, 0, 0);  // S = Q K^T
+      constexpr uint32_t id_o = idesc_bf16_f32(TR, D, 0, 1);   // O += P V (P from TMEM, V MN-major)
+      constexpr uint64_t kSlotStep = kTile >> 4;
+      const uint64_t q_desc = desc_kmajor(sQ(0), 0), k_desc = desc_kmajor(sR(0), 0), v_desc = desc_mnmajor(sR(0), 0);
+      RingPos pos;
+      uint32_t ic = 0, vc = 0;  // vc: the next v_checked phase's parity, a bit per slot
       uint32_t pc[2] = {0, 0}, oc[2] = {0, 0};  // P V products issued, pieces finished, per slot
       bool ok = true;
-      auto ring = [&](uint32_t idx, uint32_t& slot) -> bool {
-        slot = idx % kManyRing;
-        return mbar_wait(r_full(slot), (idx / kManyRing) & 1, c.abort_flag, A.err);
-      };
       auto issue_s = [&](int sl, uint32_t kslot) -> bool {
-        if (pc[sl] > 0 && !mbar_wait(p_empty(sl), (pc[sl] - 1) & 1, c.abort_flag, A.err)) return false;
+        if (pc[sl] > 0 && !wait_on(p_empty(sl), (pc[sl] - 1) & 1, c, A.err)) return false;
         tc_fence_after();
-        mma_tile(tmem + (uint32_t)(sl * TR), sQ(sl), false, sR(kslot), false, D / 16, id_s, false);
+        const uint64_t qd = q_desc + (uint64_t)sl * kSlotStep, kd = k_desc + kslot * kSlotStep;
+        const uint32_t st = tmem + (uint32_t)(sl * TR);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (uint64_t)((k >> 2) * (kChunk >> 4) + (k & 3) * 2);
+          umma_bf16(st, qd + step, kd + step, id_s, k > 0 ? 1u : 0u);
+        }
         umma_commit(s_full(sl));
         return true;
       };
       auto issue_pv = [&](int sl, uint32_t vslot, bool first) -> bool {
-        if (!mbar_wait(p_full(sl), pc[sl] & 1, c.abort_flag, A.err)) return false;
-        if (first && !mbar_wait(o_empty(sl), (oc[sl] & 1) ^ 1, c.abort_flag, A.err)) return false;
+        if (!wait_on(p_half(sl), pc[sl] & 1, c, A.err)) return false;
+        if (first && !wait_on(o_empty(sl), (oc[sl] & 1) ^ 1, c, A.err)) return false;
         tc_fence_after();
         const uint32_t pt = tmem + (uint32_t)(sl * TR), ot = tmem + 256u + (uint32_t)(sl * D);
+        const uint64_t vd = v_desc + vslot * kSlotStep;
+#pragma unroll
         for (int k = 0; k < TR / 16; ++k) {
-          const uint64_t vd = desc_mnmajor(sR(vslot), k);
-          const uint32_t hi = pt + 32u * (uint32_t)(k >> 1) + 8u * (uint32_t)(k & 1);
-          umma_ts(ot, hi, vd, id_o, (!first || k > 0) ? 1u : 0u);
-          umma_ts(ot, hi + 16u, vd, id_o, 1u);
+          if (k == TR / 32) {
+            if (!wait_on(p_full(sl), pc[sl] & 1, c, A.err)) return false;
+            tc_fence_after();
+          }
+          const uint32_t hi = pt + (uint32_t)(32 * (k >> 1) + 8 * (k & 1));
+          umma_ts(ot, hi, vd + (uint64_t)(k * 128), id_o, k > 0 || !first ? 1u : 0u);
+          umma_ts(ot, hi + 16u, vd + (uint64_t)(k * 128), id_o, 1u);
         }
         umma_commit(p_empty(sl));
         ++pc[sl];
@@ -883,29 +1008,34 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       do {
         const int cnt[2] = {cur.count(0), cur.count(1)};
         const int nmax = cur.j1 - cur.j0;
-        if (!(ok = mbar_wait(q_full, ic & 1, c.abort_flag, A.err))) break;
+        if (!(ok = wait_on(q_full, ic & 1, c, A.err) && wait_on(r_full(pos.slot), pos.phase, c, A.err))) break;
         ++ic;
-        const uint32_t n0 = n;  // ring index of K_j0; K_(j0+i) = n0 + 2i, V_(j0+i) = n0 + 2i + 1
-        uint32_t ks = 0;
-        if (!(ok = ring(n0, ks) && (cnt[0] == 0 || issue_s(0, ks)) && (cnt[1] == 0 || issue_s(1, ks)))) break;
+        uint32_t ks = pos.slot;
+        pos.next();
+        if (!(ok = (cnt[0] == 0 || issue_s(0, ks)) && (cnt[1] == 0 || issue_s(1, ks)))) break;
         if (nmax == 1) umma_commit(q_empty);
         umma_commit(r_empty(ks));
         for (int i = 0; i < nmax && ok; ++i) {
-          uint32_t vs = 0, kn = 0;
           const bool more = i + 1 < nmax;
-          if (!(ok = ring(n0 + 2 * i + 1, vs))) break;
+          const uint32_t vs = pos.slot;
+          if (!(ok = wait_on(r_full(vs), pos.phase, c, A.err))) break;
+          pos.next();
           if (cur.partial(cur.j0 + i)) {
-            if (!(ok = mbar_wait(v_checked(vs), (vc >> vs) & 1, c.abort_flag, A.err))) break;
+            if (!(ok = wait_on(v_checked(vs), (vc >> vs) & 1, c, A.err))) break;
             vc ^= 1u << vs;
           }
-          if (more && !(ok = ring(n0 + 2 * i + 2, kn))) break;
+          if (more) {
+            ks = pos.slot;
+            if (!(ok = wait_on(r_full(ks), pos.phase, c, A.err))) break;
+            pos.next();
+          }
           for (int sl = 0; sl < 2 && ok; ++sl)
-            if (i < cnt[sl]) ok = issue_pv(sl, vs, i == 0) && (i + 1 >= cnt[sl] || issue_s(sl, kn));
+            if (i < cnt[sl]) ok = issue_pv(sl, vs, i == 0) && (i + 1 >= cnt[sl] || issue_s(sl, ks));
           if (!ok) break;
           umma_commit(r_empty(vs));
           if (more) {
             if (i + 2 == nmax) umma_commit(q_empty);  // the piece's last product with Q issued
-            umma_commit(r_empty(kn));
+            umma_commit(r_empty(ks));
           }
         }
         if (!ok) break;
@@ -914,7 +1044,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             umma_commit(o_full(sl));
             ++oc[sl];
           }
-        n = n0 + 2 * (uint32_t)nmax;
       } while (cur.next(A));
       umma_commit(final_bar);
       drain(final_bar, 0);
@@ -924,16 +1053,17 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // 16-byte vectors [w * NV, +NV) of the row's D / 8
       constexpr int NV = D / 16;
       const int w = warp - 2;
-      uint32_t n = 0, ic = 0;
+      RingPos pos;
+      uint32_t ic = 0;
       bool ok = true;
       do {
-        const int64_t seen = (int64_t)cur.r.kv - cur.r.n + cur.tok(0);  // the first row's last key
+        const int seen = cur.r.kv - cur.r.n + cur.tok(0);  // the first row's last key
         unsigned* const notes = sh.notes[ic % kNotes] + w * (NV * 4);
         bool noting = false;
-        for (uint32_t i2 = 0; i2 < 2 * (uint32_t)(cur.j1 - cur.j0); ++i2, ++n) {
+        for (uint32_t i2 = 0; i2 < 2 * (uint32_t)(cur.j1 - cur.j0); ++i2, pos.next()) {
           const int j = cur.j0 + (int)(i2 >> 1);
-          const uint32_t slot = n % kManyRing;
-          if (!(ok = warp_wait(r_full(slot), (n / kManyRing) & 1, c, A.err, lane))) break;
+          const uint32_t slot = pos.slot;
+          if (!(ok = warp_wait_on(r_full(slot), pos.phase, c, A.err, lane))) break;
           if (!(i2 & 1) || !cur.partial(j)) {
             warp_arrive(r_empty(slot), lane);
             continue;
@@ -945,8 +1075,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             __syncwarp();
           }
           uint8_t* const tile = c.base_ptr + (2 + slot) * kTile;
-          const int64_t k0 = (int64_t)j * TR;
-          const int from = seen + 1 > k0 ? (int)(seen + 1 - k0) : 0;
+          const int k0 = j * TR, from = seen + 1 > k0 ? seen + 1 - k0 : 0;
           for (int i = from * NV + lane; i < TR * NV; i += 32) {
             const int key = i / NV, v = w * NV + (i - key * NV);
             uint4* const p = reinterpret_cast<uint4*>(tile + (v >> 3) * kChunk + key * 128 + (((v & 7) ^ (key & 7)) << 4));
@@ -981,7 +1110,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax rows (warpgroups 1, 2)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegsHigh));
-    const Ranges ranges(units, gridDim.x);
     const int sl = (warp - 4) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // the slot's row: token r / group, head r % group
@@ -993,78 +1121,28 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     bool ok = true;
     do {
       const int cnt = cur.count(sl);
-      const int64_t token = cur.tok(sl) + tok;  // of the request
+      const int token = cur.tok(sl) + tok;  // of the request
       const bool live = tok < cur.r.tt && token < cur.r.n;
-      const int64_t lim = (int64_t)cur.r.kv - cur.r.n + token;  // the row's last key
+      const int lim = cur.r.kv - cur.r.n + token;  // the row's last key
       float m = -INFINITY, l = 0.0f;
       for (int j = cur.j0; j < cur.j0 + cnt && ok; ++j) {
         // new scores; they also mean the slot's previous P V has finished
-        if (!(ok = warp_wait(s_full(sl), sc & 1, c, A.err, lane))) break;
+        if (!(ok = warp_wait_on(s_full(sl), sc & 1, c, A.err, lane))) break;
         ++sc;
         tc_fence_after();
         // columns of this tile that the row sees: [0, vis]
-        const int64_t left = lim - (int64_t)j * TR;
-        const int vis = left >= TR ? TR : (int)(left < -1 ? -1 : left);
-        const bool part = __any_sync(0xffffffffu, vis < TR - 1);
-        float ps[8], mx[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ps[i] = 0.0f;
-          mx[i] = -INFINITY;
-        }
-#pragma unroll 1
-        for (int cc = 0; cc < TR / 32; ++cc) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem_row(tmem, quarter, s_col + (uint32_t)(cc * 32)), v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!part || cc * 32 + e <= vis) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(v[e]));
-        }
-        float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-        mt *= sl2;
-        const bool move = mt > m + kMoveLog2;
-        if (j > cur.j0 && __any_sync(0xffffffffu, move)) {
-          const float f = move ? ex2_approx(m - mt) : 1.0f;
-          l *= f;
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t ov[32];
-            tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
-            tmem_st_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
-          }
-        }
-        if (move) m = mt;
-        const float mb = m == -INFINITY ? 0.0f : m;
-#pragma unroll 1
-        for (int cc = 0; cc < TR / 32; ++cc) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem_row(tmem, quarter, s_col + (uint32_t)(cc * 32)), v);
-          tmem_ld_wait();
-          uint32_t pk[32];  // 16 columns of hi pairs, 16 of lo pairs
-#pragma unroll
-          for (int e2 = 0; e2 < 16; ++e2) {
-            const int col = cc * 32 + 2 * e2;
-            const float f0 = (!part || col <= vis) ? ex2_approx(fmaf(__uint_as_float(v[2 * e2]), sl2, -mb)) : 0.0f;
-            const float f1 = (!part || col + 1 <= vis) ? ex2_approx(fmaf(__uint_as_float(v[2 * e2 + 1]), sl2, -mb)) : 0.0f;
-            ps[(2 * e2) & 7] += f0;
-            ps[(2 * e2 + 1) & 7] += f1;
-            const uint32_t h = pack_bf16(f0, f1);
-            pk[e2] = h;
-            pk[16 + e2] = pack_bf16(f0 - __uint_as_float(h << 16), f1 - __uint_as_float(h & 0xffff0000u));
-          }
-          tmem_st_32x32b_x32(tmem_row(tmem, quarter, s_col + (uint32_t)(cc * 32)), pk);
-        }
-        tmem_st_wait();
-        l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+        const int vis = lim - j * TR;
+        const uint32_t sa = tmem_row(tmem, quarter, s_col), oa = tmem_row(tmem, quarter, o_col);
+        if (__any_sync(0xffffffffu, vis < TR - 1))
+          many_softmax<D, true>(sa, oa, p_half(sl), lane, sl2, vis, j == cur.j0, m, l);
+        else
+          many_softmax<D, false>(sa, oa, p_half(sl), lane, sl2, vis, j == cur.j0, m, l);
         tc_fence_before();
         warp_arrive(p_full(sl), lane);
       }
       if (!ok) break;
       if (cnt > 0) {
-        if (!(ok = warp_wait(o_full(sl), oc & 1, c, A.err, lane))) break;
+        if (!(ok = warp_wait_on(o_full(sl), oc & 1, c, A.err, lane))) break;
         ++oc;
         tc_fence_after();
       }
@@ -1080,7 +1158,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (((notes[(cc * 32 + e) >> 1] >> (16 * (e & 1))) & 0xffffu) <= rel) ov[e] = 0x7fffffffu;
       };
       const int head = cur.h * A.group + g;
-      const int64_t row = cur.r.q0 + token;
+      const int64_t row = (int64_t)cur.r.q0 + token;
       bf16* const dst = A.o + row * A.o_token + (int64_t)head * A.o_head;
       const auto put_lse = [&](float top, float sum) {
         if (A.lse)
@@ -1127,6 +1205,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         __threadfence();
         warp_arrive(part_full, lane);
+        const Ranges ranges(units, gridDim.x);
         const int64_t item0 = cur.u - cur.j0;
         const int c0 = (int)ranges.owner(item0), pieces = (int)ranges.owner(item0 + cur.nkv - 1) - c0 + 1;
         if (warp == 4 && lane == 0) {
@@ -1137,7 +1216,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             mbar_arrive(part_last);
           }
         }
-        if (!(ok = warp_wait(part_last, xc & 1, c, A.err, lane))) break;
+        if (!(ok = warp_wait_on(part_last, xc & 1, c, A.err, lane))) break;
         ++xc;
         if (*reinterpret_cast<volatile int*>(&sh.last)) {
           __threadfence();
