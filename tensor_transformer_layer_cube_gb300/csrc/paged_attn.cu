@@ -573,18 +573,19 @@ constexpr int kManySmem = 7 * (int)kTile + 512 + (int)sizeof(ManyShared) + 1024;
 static_assert(kManySmem <= 232448, "shared memory of one CTA");
 TP3D_HD constexpr size_t many_part_floats(int d) { return (size_t)2 * TR * (d + 2); }
 
-// sum of floor((a i + b) / m) for i < n, all non-negative (the Euclidean recursion)
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// sum of floor((a i + b) / m) for i < n (the Euclidean recursion); a n + b
+// stays in 32 bits
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t s = 0;
   while (n > 0) {
-    s += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+    s += (int64_t)(a / m) * ((int64_t)n * (n - 1) / 2) + (int64_t)(b / m) * n;
     a %= m;
     b %= m;
-    const int64_t top = a * n + b;
+    const uint32_t top = a * n + b;
     if (top < m) break;
     n = top / m;
     b = top % m;
-    const int64_t t = a;
+    const uint32_t t = a;
     a = m;
     m = t;
   }
@@ -602,11 +603,13 @@ struct ManyRequest {
   }
   __device__ int tiles(int k) const { return tiles_upto((k + 1) * 2 * tt); }
   // key tiles of the pairs before pair k (the last pair's are not among them)
-  __device__ int64_t before(int64_t k) const {
-    const int64_t w = 2 * tt, ctx = (int64_t)kv - n;
-    int64_t z = ctx < 0 ? -ctx / w : 0;  // pairs whose tokens all see nothing
+  __device__ int64_t before(int k) const {
+    const int w = 2 * tt, ctx = kv - n;
+    int z = ctx < 0 ? -ctx / w : 0;  // pairs whose tokens all see nothing
     if (z > k) z = k;
-    return z + floor_sum(k - z, TR, w, ctx + (z + 1) * w + TR - 1);
+    // whole tiles of the shared part first: what is left stays below n + a few tiles
+    const int b = ctx + (z + 1) * w + TR - 1;
+    return z + (int64_t)(b / TR) * (k - z) + floor_sum((uint32_t)(k - z), TR, (uint32_t)w, (uint32_t)(b % TR));
   }
   __device__ int64_t total() const {
     const int p = pairs();
@@ -625,22 +628,36 @@ __device__ __forceinline__ ManyRequest many_request(const PagedAttn& A, int b) {
 }
 
 // One piece of a CTA's range: key tiles [j0, j1) of pair k of (request b, head h).
+//
+// The pairs of a head come folded - last, first, last but one, second, ... -
+// so that neighbours in the sequence add up to like amounts of work, and a
+// range boundary within kSnap tiles of a pair's edge is moved there: leaving a
+// part and joining it costs about as much as that many tiles.
+constexpr int kSnap = 4;
 struct ManyCursor {
   ManyRequest r;
-  int b, h, k, pairs;
+  int b, h, i, k, pairs;
   int j0, j1, nkv;  // nkv: the pair's key tiles
-  int64_t u, u1;    // the piece's first unit, the range's end
-  __device__ void set(const PagedAttn&) {
-    nkv = r.tiles(k);
-    const int64_t left = u1 - u;
-    j1 = nkv - j0 <= left ? nkv : j0 + (int)left;
+  int64_t u, u1;    // the piece's first unit, the range's end (before it is moved)
+  __device__ static int fold(int i, int pairs) { return i & 1 ? i >> 1 : pairs - 1 - (i >> 1); }
+  // where a boundary `off` tiles into a pair of n comes to lie
+  __device__ static int snap(int off, int n) {
+    const int rest = n - off;
+    return (off < rest ? off : rest) > kSnap ? off : off <= rest ? 0 : n;
   }
-  __device__ bool next(const PagedAttn& A) {
-    u += j1 - j0;
-    if (u >= u1) return false;
+  // enters position i of the folded pairs at tile j0 (unit u): false when the range ends before it
+  __device__ bool enter() {
+    k = fold(i, pairs);
+    nkv = r.tiles(k);
+    const int64_t end = u1 - (u - j0);
+    j1 = end >= nkv ? nkv : end > 0 ? snap((int)end, nkv) : 0;
+    return j1 > j0;
+  }
+  __device__ bool following(const PagedAttn& A) {
     j0 = 0;
-    if (++k == pairs) {
-      k = 0;
+    if (u >= u1) return false;
+    if (++i == pairs) {
+      i = 0;
       if (++h == A.c.kv_heads) {
         h = 0;
         do r = many_request(A, ++b);
@@ -648,8 +665,11 @@ struct ManyCursor {
         pairs = r.pairs();
       }
     }
-    set(A);
-    return true;
+    return enter();
+  }
+  __device__ bool next(const PagedAttn& A) {
+    u += j1 - j0;
+    return following(A);
   }
   __device__ int tok(int sl) const { return (2 * k + sl) * r.tt; }  // a slot's first token
   __device__ bool two() const { return tok(1) < r.n; }
@@ -672,6 +692,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void st_shared4(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // 16-bit minimum in a word of two (a rare path: emulated on the word)
 __device__ __forceinline__ void note_min(unsigned* word, int half, unsigned v) {
   unsigned old = *reinterpret_cast<volatile unsigned*>(word);
@@ -681,6 +710,13 @@ __device__ __forceinline__ void note_min(unsigned* word, int half, unsigned v) {
     if (seen == old) break;
     old = seen;
   }
+}
+
+// One lane of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // A position in the ring: slot, and the parity of the slot's phase.
@@ -863,6 +899,33 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (one || carry * A.c.kv_heads > cur.u) break;
     }
   }
+  __syncthreads();
+  cur.b = sh.b0;
+  cur.r = many_request(A, cur.b);
+  cur.pairs = cur.r.pairs();
+  {
+    int64_t off = cur.u - sh.before;
+    const int64_t per_head = cur.r.total();
+    cur.h = (int)(off / per_head);
+    off -= cur.h * per_head;
+    // tiles before position i of the folded pairs: those of the last (i + 1) / 2 and the first i / 2
+    const auto folded = [&](int i) {
+      return i == 0 ? (int64_t)0 : per_head - cur.r.before(cur.pairs - (i + 1) / 2) + cur.r.before(i / 2);
+    };
+    // the last position that begins at or before `off`: 32 candidates at a time, one a lane
+    int lo = 0, hi = cur.pairs;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+      const int n = __popc(__ballot_sync(0xffffffffu, i < hi && folded(i) <= off));  // one at least: lo itself
+      lo += (n - 1) * step;
+      hi = lo + step < hi ? lo + step : hi;
+    }
+    cur.i = lo;
+    const int into = (int)(off - folded(lo)), n = cur.r.tiles(ManyCursor::fold(lo, cur.pairs));
+    cur.j0 = into == 0 ? 0 : ManyCursor::snap(into, n);
+    cur.u += cur.j0 - into;
+    if (!(cur.j0 == n ? cur.following(A) : cur.enter())) return;
+  }
   if (threadIdx.x == 0) {
     for (int k = 0; k < 32; ++k) {
       // p_half, p_full, o_empty: one arrival per row warp of the slot; r_empty: the
@@ -887,25 +950,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *c.tmem_holder;
-  cur.b = sh.b0;
-  cur.r = many_request(A, cur.b);
-  cur.pairs = cur.r.pairs();
-  {
-    int64_t off = cur.u - sh.before;
-    const int64_t per_head = cur.r.total();
-    cur.h = (int)(off / per_head);
-    off -= cur.h * per_head;
-    int lo = 0, hi = cur.pairs;  // the last pair that begins at or before `off`
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cur.r.before(mid) <= off) lo = mid;
-      else hi = mid;
-    }
-    cur.k = lo;
-    cur.j0 = (int)(off - cur.r.before(lo));
-    cur.set(A);
-  }
-
   if (warp < 4) {
     // ---------------------------------------------------------- warpgroup 0
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyRegsLow));
@@ -958,94 +1002,116 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         for (uint32_t i = n > kManyRing ? n - kManyRing : 0; i < n; ++i)
           drain(r_full(i % kManyRing), (i / kManyRing) & 1);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      // This one thread keeps the tensor core fed, so what it does between
-      // products is kept short: descriptors by addition, ring slots by
-      // counting, and the next tiles' arrival looked at before the
-      // probabilities are waited for.
+      // The whole warp walks the loop and one elected lane issues: descriptors
+      // and addresses then live in uniform registers, which the tensor
+      // instructions take directly (from a lane's own registers every one of
+      // them is moved over first, and the products no longer follow each other
+      // without a pause).  What the loop needs of a piece is broadcast once.
       constexpr uint32_t id_s = idesc_bf16_f32(TR, TR, 0, 0);  // S = Q K^T
       constexpr uint32_t id_o = idesc_bf16_f32(TR, D, 0, 1);   // O += P V (P from TMEM, V MN-major)
       constexpr uint64_t kSlotStep = kTile >> 4;
-      const uint64_t q_desc = desc_kmajor(sQ(0), 0), k_desc = desc_kmajor(sR(0), 0), v_desc = desc_mnmajor(sR(0), 0);
+      const uint32_t ubase = __shfl_sync(0xffffffffu, c.base, 0), utmem = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t q_desc = desc_kmajor(ubase, 0), k_desc = desc_kmajor(ubase + 2 * kTile, 0),
+                     v_desc = desc_mnmajor(ubase + 2 * kTile, 0);
       RingPos pos;
       uint32_t ic = 0, vc = 0;  // vc: the next v_checked phase's parity, a bit per slot
       uint32_t pc[2] = {0, 0}, oc[2] = {0, 0};  // P V products issued, pieces finished, per slot
       bool ok = true;
+      auto commit = [&](uint32_t b) {
+        if (elect_one()) umma_commit(b);
+      };
       auto issue_s = [&](int sl, uint32_t kslot) -> bool {
         if (pc[sl] > 0 && !wait_on(p_empty(sl), (pc[sl] - 1) & 1, c, A.err)) return false;
         tc_fence_after();
         const uint64_t qd = q_desc + (uint64_t)sl * kSlotStep, kd = k_desc + kslot * kSlotStep;
-        const uint32_t st = tmem + (uint32_t)(sl * TR);
+        const uint32_t st = utmem + (uint32_t)(sl * TR);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t step = (uint64_t)((k >> 2) * (kChunk >> 4) + (k & 3) * 2);
-          umma_bf16(st, qd + step, kd + step, id_s, k > 0 ? 1u : 0u);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t step = (uint64_t)((k >> 2) * (kChunk >> 4) + (k & 3) * 2);
+            umma_bf16(st, qd + step, kd + step, id_s, k > 0 ? 1u : 0u);
+          }
+          umma_commit(s_full(sl));
         }
-        umma_commit(s_full(sl));
         return true;
       };
       auto issue_pv = [&](int sl, uint32_t vslot, bool first) -> bool {
-        if (!wait_on(p_half(sl), pc[sl] & 1, c, A.err)) return false;
-        if (first && !wait_on(o_empty(sl), (oc[sl] & 1) ^ 1, c, A.err)) return false;
-        tc_fence_after();
-        const uint32_t pt = tmem + (uint32_t)(sl * TR), ot = tmem + 256u + (uint32_t)(sl * D);
+        const uint32_t pt = utmem + (uint32_t)(sl * TR), ot = utmem + 256u + (uint32_t)(sl * D);
         const uint64_t vd = v_desc + vslot * kSlotStep;
+        if (first && !wait_on(o_empty(sl), (oc[sl] & 1) ^ 1, c, A.err)) return false;
 #pragma unroll
-        for (int k = 0; k < TR / 16; ++k) {
-          if (k == TR / 32) {
-            if (!wait_on(p_full(sl), pc[sl] & 1, c, A.err)) return false;
-            tc_fence_after();
+        for (int h = 0; h < 2; ++h) {
+          if (!wait_on(h ? p_full(sl) : p_half(sl), pc[sl] & 1, c, A.err)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = h * TR / 32; k < (h + 1) * TR / 32; ++k) {
+              const uint32_t hi = pt + (uint32_t)(32 * (k >> 1) + 8 * (k & 1));
+              umma_ts(ot, hi, vd + (uint64_t)(k * 128), id_o, k > 0 || !first ? 1u : 0u);
+              umma_ts(ot, hi + 16u, vd + (uint64_t)(k * 128), id_o, 1u);
+            }
+            if (h) umma_commit(p_empty(sl));
           }
-          const uint32_t hi = pt + (uint32_t)(32 * (k >> 1) + 8 * (k & 1));
-          umma_ts(ot, hi, vd + (uint64_t)(k * 128), id_o, k > 0 || !first ? 1u : 0u);
-          umma_ts(ot, hi + 16u, vd + (uint64_t)(k * 128), id_o, 1u);
         }
-        umma_commit(p_empty(sl));
         ++pc[sl];
         return true;
       };
       do {
-        const int cnt[2] = {cur.count(0), cur.count(1)};
-        const int nmax = cur.j1 - cur.j0;
+        const int cnt[2] = {__shfl_sync(0xffffffffu, cur.count(0), 0), __shfl_sync(0xffffffffu, cur.count(1), 0)};
+        const int nmax = __shfl_sync(0xffffffffu, cur.j1 - cur.j0, 0);
+        // the first key tile of the piece that some row does not see whole
+        const int seen = cur.r.kv - cur.r.n + cur.tok(0) + 1;
+        const int part0 = __shfl_sync(0xffffffffu, (seen > 0 ? seen / TR : 0) - cur.j0, 0);
+        // the value tile of key tile i of the piece, in and (where some row does not see it whole) checked
+        auto values = [&](int i, uint32_t& vs) -> bool {
+          vs = pos.slot;
+          if (!wait_on(r_full(vs), pos.phase, c, A.err)) return false;
+          pos.next();
+          if (i < part0) return true;
+          const uint32_t parity = (vc >> vs) & 1;
+          vc ^= 1u << vs;
+          return wait_on(v_checked(vs), parity, c, A.err);
+        };
         if (!(ok = wait_on(q_full, ic & 1, c, A.err) && wait_on(r_full(pos.slot), pos.phase, c, A.err))) break;
         ++ic;
-        uint32_t ks = pos.slot;
+        uint32_t ks = pos.slot, vs = 0, vn = 0;
         pos.next();
         if (!(ok = (cnt[0] == 0 || issue_s(0, ks)) && (cnt[1] == 0 || issue_s(1, ks)))) break;
-        if (nmax == 1) umma_commit(q_empty);
-        umma_commit(r_empty(ks));
-        for (int i = 0; i < nmax && ok; ++i) {
+        if (nmax == 1) commit(q_empty);
+        commit(r_empty(ks));
+        if (!(ok = values(0, vs))) break;
+        // P0 V, S0 of the next tile, P1 V, S1 of the next tile; a slot's next S
+        // waits for its P V (it overwrites P), and what else the next tile
+        // needs is waited for in the shadow of that
+        for (int i = 0; i < nmax; ++i) {
           const bool more = i + 1 < nmax;
-          const uint32_t vs = pos.slot;
-          if (!(ok = wait_on(r_full(vs), pos.phase, c, A.err))) break;
-          pos.next();
-          if (cur.partial(cur.j0 + i)) {
-            if (!(ok = wait_on(v_checked(vs), (vc >> vs) & 1, c, A.err))) break;
-            vc ^= 1u << vs;
-          }
+          if (i < cnt[0] && !(ok = issue_pv(0, vs, i == 0))) break;
           if (more) {
             ks = pos.slot;
             if (!(ok = wait_on(r_full(ks), pos.phase, c, A.err))) break;
             pos.next();
+            if (i + 1 < cnt[0] && !(ok = issue_s(0, ks))) break;
           }
-          for (int sl = 0; sl < 2 && ok; ++sl)
-            if (i < cnt[sl]) ok = issue_pv(sl, vs, i == 0) && (i + 1 >= cnt[sl] || issue_s(sl, ks));
-          if (!ok) break;
-          umma_commit(r_empty(vs));
+          if (i < cnt[1] && !(ok = issue_pv(1, vs, i == 0))) break;
+          commit(r_empty(vs));
           if (more) {
-            if (i + 2 == nmax) umma_commit(q_empty);  // the piece's last product with Q issued
-            umma_commit(r_empty(ks));
+            if (!(ok = values(i + 1, vn))) break;
+            if (i + 1 < cnt[1] && !(ok = issue_s(1, ks))) break;
+            commit(r_empty(ks));
+            if (i + 2 == nmax) commit(q_empty);  // the piece's last product with Q issued
+            vs = vn;
           }
         }
         if (!ok) break;
         for (int sl = 0; sl < 2; ++sl)
           if (cnt[sl] > 0) {
-            umma_commit(o_full(sl));
+            commit(o_full(sl));
             ++oc[sl];
           }
       } while (cur.next(A));
-      umma_commit(final_bar);
+      commit(final_bar);
       drain(final_bar, 0);
     } else if (warp >= 2) {
       // ------------------------------------------------------------ value check
@@ -1074,31 +1140,44 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             if (lane == 0) sh.noted[ic % kNotes][w] = 0;
             __syncwarp();
           }
-          uint8_t* const tile = c.base_ptr + (2 + slot) * kTile;
           const int k0 = j * TR, from = seen + 1 > k0 ? seen + 1 - k0 : 0;
-          for (int i = from * NV + lane; i < TR * NV; i += 32) {
-            const int key = i / NV, v = w * NV + (i - key * NV);
-            uint4* const p = reinterpret_cast<uint4*>(tile + (v >> 3) * kChunk + key * 128 + (((v & 7) ^ (key & 7)) << 4));
-            if (k0 + key >= cur.r.kv) {
-              *p = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 x = *p;
-            uint32_t* const e = reinterpret_cast<uint32_t*>(&x);
-            bool bad = false;
+          constexpr int RG = 32 / NV;  // rows per step of the warp
+          const int v = w * NV + (lane & (NV - 1)), row = lane / NV;
+          const uint32_t col = sR(slot) + (uint32_t)(v >> 3) * kChunk;
+          const auto at = [&](int key) { return col + (uint32_t)(key * 128 + (((v & 7) ^ (key & 7)) << 4)); };
+          // rows past the request: zero
+          const int end = cur.r.kv - k0 < TR ? cur.r.kv - k0 : TR;
+#pragma unroll 1
+          for (int key = (end > 0 ? end : 0) + row; key < TR; key += RG) st_shared4(at(key), make_uint4(0, 0, 0, 0));
+          // a bf16 is not finite when its exponent is all ones: adding one to it carries
+          unsigned bad = 0;
+#pragma unroll 4
+          for (int key = from + row; key < end; key += RG) {
+            const uint4 x = ld_shared4(at(key));
+            bad |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                   ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+          }
+          if (__any_sync(0xffffffffu, (bad & 0x80008000u) != 0)) {
+#pragma unroll 1
+            for (int key = from + row; key < end; key += RG) {
+              const uint4 x = ld_shared4(at(key));
+              uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t mask = 0x7f80u << (16 * (i & 1));
+                uint32_t word = e[0];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              bad |= (e[q] & 0x7f80u) == 0x7f80u || (e[q] & 0x7f800000u) == 0x7f800000u;
-            if (bad) {
-              for (int q = 0; q < 8; ++q) {
-                const int half = q & 1;
-                if (((e[q >> 1] >> (16 * half)) & 0x7f80u) != 0x7f80u) continue;
-                e[q >> 1] &= half ? 0x0000ffffu : 0xffff0000u;
-                note_min(notes + (v - w * NV) * 4 + (q >> 1), half, (unsigned)(k0 + key - seen < 0xfffe ? k0 + key - seen : 0xfffe));
+                for (int q = 1; q < 4; ++q) word = (i >> 1) == q ? e[q] : word;
+                if ((word & mask) != mask) continue;
+                word &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) e[q] = (i >> 1) == q ? word : e[q];
+                note_min(notes + (v - w * NV) * 4 + (i >> 1), i & 1,
+                         (unsigned)(k0 + key - seen < 0xfffe ? k0 + key - seen : 0xfffe));
               }
-              *p = x;
-              sh.noted[ic % kNotes][w] = 1;
+              st_shared4(at(key), make_uint4(e[0], e[1], e[2], e[3]));
             }
+            if (lane == 0) sh.noted[ic % kNotes][w] = 1;
           }
           fence_proxy_async_smem();  // the tensor core reads what was rewritten
           warp_arrive(v_checked(slot), lane);
@@ -1152,7 +1231,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const unsigned rel = (unsigned)(token - cur.tok(0));  // the row's last key - the pair's first row's
       const bool hurt = cnt > 0 && cur.partial(cur.j0 + cnt - 1) && (sh.noted[ic % kNotes][0] | sh.noted[ic % kNotes][1]) != 0;
       const auto spoil = [&](uint32_t (&ov)[32], int cc) {
-        if (!hurt) return;
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           if (((notes[(cc * 32 + e) >> 1] >> (16 * (e & 1))) & 0xffffu) <= rel) ov[e] = 0x7fffffffu;
@@ -1167,15 +1245,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       };
       if (whole) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        if (cnt > 0)
+        if (cnt > 0) {
+#pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t ov[32];
             tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
             tmem_ld_wait();
-            spoil(ov, cc);
+            if (hurt) spoil(ov, cc);
             if (live) store_row32(dst + cc * 32, ov, inv);
           }
-        if (cnt > 0) {
           tc_fence_before();
           warp_arrive(o_empty(sl), lane);
         }
@@ -1185,11 +1263,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         float* const part = parts + ((size_t)blockIdx.x * 2 + (cur.j0 == 0 ? 1 : 0)) * pf;
         const int prow = sl * TR + r;
         if (cnt > 0) {
+#pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t ov[32];
             tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
             tmem_ld_wait();
-            spoil(ov, cc);
+            if (hurt) spoil(ov, cc);
             if (live)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
@@ -1206,8 +1285,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         __threadfence();
         warp_arrive(part_full, lane);
         const Ranges ranges(units, gridDim.x);
+        // the CTAs whose boundaries lie inside the item and stay there, and the one before them
         const int64_t item0 = cur.u - cur.j0;
-        const int c0 = (int)ranges.owner(item0), pieces = (int)ranges.owner(item0 + cur.nkv - 1) - c0 + 1;
+        const int c0 = (int)ranges.owner(item0 + kSnap),
+                  pieces = (int)ranges.owner(item0 + cur.nkv - kSnap - 1) - c0 + 1;
         if (warp == 4 && lane == 0) {
           if ((ok = mbar_wait(part_full, xc & 1, c.abort_flag, A.err))) {
             __threadfence();
@@ -1226,29 +1307,41 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll 4
             for (int p = 0; p < pieces; ++p) top = fmaxf(top, __ldcg(at(p) + (size_t)2 * TR * D + prow));
             const float tb = top == -INFINITY ? 0.0f : top;
-            for (int cc = 0; cc < D / 32; ++cc) {
-              float acc[32];
+            // half of the row at a time, all its loads of a part in flight at once
+#pragma unroll 1
+            for (int hc = 0; hc < 2; ++hc) {
+              constexpr int H = D / 2;
+              float acc[H];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) acc[e] = 0.0f;
+              for (int e = 0; e < H; ++e) acc[e] = 0.0f;
               sum = 0.0f;
+#pragma unroll 1
               for (int p = 0; p < pieces; ++p) {
                 const float lp = __ldcg(at(p) + (size_t)2 * TR * (D + 1) + prow);
+                const float mp = __ldcg(at(p) + (size_t)2 * TR * D + prow);
+                float4 v[H / 4];
+#pragma unroll
+                for (int e = 0; e < H / 4; ++e)
+                  v[e] = __ldcg(reinterpret_cast<const float4*>(at(p)) + (size_t)(hc * (H / 4) + e) * (2 * TR) + prow);
                 if (lp == 0.0f) continue;  // no key of this row in the part, which may hold no O then
-                const float f = ex2_approx(__ldcg(at(p) + (size_t)2 * TR * D + prow) - tb);
+                const float f = ex2_approx(mp - tb);
                 sum += f * lp;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(at(p)) + (size_t)(cc * 8 + e) * (2 * TR) + prow);
-                  acc[4 * e] += f * v.x;
-                  acc[4 * e + 1] += f * v.y;
-                  acc[4 * e + 2] += f * v.z;
-                  acc[4 * e + 3] += f * v.w;
+                for (int e = 0; e < H / 4; ++e) {
+                  acc[4 * e] += f * v[e].x;
+                  acc[4 * e + 1] += f * v[e].y;
+                  acc[4 * e + 2] += f * v[e].z;
+                  acc[4 * e + 3] += f * v[e].w;
                 }
               }
-              uint32_t ov[32];
+              const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(acc[e]);
-              store_row32(dst + cc * 32, ov, sum == 0.0f ? 0.0f : 1.0f / sum);
+              for (int e = 0; e < H / 8; ++e)
+                *reinterpret_cast<uint4*>(dst + hc * H + e * 8) =
+                    make_uint4(pack_bf16(acc[8 * e] * inv, acc[8 * e + 1] * inv),
+                               pack_bf16(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
+                               pack_bf16(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
+                               pack_bf16(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
             }
             put_lse(top, sum);
           }
