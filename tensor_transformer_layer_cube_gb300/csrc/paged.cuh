@@ -15,6 +15,7 @@ struct PagedAttn {
   tp3d_kv_cache c;
   int32_t page_log2;
   int32_t requests, group;  // group: query heads per key/value head
+  int32_t few_rows;         // requests with up to this many rows per key/value head go to the kernel for few
   int64_t tokens;
   const int32_t *q_start, *kv_len, *table;
   int64_t width;  // block table columns
@@ -27,7 +28,7 @@ struct PagedAttn {
   int* err;
 };
 
-tp3d_status launch_paged_attn(tp3d_ctx* ctx, const PagedAttn& A, int max_new, void* workspace, cudaStream_t s);
+tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* workspace, cudaStream_t s);
 size_t paged_attn_workspace(const tp3d_ctx* ctx, int head_dim);
 
 #if defined(__CUDACC__)

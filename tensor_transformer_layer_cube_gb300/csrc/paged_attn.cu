@@ -99,6 +99,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Programmatic dependent launch: the kernel that follows may start its
+// prologue now / wait until the one before has finished.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The equal contiguous ranges of `units` units over `n` CTAs, and the CTA that unit u belongs to.
 struct Ranges {
   int64_t base, rem;
@@ -122,7 +127,7 @@ __device__ __forceinline__ int few_tiles(const PagedAttn& A, int b, PagedRequest
   *r = paged_request(A, b);
   const int64_t rows = (int64_t)r->n * A.group;
   if (rows == 0) return 0;
-  if (rows > kFewRows) {
+  if (rows > A.few_rows) {
     if (alone) raise_error(A.err, TP3D_EPAGES);
     return 0;
   }
@@ -160,6 +165,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
   const uint32_t stages = smem_u32(tiles_ptr);
   FewShared& sh = *reinterpret_cast<FewShared*>(tiles_ptr + kFewStages * kFewStageBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_launch_dependents();
 
   // ---- this CTA's range of the tile sequence
   int64_t units = 0, u0 = 0, u1 = 0;
@@ -621,7 +627,7 @@ __device__ __forceinline__ ManyRequest many_request(const PagedAttn& A, int b) {
   const PagedRequest r = paged_request(A, b);
   ManyRequest m;
   m.q0 = (int)r.q0;
-  m.n = (int64_t)r.n * A.group > kFewRows ? r.n : 0;  // the others are the kernel above's
+  m.n = (int64_t)r.n * A.group > A.few_rows ? r.n : 0;  // the others are the kernel above's
   m.kv = r.kv;
   m.tt = TR / A.group;
   return m;
@@ -886,7 +892,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const Ranges R(units, gridDim.x);
     cur.u = R.begin(blockIdx.x);
     cur.u1 = R.begin(blockIdx.x + 1);
-    if (cur.u >= cur.u1) return;
+    if (cur.u >= cur.u1) {
+      grid_wait();
+      return;
+    }
     const bool one = A.requests <= kManyThreads;
     carry = 0;
     for (int base = 0; base < A.requests; base += kManyThreads) {
@@ -924,8 +933,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const int into = (int)(off - folded(lo)), n = cur.r.tiles(ManyCursor::fold(lo, cur.pairs));
     cur.j0 = into == 0 ? 0 : ManyCursor::snap(into, n);
     cur.u += cur.j0 - into;
-    if (!(cur.j0 == n ? cur.following(A) : cur.enter())) return;
+    if (!(cur.j0 == n ? cur.following(A) : cur.enter())) {
+      grid_wait();
+      return;
+    }
   }
+  grid_wait();  // the kernel before shares the workspace
   if (threadIdx.x == 0) {
     for (int k = 0; k < 32; ++k) {
       // p_half, p_full, o_empty: one arrival per row warp of the slot; r_empty: the
@@ -1403,7 +1416,7 @@ tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool alone, void* work
 }
 
 template <int D>
-tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, void* workspace, cudaStream_t s) {
+tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, bool after, void* workspace, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   const int64_t qd[3] = {D, (int64_t)A.group * A.c.kv_heads, A.tokens}, qs[2] = {A.q_head, A.q_token};
   const uint32_t qb[3] = {64, (uint32_t)A.group, (uint32_t)(TR / A.group)};
@@ -1418,9 +1431,21 @@ tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, void* workspace, cuda
   cudaFuncAttributes fa;
   TP3D_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_attn_many_kernel<D>));
   if (fa.numRegs * kManyThreads < 128 * kManyRegsLow + 256 * kManyRegsHigh) return TP3D_EUNSUPPORTED;
-  paged_attn_many_kernel<D><<<ctx->num_sms, kManyThreads, kManySmem, s>>>(mq, mk, mv, A, static_cast<float*>(workspace),
-                                                                        ctx->d_paged);
-  return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
+  // launched while the kernel before still runs, to have its prologue behind it
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctx->num_sms);
+  cfg.blockDim = dim3(kManyThreads);
+  cfg.dynamicSmemBytes = kManySmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_attn_many_kernel<D>, mq, mk, mv, A, static_cast<float*>(workspace),
+                            ctx->d_paged) == cudaSuccess
+             ? TP3D_OK
+             : TP3D_ECUDA;
 }
 
 }  // namespace
@@ -1431,13 +1456,18 @@ size_t paged_attn_workspace(const tp3d_ctx* ctx, int d) {
   return (few > many ? few : many) * sizeof(float);
 }
 
-tp3d_status launch_paged_attn(tp3d_ctx* ctx, const PagedAttn& A, int max_new, void* workspace, cudaStream_t s) {
+tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* workspace, cudaStream_t s) {
   if (ctx->num_sms * kFewPerSm > kPagedCounters) return TP3D_EUNSUPPORTED;
   const int64_t most = (max_new > 0 && max_new < A.tokens ? max_new : A.tokens) * A.group;
+  A.few_rows = kFewRows;
   const bool alone = most <= kFewRows, d128 = A.c.head_dim == 128;
-  TP3D_TRY(d128 ? launch_few<128>(ctx, A, alone, workspace, s) : launch_few<64>(ctx, A, alone, workspace, s));
+  // One request that may have many rows goes to that kernel whatever it has
+  // (all its rows are computed there all the same, and a launch is saved).
+  const bool one = !alone && A.requests == 1;
+  if (one) A.few_rows = 0;
+  if (!one) TP3D_TRY(d128 ? launch_few<128>(ctx, A, alone, workspace, s) : launch_few<64>(ctx, A, alone, workspace, s));
   if (alone) return TP3D_OK;
-  return d128 ? launch_many<128>(ctx, A, workspace, s) : launch_many<64>(ctx, A, workspace, s);
+  return d128 ? launch_many<128>(ctx, A, !one, workspace, s) : launch_many<64>(ctx, A, !one, workspace, s);
 }
 
 }  // namespace tp3d
