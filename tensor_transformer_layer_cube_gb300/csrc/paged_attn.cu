@@ -46,6 +46,7 @@ constexpr int kFewRows = 64;
 constexpr int kFewStages = 3;
 constexpr int kFewPerSm = 2;
 constexpr uint32_t kFewStageBytes = 32768;  // a tile's keys, then its values
+constexpr int kJoinOnce = 16;  // parts of an item joined in one step
 constexpr float kMoveLog2 = 8.0f;
 
 template <int D>
@@ -495,33 +496,85 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         }
       }
       if (!whole) {
-        __threadfence();
-        __syncthreads();
-        // the count returns to zero with the item's last arrival
-        if (tid == 0) sh.last = atomicInc(counters + c0, (unsigned)pieces - 1) == (unsigned)pieces - 1;
-        __syncthreads();
-        if (sh.last) {
-          __threadfence();
-          for (int i = tid; i < elems; i += kFewThreads) {
-            const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
-            const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * pf; };
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll 4
-            for (int p = 0; p < pieces; ++p) top = fmaxf(top, __ldcg(at(p) + kFewRows * D + r));
-            const float tb = top == -INFINITY ? 0.0f : top;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int p = 0; p < pieces; ++p) {
-              const float f = ex2_approx(__ldcg(at(p) + kFewRows * D + r) - tb);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(at(p) + (size_t)r * D + col));
-              sum += f * __ldcg(at(p) + kFewRows * (D + 1) + r);
-              acc.x += f * v.x;
-              acc.y += f * v.y;
-              acc.z += f * v.z;
-              acc.w += f * v.w;
-            }
-            finish(r, col, acc, tb, sum);
+        const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * pf; };
+        // adds the parts first, first + step, .. (n of them) in that order: into O, or into the first one's place
+        const auto join = [&](int first, int step, int n, bool out) {
+          float* const wm = so;  // [part][row]: maximum, then weight
+          float* const wl = so + n * rows;
+          for (int i = tid; i < n * rows; i += kFewThreads) {
+            const float* x = at(first + i / rows * step) + kFewRows * D + i % rows;
+            wm[i] = __ldcg(x);
+            wl[i] = __ldcg(x + kFewRows);
           }
+          __syncthreads();
+          for (int r = tid; r < rows; r += kFewThreads) {
+            float top = -INFINITY, sum = 0.0f;
+            for (int i = 0; i < n; ++i) top = fmaxf(top, wm[i * rows + r]);
+            const float tb = top == -INFINITY ? 0.0f : top;
+            for (int i = 0; i < n; ++i) {
+              const float f = ex2_approx(wm[i * rows + r] - tb);
+              sum += f * wl[i * rows + r];
+              wm[i * rows + r] = f;
+            }
+            sh.m[r >> 4][r & 15] = top;
+            sh.l[r >> 4][r & 15] = sum;
+          }
+          __syncthreads();
+          for (int i0 = tid; i0 < elems; i0 += 4 * kFewThreads) {
+            float4 acc[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int e = i0 + q * kFewThreads;
+                if (e >= elems) break;
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(at(first + i * step)) + e);
+                const float f = wm[i * rows + e / (D / 4)];
+                acc[q].x += f * v.x;
+                acc[q].y += f * v.y;
+                acc[q].z += f * v.z;
+                acc[q].w += f * v.w;
+              }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int e = i0 + q * kFewThreads;
+              if (e >= elems) break;
+              const int r = e / (D / 4), col = (e - r * (D / 4)) * 4;
+              const float top = sh.m[r >> 4][r & 15], sum = sh.l[r >> 4][r & 15];
+              if (out) {
+                finish(r, col, acc[q], top == -INFINITY ? 0.0f : top, sum);
+              } else {
+                float* const to = at(first);
+                __stcg(reinterpret_cast<float4*>(to) + e, acc[q]);
+                if (col == 0) {
+                  __stcg(to + kFewRows * D + r, top);
+                  __stcg(to + kFewRows * (D + 1) + r, sum);
+                }
+              }
+            }
+          }
+        };
+        // this CTA's arrival is the last of n at the counter (which then is zero again)
+        const auto last_of = [&](unsigned* counter, int n) {
+          __threadfence();
+          __syncthreads();
+          if (tid == 0) sh.last = atomicInc(counter, (unsigned)n - 1) == (unsigned)n - 1;
+          __syncthreads();
+          const bool last = sh.last != 0;
+          if (last) __threadfence();
+          return last;
+        };
+        // Many parts are joined in two levels: groups of neighbours first, then
+        // the groups, so that one CTA never reads them all.
+        const int gsize = pieces <= kJoinOnce ? pieces : (int)ceilf(sqrtf((float)pieces));
+        const int groups = (pieces + gsize - 1) / gsize, g = ((int)blockIdx.x - c0) / gsize;
+        const int mine = pieces - g * gsize < gsize ? pieces - g * gsize : gsize;
+        // a CTA can be an item's first and another's later part: counters of their own
+        if (last_of(counters + (g == 0 ? 0 : gridDim.x) + c0 + g * gsize, mine)) {
+          join(g * gsize, 1, mine, groups == 1);
+          if (groups > 1 && last_of(counters + 2 * gridDim.x + c0, groups)) join(0, gsize, groups, true);
         }
       }
       begin = true;
@@ -1457,7 +1510,7 @@ size_t paged_attn_workspace(const tp3d_ctx* ctx, int d) {
 }
 
 tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* workspace, cudaStream_t s) {
-  if (ctx->num_sms * kFewPerSm > kPagedCounters) return TP3D_EUNSUPPORTED;
+  if (ctx->num_sms * kFewPerSm * 3 > kPagedCounters) return TP3D_EUNSUPPORTED;
   const int64_t most = (max_new > 0 && max_new < A.tokens ? max_new : A.tokens) * A.group;
   A.few_rows = kFewRows;
   const bool alone = most <= kFewRows, d128 = A.c.head_dim == 128;
