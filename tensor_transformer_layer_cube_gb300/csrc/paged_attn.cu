@@ -18,39 +18,40 @@ namespace {
 // ------------------------------------------------------------------ few rows
 // Requests with at most kFewRows rows (new tokens x query heads) per key/value
 // head: generation steps and short chunks.  Every row of a key/value head
-// shares one read of its keys and values, so with few rows the cache's bytes
-// bound the kernel: per key, 4 D bytes against 4 D rows FLOP, and HBM
-// delivers a key in about the time the legacy tensor instructions
-// (mma.sync, 16 rows x 8 keys x 16 columns) need a tenth of.
+// shares one read of its keys and values, so the cache's bytes bound the
+// kernel: per key, 4 D bytes against 4 D rows FLOP, which the legacy tensor
+// instructions (mma.sync, 16 rows x 8 keys x 16 columns) do several times
+// faster than HBM delivers them.
 //
-// Work is counted in tiles of KT keys of one (request, key/value head),
+// Work is counted in tiles of 64 keys of one (request, key/value head),
 // request by request, head by head; the CTAs take equal contiguous ranges of
 // that sequence, so one long request and many short ones balance alike and
-// nothing about the lengths is needed on the host.  A CTA streams its tiles
-// through a ring of shared-memory stages with 16-byte asynchronous copies
-// (any page layout; keys past the request are zero-filled, so stale contents
-// never reach a product).
-//
-// Four warps share a tile: with up to 16 rows each takes every fourth 16-key
-// chunk, with up to 32 every second one of half the rows, with up to 64 all
-// chunks of a quarter of them.  Each keeps its own running maximum (in base-2
+// nothing about the lengths is needed on the host.  Each of a CTA's four warps
+// takes 16 keys of every tile - one page holds them all - through a ring of
+// its own, with 16-byte asynchronous copies and no barrier between the warps:
+// a warp refills a stage as soon as it has read it, which keeps two of three
+// stages in flight (keys past the request are zero-filled, so stale contents
+// never reach a product).  Each keeps its own running maximum (in base-2
 // units; moved only when exceeded by more than 2^8, which leaves the
-// probabilities far from overflow), row sums and D columns of O in registers.
+// probabilities far from overflow), row sums and O in registers; they are
+// joined at the end of an item (request, head).
 //
-// Where a range boundary cuts an item (request, head), each CTA leaves its
-// part (maximum, sum, unnormalised O in fp32) in the workspace, and the CTA
-// whose arrival completes the item's count adds the parts in key order.
+// Where a range boundary cuts an item, each CTA leaves its part (maximum, sum,
+// unnormalised O in fp32) in the workspace, and the CTA whose arrival
+// completes the item's count adds the parts in key order.
+//
+// A short call spends most of its time on instructions fetched for the first
+// time, so what runs once is written as rolled loops, and loads are issued in
+// one place.
 constexpr int kFewThreads = 128;
 constexpr int kFewWarps = kFewThreads / 32;
-constexpr int kFewRows = 64;
-constexpr int kFewStages = 3;
+constexpr int kFewRows = 16;
+constexpr int kFewKeys = 64;  // keys of a tile
 constexpr int kFewPerSm = 2;
-constexpr uint32_t kFewStageBytes = 32768;  // a tile's keys, then its values
-constexpr int kJoinOnce = 16;  // parts of an item joined in one step
+constexpr int kFewStages = 3;
+constexpr int kFewMinTiles = 2;  // a CTA's range, where there is little work: parts cost more than a tile
+constexpr int kJoinOnce = 16;    // parts of an item joined in one step
 constexpr float kMoveLog2 = 8.0f;
-
-template <int D>
-TP3D_HD constexpr int few_tile_keys() { return (int)kFewStageBytes / (4 * D); }
 
 struct FewShared {
   float m[kFewWarps][16], l[kFewWarps][16];
@@ -59,12 +60,13 @@ struct FewShared {
   int b0;
   int last;
   int poisoned;
-  int poison[128];  // per column: the first key with a non-finite value in a partly masked tile
+  int poison[128];  // per column: the first key with a non-finite value that some row does not see
 };
 
-template <int D>
-constexpr size_t few_smem() { return (size_t)kFewStages * kFewStageBytes + sizeof(FewShared) + 128; }
-
+TP3D_HD constexpr uint32_t few_stage_bytes(int d) { return 16u * 4u * (uint32_t)d; }  // 16 keys, then 16 values
+constexpr size_t few_smem(int d) {
+  return (size_t)kFewWarps * kFewStages * few_stage_bytes(d) + sizeof(FewShared) + 128;
+}
 TP3D_HD constexpr size_t few_part_floats(int d) { return (size_t)kFewRows * (d + 2); }
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool in) {
@@ -99,6 +101,37 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint4 ld_shared4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void st_shared4(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// some of the eight bf16 of x are not finite: an exponent of all ones carries when one is added to it
+__device__ __forceinline__ unsigned not_finite(const uint4& x) {
+  return (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+          ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) & 0x80008000u;
+}
+// Sets the non-finite ones of the eight bf16 of x to zero; note(i) for each.
+template <class Note>
+__device__ __forceinline__ uint4 make_finite(const uint4& x, const Note& note) {
+  uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t mask = 0x7f80u << (16 * (i & 1));
+    uint32_t word = e[0];
+#pragma unroll
+    for (int q = 1; q < 4; ++q) word = (i >> 1) == q ? e[q] : word;
+    if ((word & mask) != mask) continue;
+    word &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) e[q] = (i >> 1) == q ? word : e[q];
+    note(i);
+  }
+  return make_uint4(e[0], e[1], e[2], e[3]);
+}
 
 // Programmatic dependent launch: the kernel that follows may start its
 // prologue now / wait until the one before has finished.
@@ -120,188 +153,178 @@ struct Ranges {
 struct FewCursor {
   int b, h, tile, tiles, n, kv;
   int64_t q0;
-};
-
-// tiles of request b (0: not this kernel's)
-template <int D>
-__device__ __forceinline__ int few_tiles(const PagedAttn& A, int b, PagedRequest* r, bool alone) {
-  *r = paged_request(A, b);
-  const int64_t rows = (int64_t)r->n * A.group;
-  if (rows == 0) return 0;
-  if (rows > A.few_rows) {
-    if (alone) raise_error(A.err, TP3D_EPAGES);
-    return 0;
+  // takes request b; tiles = 0 where it is not this kernel's
+  __device__ void enter(const PagedAttn& A, bool alone) {
+    const PagedRequest r = paged_request(A, b);
+    n = r.n;
+    kv = r.kv;
+    q0 = r.q0;
+    const int64_t rows = (int64_t)n * A.group;
+    tiles = kv > 0 ? (kv - 1) / kFewKeys + 1 : 1;  // a request without keys still has rows to write
+    if (rows == 0 || rows > A.few_rows) {
+      tiles = 0;
+      if (alone && rows) raise_error(A.err, TP3D_EPAGES);
+    }
   }
-  constexpr int KT = few_tile_keys<D>();
-  return r->kv > 0 ? (r->kv - 1) / KT + 1 : 1;  // a request without keys still has rows to write
-}
-
-template <int D>
-__device__ __forceinline__ void few_enter(const PagedAttn& A, FewCursor& c, bool alone) {
-  PagedRequest r;
-  c.tiles = few_tiles<D>(A, c.b, &r, alone);
-  c.n = r.n;
-  c.kv = r.kv;
-  c.q0 = r.q0;
-}
-template <int D>
-__device__ __forceinline__ void few_advance(const PagedAttn& A, FewCursor& c, bool alone) {
-  if (++c.tile < c.tiles) return;
-  c.tile = 0;
-  if (++c.h < A.c.kv_heads) return;
-  c.h = 0;
-  do {
-    ++c.b;
-    few_enter<D>(A, c, alone);
-  } while (c.tiles == 0);
-}
+  __device__ void advance(const PagedAttn& A, bool alone) {
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++h < A.c.kv_heads) return;
+    h = 0;
+    do {
+      ++b;
+      enter(A, alone);
+    } while (tiles == 0);
+  }
+};
 
 // `alone`: no other kernel of the call takes the requests with more rows
 template <int D>
 __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     paged_attn_few_kernel(const PagedAttn A, bool alone, float* __restrict__ parts, unsigned* __restrict__ counters) {
-  constexpr int KT = few_tile_keys<D>(), NG = KT / 16, RV = D / 8, NT = D / 8;  // RV: 16-byte vectors of a row
+  constexpr int RV = D / 8, NT = D / 8;  // 16-byte vectors of a row, 8-column tiles of O
+  constexpr uint32_t kStage = few_stage_bytes(D);
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* const tiles_ptr = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
-  const uint32_t stages = smem_u32(tiles_ptr);
-  FewShared& sh = *reinterpret_cast<FewShared*>(tiles_ptr + kFewStages * kFewStageBytes);
+  uint8_t* const ring_ptr = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+  FewShared& sh = *reinterpret_cast<FewShared*>(ring_ptr + kFewWarps * kFewStages * kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ring = smem_u32(ring_ptr) + (uint32_t)warp * kFewStages * kStage;  // this warp's stages
   grid_launch_dependents();
 
   // ---- this CTA's range of the tile sequence
+  FewCursor c;
   int64_t units = 0, u0 = 0, u1 = 0;
+  int ctas = 0;
   {
     // sums of the tiles over the requests, kFewThreads at a time; the second
-    // pass finds the request of the range's first tile
+    // round (only with more requests than that) finds the request of the
+    // range's first tile
     long long carry = 0;
-    auto chunk = [&](int base, long long& mine, int& tiles) {
-      PagedRequest r;
-      const int b = base + tid;
-      tiles = b < A.requests ? few_tiles<D>(A, b, &r, alone) : 0;
-      long long x = tiles;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) sh.scan[warp] = x;
-      __syncthreads();
-      mine = carry + x - tiles;
-#pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
-        if (w < warp) mine += sh.scan[w];
-        carry += sh.scan[w];
-      }
-    };
-    long long mine = 0;
-    int tiles = 0;
-    for (int base = 0; base < A.requests; base += kFewThreads) chunk(base, mine, tiles);
-    units = carry * A.c.kv_heads;
-    const Ranges R(units, gridDim.x);
-    u0 = R.begin(blockIdx.x);
-    u1 = R.begin(blockIdx.x + 1);
-    if (u0 >= u1) return;
     const bool one = A.requests <= kFewThreads;
-    carry = 0;
-    for (int base = 0; base < A.requests; base += kFewThreads) {
-      if (!one) chunk(base, mine, tiles);
-      const long long at = mine * A.c.kv_heads;
-      if (tiles > 0 && at <= u0 && u0 < at + (long long)tiles * A.c.kv_heads) {
-        sh.b0 = base + tid;
-        sh.before = at;
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+      carry = 0;
+#pragma unroll 1
+      for (int base = 0; base < A.requests; base += kFewThreads) {
+        c.b = base + tid;
+        c.tiles = 0;
+        if (c.b < A.requests) c.enter(A, alone);
+        long long x = c.tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) sh.scan[warp] = x;
+        __syncthreads();
+        long long at = carry + x - c.tiles;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+          if (w < warp) at += sh.scan[w];
+          carry += sh.scan[w];
+        }
+        if (one || round == 1) {
+          if (round == 0) {
+            units = carry * A.c.kv_heads;
+            const int64_t most = (units + kFewMinTiles - 1) / kFewMinTiles;
+            ctas = most < gridDim.x ? (int)most : (int)gridDim.x;
+            if (blockIdx.x >= ctas) return;
+            const Ranges R(units, ctas);
+            u0 = R.begin(blockIdx.x);
+            u1 = R.begin(blockIdx.x + 1);
+          }
+          at *= A.c.kv_heads;
+          if (c.tiles > 0 && at <= u0 && u0 < at + (long long)c.tiles * A.c.kv_heads) {
+            sh.b0 = c.b;
+            sh.before = at;
+          }
+          if (carry * A.c.kv_heads > u0) break;
+        }
       }
-      if (one || carry * A.c.kv_heads > u0) break;
+      if (one) break;
+      if (round == 0) {
+        units = carry * A.c.kv_heads;
+        const int64_t most = (units + kFewMinTiles - 1) / kFewMinTiles;
+        ctas = most < gridDim.x ? (int)most : (int)gridDim.x;
+        if (blockIdx.x >= ctas) return;
+        const Ranges R(units, ctas);
+        u0 = R.begin(blockIdx.x);
+        u1 = R.begin(blockIdx.x + 1);
+      }
     }
-    for (int i = tid; i < 128; i += kFewThreads) sh.poison[i] = INT32_MAX;
+    sh.poison[tid] = INT32_MAX;
     if (tid == 0) sh.poisoned = 0;
     __syncthreads();
-  }
-  const Ranges ranges(units, gridDim.x);
-  FewCursor c;
-  c.b = sh.b0;
-  few_enter<D>(A, c, alone);
-  {
+    c.b = sh.b0;
+    c.enter(A, alone);
     const int64_t off = u0 - sh.before;
     c.h = (int)(off / c.tiles);
     c.tile = (int)(off - (int64_t)c.h * c.tiles);
-  }
-
-  // ---- loads: thread -> vector (tid % RV) of rows tid / RV + i * (kFewThreads / RV)
-  const bf16* const kpool = static_cast<const bf16*>(A.c.k);
-  const bf16* const vpool = static_cast<const bf16*>(A.c.v);
-  FewCursor ld = c;
-  int64_t lu = u0;  // the unit that ld stands at
-  int32_t ld_page = 0;  // the page of 16-key group (lane % NG) of that tile; -1: none
-  auto fetch_pages = [&]() {
-    const int64_t key = (int64_t)ld.tile * KT + (lane & (NG - 1)) * 16;
-    ld_page = -1;
-    if (key < ld.kv) {
-      ld_page = __ldg(A.table + (int64_t)ld.b * A.width + (key >> A.page_log2));
-      if (ld_page < 0 || ld_page >= A.c.pages) {
-        raise_error(A.err, TP3D_EPAGES);
-        ld_page = -1;
-      }
-    }
-  };
-  auto load = [&](int stage) {
-    constexpr int RS = kFewThreads / RV;  // rows per step: 8 or 16
-    const int v = tid & (RV - 1), r0 = tid / RV;
-    const uint32_t base = stages + (uint32_t)stage * kFewStageBytes;
-#pragma unroll
-    for (int i = 0; i < KT / RS; ++i) {
-      const int r = r0 + i * RS;
-      const int32_t page = __shfl_sync(0xffffffffu, ld_page, (i * RS) >> 4);  // 16 rows share a page
-      const int64_t key = (int64_t)ld.tile * KT + r;
-      const bool in = page >= 0 && key < ld.kv;
-      const int64_t at = in ? (int64_t)page * A.c.page_stride + (key & (A.c.page - 1)) * A.c.token_stride +
-                                  ld.h * A.c.head_stride + v * 8
-                            : 0;
-      // vector v of row r at v ^ (r mod 8): the eight rows of an 8 x 8 block fall in different banks
-      const uint32_t dst = base + (uint32_t)(r * RV + (v ^ (r & 7))) * 16u;
-      cp_async16_zfill(dst, kpool + at, in);
-      cp_async16_zfill(dst + kFewStageBytes / 2, vpool + at, in);
-    }
-  };
-  fetch_pages();
-  for (int s = 0; s < kFewStages - 1; ++s) {
-    if (lu < u1) {
-      load(s);
-      if (++lu < u1) {
-        few_advance<D>(A, ld, alone);
-        fetch_pages();
-      }
-    }
-    cp_commit();
   }
 
   const float sl2 = A.scale * kLog2e;
   uint32_t qf[D / 16][4];
   float o[NT][4], m[2], l[2];
   int lim[2];  // the last key that this thread's two rows see
-  int WM = 1, stage = 0;
-  bool begin = true;
-  for (int64_t u = u0; u < u1; ++u) {
-    cp_wait<kFewStages - 2>();
-    __syncthreads();  // the tile of unit u is in; everybody is done with unit u - 1's
-    {
-      const int s = stage == 0 ? kFewStages - 1 : stage - 1;
-      if (lu < u1) {
-        load(s);
-        if (++lu < u1) {
-          few_advance<D>(A, ld, alone);
-          fetch_pages();
+  FewCursor ld = c;
+  int64_t lu = u0, u = u0;  // the units to load and to compute next
+  int32_t page = -1;        // of this warp's 16 keys of unit lu
+  bool begin = true, fetch = true;
+  int stage = 0;            // to load into; the next one is the oldest
+#pragma unroll 1
+  for (int step = 0;; ++step) {
+    // ---- load unit lu, whose page was looked up a step ago
+    if (fetch && step == 0) {
+      const int key = ld.tile * kFewKeys + warp * 16;
+      if (key < ld.kv) page = __ldg(A.table + (int64_t)ld.b * A.width + (key >> A.page_log2));
+    }
+    if (fetch) {
+      const int key = ld.tile * kFewKeys + warp * 16, left = ld.kv - key;
+      if (left > 0) {
+        const bool in = page >= 0 && page < A.c.pages;
+        if (!in) raise_error(A.err, TP3D_EPAGES);
+        // lane -> vector (lane % RV) of rows lane / RV + i * (32 / RV); vector v of row r lies at
+        // v ^ (r mod 8), so that the eight rows of an 8 x 8 block fall in different banks
+        const int v = lane & (RV - 1), r0 = lane / RV;
+        const int64_t at = in ? (int64_t)page * A.c.page_stride + (int64_t)((key & (A.c.page - 1)) + r0) * A.c.token_stride +
+                                    ld.h * A.c.head_stride + v * 8
+                              : 0;
+        const bf16* ks = static_cast<const bf16*>(A.c.k) + at;
+        const bf16* vs = static_cast<const bf16*>(A.c.v) + at;
+        const int64_t hop = in ? (int64_t)(32 / RV) * A.c.token_stride : 0;
+        const uint32_t dst = ring + (uint32_t)stage * kStage;
+#pragma unroll
+        for (int i = 0; i < RV / 2; ++i) {
+          const int r = r0 + i * (32 / RV);
+          const uint32_t to = dst + (uint32_t)(r * RV + (v ^ (r & 7))) * 16u;
+          const bool have = in && r < left;
+          cp_async16_zfill(to, have ? ks : static_cast<const bf16*>(A.c.k), have);
+          cp_async16_zfill(to + kStage / 2, have ? vs : static_cast<const bf16*>(A.c.v), have);
+          ks += hop;
+          vs += hop;
         }
       }
-      cp_commit();
+      fetch = ++lu < u1;
+      if (fetch) {
+        ld.advance(A, alone);
+        const int next = ld.tile * kFewKeys + warp * 16;
+        page = next < ld.kv ? __ldg(A.table + (int64_t)ld.b * A.width + (next >> A.page_log2)) : -1;
+      }
     }
+    cp_commit();
+    stage = stage == kFewStages - 1 ? 0 : stage + 1;
+    if (step < kFewStages - 1) continue;
+
+    // ---- compute unit u, in the oldest stage
+    cp_wait<kFewStages - 1>();
+    __syncwarp();
     const int rows = c.n * A.group;
     if (begin) {
-      WM = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
       begin = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = (warp & (WM - 1)) * 16 + (lane >> 2) + 8 * e;
+        const int r = (lane >> 2) + 8 * e;
         const bool in = r < rows;
         const int tok = in ? r / A.group : 0, g = in ? r - tok * A.group : 0;
         lim[e] = in ? c.kv - c.n + tok : c.kv - 1;
@@ -319,13 +342,26 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
     }
-    const int WK = kFewWarps / WM;
-    const uint32_t sk = stages + (uint32_t)stage * kFewStageBytes, sv = sk + kFewStageBytes / 2;
-    // keys of this tile that some row does not see: past kv - n (kv when n = 1)
-    const bool partial = (int64_t)(c.tile + 1) * KT - 1 > (int64_t)c.kv - c.n;
-    for (int kc = warp / WM; kc < NG; kc += WK) {
-      const int key0 = c.tile * KT + kc * 16;
-      if (key0 >= c.kv) break;
+    const uint32_t sk = ring + (uint32_t)stage * kStage, sv = sk + kStage / 2;
+    const int key0 = c.tile * kFewKeys + warp * 16;
+    if (key0 < c.kv) {
+      // keys that some row does not see: past kv - n
+      const bool partial = key0 + 15 > c.kv - c.n;
+      if (partial && c.n > 1) {
+        // A probability of 0 does not silence a value that is not finite: such
+        // a value becomes 0, and rows that see its key get NaN in its column
+        // at the end.
+#pragma unroll 1
+        for (int i = lane; i < 16 * RV; i += 32) {
+          const int r = i / RV, v = i & (RV - 1);
+          const uint32_t at = sv + (uint32_t)(r * RV + (v ^ (r & 7))) * 16u;
+          const uint4 x = ld_shared4(at);
+          if (key0 + r <= c.kv - c.n || !not_finite(x)) continue;
+          st_shared4(at, make_finite(x, [&](int e) { atomicMin(&sh.poison[v * 8 + e], key0 + r); }));
+          sh.poisoned = 1;
+        }
+        __syncwarp();
+      }
       // S = Q K^T for 16 keys: two 8-key tiles, two partial sums each
       float s[2][2][4];
 #pragma unroll
@@ -335,7 +371,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[x][y][e] = 0.0f;
       {
-        const int row = kc * 16 + (lane & 7) + ((lane >> 4) << 3);
+        const int row = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const int vec = 2 * k + ((lane >> 3) & 1);
@@ -345,7 +381,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
           mma16816(s[1][k & 1], qf[k], kb[2], kb[3]);
         }
       }
-      float mx[2] = {-INFINITY, -INFINITY};
+      float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -353,15 +389,13 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
           float v = s[x][0][e] + s[x][1][e];
           if (partial && key0 + x * 8 + (lane & 3) * 2 + (e & 1) > lim[e >> 1]) v = -INFINITY;
           s[x][0][e] = v;
-          mx[e >> 1] = fmaxf(mx[e >> 1], v);
+          mt[e >> 1] = fmaxf(mt[e >> 1], v);
         }
       bool move = false;
-      float mt[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-        mt[e] = mx[e] * sl2;
+        mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], 1));
+        mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], 2)) * sl2;
         move |= mt[e] > m[e] + kMoveLog2;
       }
       if (__any_sync(0xffffffffu, move)) {
@@ -397,27 +431,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         ph[i] = pack_bf16(x, y);
         pl[i] = pack_bf16(x - __uint_as_float(ph[i] << 16), y - __uint_as_float(ph[i] & 0xffff0000u));
       }
-      const int row = kc * 16 + (lane & 15);
+      const int row = lane & 15;
 #pragma unroll
       for (int j = 0; j < NT; j += 2) {
         const int vec = j + (lane >> 4);
         uint32_t vb[4];
         ldmatrix4_trans(vb, sv + (uint32_t)(row * RV + (vec ^ (row & 7))) * 16u);
-        if (partial && c.n > 1) {
-          // A probability of 0 does not silence a value that is not finite:
-          // such a value becomes 0 here, and rows that see its key get NaN in
-          // its column at the end.
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (((vb[x] >> (16 * e)) & 0x7f80u) == 0x7f80u) {
-                vb[x] &= e ? 0x0000ffffu : 0xffff0000u;
-                atomicMin(&sh.poison[(j + (x >> 1)) * 8 + (lane >> 2)],
-                          key0 + (x & 1) * 8 + (lane & 3) * 2 + e);
-                sh.poisoned = 1;
-              }
-        }
         mma16816(o[j], ph, vb[0], vb[1]);
         mma16816(o[j + 1], ph, vb[2], vb[3]);
         mma16816(o[j], pl, vb[0], vb[1]);
@@ -426,12 +445,14 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     }
 
     // ---- the item's last tile, or this CTA's: join the warps and write
-    if (c.tile + 1 == c.tiles || u + 1 == u1) {
+    const bool done = u + 1 == u1;
+    if (c.tile + 1 == c.tiles || done) {
       const int64_t item0 = u - c.tile;  // the item's first unit
       const bool whole = item0 >= u0 && c.tile + 1 == c.tiles;
-      __syncthreads();  // every warp is done with the tile: its stage takes the parts
-      float* const so = reinterpret_cast<float*>(tiles_ptr + (size_t)stage * kFewStageBytes);  // [warp][16][D]
-      const auto swz = [](int r, int col) { return r * D + (col ^ ((r & 3) << 3)); };
+      // the stage just read takes the warp's O: [row][D], column ^ (row mod 4) * 8 against bank conflicts
+      float* const so = reinterpret_cast<float*>(ring_ptr + (size_t)(warp * kFewStages + stage) * kStage);
+      __syncthreads();  // (also: every warp's notes are in)
+      const bool hurt = sh.poisoned != 0;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -441,24 +462,20 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
           sh.m[warp][r] = m[e];
           sh.l[warp][r] = l[e];
         }
-        const bool hurt = sh.poisoned != 0;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const int col = j * 8 + (lane & 3) * 2;
-          float2 v = make_float2(o[j][2 * e], o[j][2 * e + 1]);
-          if (hurt) {
-            if (sh.poison[col] <= lim[e]) v.x = __int_as_float(0x7fffffff);
-            if (sh.poison[col + 1] <= lim[e]) v.y = __int_as_float(0x7fffffff);
-          }
-          *reinterpret_cast<float2*>(so + warp * 16 * D + swz(r, col)) = v;
+          *reinterpret_cast<float2*>(so + r * D + (col ^ ((r & 3) << 3))) = make_float2(o[j][2 * e], o[j][2 * e + 1]);
         }
       }
       __syncthreads();
+      const Ranges ranges(units, ctas);
       const int c0 = whole ? 0 : (int)ranges.owner(item0);
       const int pieces = whole ? 1 : (int)ranges.owner(item0 + c.tiles - 1) - c0 + 1;
       const size_t pf = few_part_floats(D);
-      // a part that begins its item is its CTA's last piece, slot 1; one that continues it the first, slot 0
-      float* const part = parts + ((size_t)blockIdx.x * 2 + (item0 >= u0 ? 1 : 0)) * pf;
+      // the part of the item's p-th CTA: an item begins in its CTA's last piece (slot 1), goes on in the
+      // next one's first (slot 0)
+      const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * pf; };
       const auto finish = [&](int r, int col, float4 v, float top, float sum) {
         const int tok = r / A.group;
         const int64_t t = c.q0 + tok;
@@ -467,127 +484,122 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         *reinterpret_cast<uint2*>(A.o + t * A.o_token + (int64_t)head * A.o_head + col) =
             make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
         if (A.lse && col == 0)
-          A.lse[t * (int64_t)(A.group * A.c.kv_heads) + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+          A.lse[t * (int64_t)(A.group * A.c.kv_heads) + head] =
+              sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * kLn2;
+      };
+      const auto leave = [&](float* to, int r, int col, float4 v, float top, float sum) {
+        __stcg(reinterpret_cast<float4*>(to + (size_t)r * D + col), v);
+        if (col == 0) {
+          __stcg(to + kFewRows * D + r, top);
+          __stcg(to + kFewRows * (D + 1) + r, sum);
+        }
       };
       const int elems = rows * (D / 4);
+#pragma unroll 1
       for (int i = tid; i < elems; i += kFewThreads) {
-        const int r = i / (D / 4), col = (i - r * (D / 4)) * 4, rt = r >> 4, rr = r & 15;
+        const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
         float top = -INFINITY, sum = 0.0f;
-        for (int w = rt; w < kFewWarps; w += WM) top = fmaxf(top, sh.m[w][rr]);
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, sh.m[w][r]);
         const float tb = top == -INFINITY ? 0.0f : top;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int w = rt; w < kFewWarps; w += WM) {
-          const float f = ex2_approx(sh.m[w][rr] - tb);
-          const float4 v = *reinterpret_cast<const float4*>(so + w * 16 * D + swz(rr, col));
-          sum += f * sh.l[w][rr];
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+          const float f = ex2_approx(sh.m[w][r] - tb);
+          const float4 v = *reinterpret_cast<const float4*>(so + (w - warp) * (int)(kFewStages * kStage / 4) + r * D +
+                                                           (col ^ ((r & 3) << 3)));
+          sum += f * sh.l[w][r];
           acc.x += f * v.x;
           acc.y += f * v.y;
           acc.z += f * v.z;
           acc.w += f * v.w;
         }
-        if (whole) {
-          finish(r, col, acc, tb, sum);
-        } else {
-          __stcg(reinterpret_cast<float4*>(part + (size_t)r * D + col), acc);
-          if (col == 0) {
-            __stcg(part + kFewRows * D + r, top);
-            __stcg(part + kFewRows * (D + 1) + r, sum);
-          }
+        if (hurt) {
+          const int lr = c.kv - c.n + r / A.group;
+          float* const x = reinterpret_cast<float*>(&acc);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (sh.poison[col + e] <= lr) x[e] = __int_as_float(0x7fffffff);
         }
+        if (whole) finish(r, col, acc, top, sum);
+        else leave(at((int)blockIdx.x - c0), r, col, acc, top, sum);
       }
       if (!whole) {
-        const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * pf; };
-        // adds the parts first, first + step, .. (n of them) in that order: into O, or into the first one's place
-        const auto join = [&](int first, int step, int n, bool out) {
-          float* const wm = so;  // [part][row]: maximum, then weight
-          float* const wl = so + n * rows;
-          for (int i = tid; i < n * rows; i += kFewThreads) {
-            const float* x = at(first + i / rows * step) + kFewRows * D + i % rows;
-            wm[i] = __ldcg(x);
-            wl[i] = __ldcg(x + kFewRows);
-          }
-          __syncthreads();
-          for (int r = tid; r < rows; r += kFewThreads) {
-            float top = -INFINITY, sum = 0.0f;
-            for (int i = 0; i < n; ++i) top = fmaxf(top, wm[i * rows + r]);
-            const float tb = top == -INFINITY ? 0.0f : top;
-            for (int i = 0; i < n; ++i) {
-              const float f = ex2_approx(wm[i * rows + r] - tb);
-              sum += f * wl[i * rows + r];
-              wm[i * rows + r] = f;
-            }
-            sh.m[r >> 4][r & 15] = top;
-            sh.l[r >> 4][r & 15] = sum;
-          }
-          __syncthreads();
-          for (int i0 = tid; i0 < elems; i0 += 4 * kFewThreads) {
-            float4 acc[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int i = 0; i < n; ++i)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int e = i0 + q * kFewThreads;
-                if (e >= elems) break;
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(at(first + i * step)) + e);
-                const float f = wm[i * rows + e / (D / 4)];
-                acc[q].x += f * v.x;
-                acc[q].y += f * v.y;
-                acc[q].z += f * v.z;
-                acc[q].w += f * v.w;
-              }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int e = i0 + q * kFewThreads;
-              if (e >= elems) break;
-              const int r = e / (D / 4), col = (e - r * (D / 4)) * 4;
-              const float top = sh.m[r >> 4][r & 15], sum = sh.l[r >> 4][r & 15];
-              if (out) {
-                finish(r, col, acc[q], top == -INFINITY ? 0.0f : top, sum);
-              } else {
-                float* const to = at(first);
-                __stcg(reinterpret_cast<float4*>(to) + e, acc[q]);
-                if (col == 0) {
-                  __stcg(to + kFewRows * D + r, top);
-                  __stcg(to + kFewRows * (D + 1) + r, sum);
-                }
-              }
-            }
-          }
-        };
-        // this CTA's arrival is the last of n at the counter (which then is zero again)
-        const auto last_of = [&](unsigned* counter, int n) {
+        // Adds parts in order.  Many are joined in two levels: groups of
+        // neighbours first, then the groups, so that one CTA never reads them
+        // all.  A CTA's arrival may be the last at its group's counter, then
+        // at the item's (which so return to zero); one CTA can be an item's
+        // first and another's later part: counters of their own.
+        const int gsize = pieces <= kJoinOnce ? pieces : (int)ceilf(sqrtf((float)pieces));
+        const int groups = (pieces + gsize - 1) / gsize, g = ((int)blockIdx.x - c0) / gsize;
+        unsigned* counter = counters + (g == 0 ? 0 : gridDim.x) + c0 + g * gsize;
+        int first = g * gsize, by = 1, n = pieces - first < gsize ? pieces - first : gsize;
+#pragma unroll 1
+        for (int level = groups == 1 ? 1 : 0; level < 2; ++level) {
           __threadfence();
           __syncthreads();
           if (tid == 0) sh.last = atomicInc(counter, (unsigned)n - 1) == (unsigned)n - 1;
           __syncthreads();
-          const bool last = sh.last != 0;
-          if (last) __threadfence();
-          return last;
-        };
-        // Many parts are joined in two levels: groups of neighbours first, then
-        // the groups, so that one CTA never reads them all.
-        const int gsize = pieces <= kJoinOnce ? pieces : (int)ceilf(sqrtf((float)pieces));
-        const int groups = (pieces + gsize - 1) / gsize, g = ((int)blockIdx.x - c0) / gsize;
-        const int mine = pieces - g * gsize < gsize ? pieces - g * gsize : gsize;
-        // a CTA can be an item's first and another's later part: counters of their own
-        if (last_of(counters + (g == 0 ? 0 : gridDim.x) + c0 + g * gsize, mine)) {
-          join(g * gsize, 1, mine, groups == 1);
-          if (groups > 1 && last_of(counters + 2 * gridDim.x + c0, groups)) join(0, gsize, groups, true);
+          if (!sh.last) break;
+          __threadfence();
+          // the parts' maxima and sums, then each part's weight, in this CTA's read stages
+          float* const wm = reinterpret_cast<float*>(ring_ptr + (size_t)stage * kStage);
+          float* const wl = wm + kFewStages * kStage / 4;  // the next warp's stage
+          for (int i = tid; i < n * rows; i += kFewThreads) {
+            const float* x = at(first + i / rows * by) + kFewRows * D + i % rows;
+            wm[i] = __ldcg(x);
+            wl[i] = __ldcg(x + kFewRows);
+          }
+          __syncthreads();
+          if (tid < rows) {
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) top = fmaxf(top, wm[i * rows + tid]);
+            const float tb = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+              const float f = ex2_approx(wm[i * rows + tid] - tb);
+              sum += f * wl[i * rows + tid];
+              wm[i * rows + tid] = f;
+            }
+            sh.m[0][tid] = top;
+            sh.l[0][tid] = sum;
+          }
+          __syncthreads();
+#pragma unroll 1
+          for (int e = tid; e < elems; e += kFewThreads) {
+            const int r = e / (D / 4), col = (e - r * (D / 4)) * 4;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(at(first + i * by)) + e);
+              const float f = wm[i * rows + r];
+              acc.x += f * v.x;
+              acc.y += f * v.y;
+              acc.z += f * v.z;
+              acc.w += f * v.w;
+            }
+            if (level == 1) finish(r, col, acc, sh.m[0][r], sh.l[0][r]);
+            else leave(at(first), r, col, acc, sh.m[0][r], sh.l[0][r]);
+          }
+          counter = counters + 2 * gridDim.x + c0;
+          first = 0;
+          by = gsize;
+          n = groups;
         }
       }
+      if (done) break;
       begin = true;
-      if (sh.poisoned) {
-        __syncthreads();
-        for (int i = tid; i < 128; i += kFewThreads) sh.poison[i] = INT32_MAX;
+      __syncthreads();  // the stages go back to the loads
+      if (hurt) {
+        sh.poison[tid] = INT32_MAX;
         if (tid == 0) sh.poisoned = 0;
+        __syncthreads();
       }
     }
-    if (u + 1 < u1) few_advance<D>(A, c, alone);
-    stage = stage == kFewStages - 1 ? 0 : stage + 1;
+    ++u;
+    c.advance(A, alone);
   }
-  cp_wait<0>();
 }
 
 // ------------------------------------------------------------------ many rows
@@ -749,15 +761,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
-}
-
-__device__ __forceinline__ uint4 ld_shared4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void st_shared4(uint32_t a, const uint4& v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // 16-bit minimum in a word of two (a rare path: emulated on the word)
@@ -1215,33 +1218,16 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const int end = cur.r.kv - k0 < TR ? cur.r.kv - k0 : TR;
 #pragma unroll 1
           for (int key = (end > 0 ? end : 0) + row; key < TR; key += RG) st_shared4(at(key), make_uint4(0, 0, 0, 0));
-          // a bf16 is not finite when its exponent is all ones: adding one to it carries
           unsigned bad = 0;
 #pragma unroll 4
-          for (int key = from + row; key < end; key += RG) {
-            const uint4 x = ld_shared4(at(key));
-            bad |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                   ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
-          }
-          if (__any_sync(0xffffffffu, (bad & 0x80008000u) != 0)) {
+          for (int key = from + row; key < end; key += RG) bad |= not_finite(ld_shared4(at(key)));
+          if (__any_sync(0xffffffffu, bad != 0)) {
 #pragma unroll 1
             for (int key = from + row; key < end; key += RG) {
-              const uint4 x = ld_shared4(at(key));
-              uint32_t e[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll 1
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t mask = 0x7f80u << (16 * (i & 1));
-                uint32_t word = e[0];
-#pragma unroll
-                for (int q = 1; q < 4; ++q) word = (i >> 1) == q ? e[q] : word;
-                if ((word & mask) != mask) continue;
-                word &= i & 1 ? 0x0000ffffu : 0xffff0000u;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) e[q] = (i >> 1) == q ? word : e[q];
-                note_min(notes + (v - w * NV) * 4 + (i >> 1), i & 1,
-                         (unsigned)(k0 + key - seen < 0xfffe ? k0 + key - seen : 0xfffe));
-              }
-              st_shared4(at(key), make_uint4(e[0], e[1], e[2], e[3]));
+              const unsigned rel = (unsigned)(k0 + key - seen < 0xfffe ? k0 + key - seen : 0xfffe);
+              st_shared4(at(key), make_finite(ld_shared4(at(key)), [&](int i) {
+                           note_min(notes + (v - w * NV) * 4 + (i >> 1), i & 1, rel);
+                         }));
             }
             if (lane == 0) sh.noted[ic % kNotes][w] = 1;
           }
@@ -1462,8 +1448,8 @@ tp3d_status row_map(CUtensorMap* m, const void* ptr, int rank, const int64_t* di
 template <int D>
 tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool alone, void* workspace, cudaStream_t s) {
   TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)few_smem<D>()));
-  paged_attn_few_kernel<D><<<ctx->num_sms * kFewPerSm, kFewThreads, few_smem<D>(), s>>>(
+                                     (int)few_smem(D)));
+  paged_attn_few_kernel<D><<<ctx->num_sms * kFewPerSm, kFewThreads, few_smem(D), s>>>(
       A, alone, static_cast<float*>(workspace), ctx->d_paged);
   return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
 }
