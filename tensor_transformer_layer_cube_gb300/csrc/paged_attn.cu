@@ -49,14 +49,15 @@ constexpr int kFewRows = 16;
 constexpr int kFewKeys = 64;  // keys of a tile
 constexpr int kFewPerSm = 2;
 constexpr int kFewStages = 3;
-constexpr int kFewMinTiles = 2;  // a CTA's range, where there is little work: parts cost more than a tile
+constexpr int kFewMinTiles = 4;  // a CTA's range, where there is little work
+constexpr int kFewSnap = 2;      // a range boundary this near an item's edge moves there: parts cost more
 constexpr int kJoinOnce = 16;    // parts of an item joined in one step
 constexpr float kMoveLog2 = 8.0f;
 
 struct FewShared {
   float m[kFewWarps][16], l[kFewWarps][16];
   long long scan[kFewWarps];
-  long long before;  // units before request `b0` (the CTA's first)
+  int before;  // units before request `b0` (the CTA's first)
   int b0;
   int last;
   int poisoned;
@@ -149,12 +150,25 @@ struct Ranges {
   }
 };
 
-// A position in the sequence of tiles: tile `tile` of `tiles` of (request b, head h).
+// The CTAs' equal shares of the sequence, in 32 bits (a call has fewer than
+// 2^31 tiles; see the kernel), and the CTA whose share unit u falls in.
+struct FewRanges {
+  unsigned base, rem;
+  __device__ FewRanges(unsigned units, unsigned n) : base(units / n), rem(units % n) {}
+  __device__ int begin(unsigned c) const { return (int)(c * base + (c < rem ? c : rem)); }
+  __device__ int owner(unsigned u) const {
+    const unsigned big = rem * (base + 1);
+    return (int)(u < big ? u / (base + 1) : rem + (u - big) / base);
+  }
+};
+
+// A position in a CTA's range: tile `tile`, below `end`, of the `tiles` of
+// (request b, head h), whose first is unit `at`.
 struct FewCursor {
-  int b, h, tile, tiles, n, kv;
+  int b, h, tile, end, tiles, n, kv, at, u1;  // u1: the range's end (before it is moved)
   int64_t q0;
   // takes request b; tiles = 0 where it is not this kernel's
-  __device__ void enter(const PagedAttn& A, bool alone) {
+  __device__ void take(const PagedAttn& A, bool alone) {
     const PagedRequest r = paged_request(A, b);
     n = r.n;
     kv = r.kv;
@@ -166,15 +180,33 @@ struct FewCursor {
       if (alone && rows) raise_error(A.err, TP3D_EPAGES);
     }
   }
-  __device__ void advance(const PagedAttn& A, bool alone) {
-    if (++tile < tiles) return;
+  // where a boundary `off` tiles into an item comes to lie
+  __device__ int snap(int off) const {
+    const int rest = tiles - off;
+    return (off < rest ? off : rest) > kFewSnap ? off : off <= rest ? 0 : tiles;
+  }
+  // the range's share of this item: false when it ends before it
+  __device__ bool share() {
+    const int left = u1 - at;
+    end = left >= tiles ? tiles : left > 0 ? snap(left) : 0;
+    return end > tile;
+  }
+  __device__ bool next_item(const PagedAttn& A, bool alone) {
     tile = 0;
-    if (++h < A.c.kv_heads) return;
-    h = 0;
-    do {
-      ++b;
-      enter(A, alone);
-    } while (tiles == 0);
+    at += tiles;
+    if (at >= u1) return false;
+    if (++h == A.c.kv_heads) {
+      h = 0;
+      do {
+        ++b;
+        take(A, alone);
+      } while (tiles == 0);
+    }
+    return share();
+  }
+  __device__ bool advance(const PagedAttn& A, bool alone) {
+    if (++tile < end) return true;
+    return end == tiles && next_item(A, alone);
   }
 };
 
@@ -193,22 +225,21 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
 
   // ---- this CTA's range of the tile sequence
   FewCursor c;
-  int64_t units = 0, u0 = 0, u1 = 0;
-  int ctas = 0;
+  unsigned units = 0, ctas = 0;
   {
-    // sums of the tiles over the requests, kFewThreads at a time; the second
+    // sums of the tiles over the requests, kFewThreads at a time; a second
     // round (only with more requests than that) finds the request of the
     // range's first tile
-    long long carry = 0;
     const bool one = A.requests <= kFewThreads;
+    int u0 = -1;
 #pragma unroll 1
     for (int round = 0; round < 2; ++round) {
-      carry = 0;
+      long long carry = 0;
 #pragma unroll 1
       for (int base = 0; base < A.requests; base += kFewThreads) {
         c.b = base + tid;
         c.tiles = 0;
-        if (c.b < A.requests) c.enter(A, alone);
+        if (c.b < A.requests) c.take(A, alone);
         long long x = c.tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -224,62 +255,64 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
           if (w < warp) at += sh.scan[w];
           carry += sh.scan[w];
         }
-        if (one || round == 1) {
-          if (round == 0) {
-            units = carry * A.c.kv_heads;
-            const int64_t most = (units + kFewMinTiles - 1) / kFewMinTiles;
-            ctas = most < gridDim.x ? (int)most : (int)gridDim.x;
-            if (blockIdx.x >= ctas) return;
-            const Ranges R(units, ctas);
-            u0 = R.begin(blockIdx.x);
-            u1 = R.begin(blockIdx.x + 1);
+        if (u0 < 0 && base + kFewThreads >= A.requests) {  // the total is known
+          const long long total = carry * A.c.kv_heads;
+          if (total > INT32_MAX) {  // 2^31 tiles of 64 keys: no cache holds them
+            if (tid == 0) raise_error(A.err, TP3D_EPAGES);
+            return;
           }
+          units = (unsigned)total;
+          ctas = (units + kFewMinTiles - 1) / kFewMinTiles;
+          ctas = ctas < gridDim.x ? ctas : gridDim.x;
+          if (blockIdx.x >= ctas) return;
+          const FewRanges R(units, ctas);
+          u0 = R.begin(blockIdx.x);
+          c.u1 = R.begin(blockIdx.x + 1);
+        }
+        if (one || round == 1) {
           at *= A.c.kv_heads;
           if (c.tiles > 0 && at <= u0 && u0 < at + (long long)c.tiles * A.c.kv_heads) {
             sh.b0 = c.b;
-            sh.before = at;
+            sh.before = (int)at;
           }
           if (carry * A.c.kv_heads > u0) break;
         }
       }
       if (one) break;
-      if (round == 0) {
-        units = carry * A.c.kv_heads;
-        const int64_t most = (units + kFewMinTiles - 1) / kFewMinTiles;
-        ctas = most < gridDim.x ? (int)most : (int)gridDim.x;
-        if (blockIdx.x >= ctas) return;
-        const Ranges R(units, ctas);
-        u0 = R.begin(blockIdx.x);
-        u1 = R.begin(blockIdx.x + 1);
-      }
     }
     sh.poison[tid] = INT32_MAX;
     if (tid == 0) sh.poisoned = 0;
     __syncthreads();
     c.b = sh.b0;
-    c.enter(A, alone);
-    const int64_t off = u0 - sh.before;
-    c.h = (int)(off / c.tiles);
-    c.tile = (int)(off - (int64_t)c.h * c.tiles);
+    c.take(A, alone);
+    const int off = u0 - sh.before;
+    c.h = off / c.tiles;
+    const int into = off - c.h * c.tiles;
+    c.at = u0 - into;
+    c.tile = into == 0 ? 0 : c.snap(into);
+    if (!(c.tile == c.tiles ? c.next_item(A, alone) : c.share())) return;
   }
 
   const float sl2 = A.scale * kLog2e;
   uint32_t qf[D / 16][4];
   float o[NT][4], m[2], l[2];
   int lim[2];  // the last key that this thread's two rows see
-  FewCursor ld = c;
-  int64_t lu = u0, u = u0;  // the units to load and to compute next
-  int32_t page = -1;        // of this warp's 16 keys of unit lu
+  FewCursor ld = c;        // the tile to load next; c: to compute next
   bool begin = true, fetch = true;
-  int stage = 0;            // to load into; the next one is the oldest
+  int tile0 = c.tile;      // where this CTA's share of the item begins
+  int stage = 0;           // to load into; the next one is the oldest
+  int pages = -1, pages_b = -1, pages_at = 0;  // lane i: the page of this warp's keys of tile pages_at + i
 #pragma unroll 1
   for (int step = 0;; ++step) {
-    // ---- load unit lu, whose page was looked up a step ago
-    if (fetch && step == 0) {
-      const int key = ld.tile * kFewKeys + warp * 16;
-      if (key < ld.kv) page = __ldg(A.table + (int64_t)ld.b * A.width + (key >> A.page_log2));
-    }
+    // ---- load
     if (fetch) {
+      if (ld.b != pages_b || (unsigned)(ld.tile - pages_at) >= 32u) {
+        pages_b = ld.b;
+        pages_at = ld.tile;
+        const int64_t key = (int64_t)(ld.tile + lane) * kFewKeys + warp * 16;
+        pages = key < ld.kv ? __ldg(A.table + (int64_t)ld.b * A.width + (key >> A.page_log2)) : -1;
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, ld.tile - pages_at);
       const int key = ld.tile * kFewKeys + warp * 16, left = ld.kv - key;
       if (left > 0) {
         const bool in = page >= 0 && page < A.c.pages;
@@ -305,18 +338,13 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
           vs += hop;
         }
       }
-      fetch = ++lu < u1;
-      if (fetch) {
-        ld.advance(A, alone);
-        const int next = ld.tile * kFewKeys + warp * 16;
-        page = next < ld.kv ? __ldg(A.table + (int64_t)ld.b * A.width + (next >> A.page_log2)) : -1;
-      }
+      fetch = ld.advance(A, alone);
     }
     cp_commit();
     stage = stage == kFewStages - 1 ? 0 : stage + 1;
     if (step < kFewStages - 1) continue;
 
-    // ---- compute unit u, in the oldest stage
+    // ---- compute the tile in the oldest stage
     cp_wait<kFewStages - 1>();
     __syncwarp();
     const int rows = c.n * A.group;
@@ -445,10 +473,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     }
 
     // ---- the item's last tile, or this CTA's: join the warps and write
-    const bool done = u + 1 == u1;
-    if (c.tile + 1 == c.tiles || done) {
-      const int64_t item0 = u - c.tile;  // the item's first unit
-      const bool whole = item0 >= u0 && c.tile + 1 == c.tiles;
+    if (c.tile + 1 == c.end) {
+      const bool whole = tile0 == 0 && c.end == c.tiles;
       // the stage just read takes the warp's O: [row][D], column ^ (row mod 4) * 8 against bank conflicts
       float* const so = reinterpret_cast<float*>(ring_ptr + (size_t)(warp * kFewStages + stage) * kStage);
       __syncthreads();  // (also: every warp's notes are in)
@@ -469,9 +495,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         }
       }
       __syncthreads();
-      const Ranges ranges(units, ctas);
-      const int c0 = whole ? 0 : (int)ranges.owner(item0);
-      const int pieces = whole ? 1 : (int)ranges.owner(item0 + c.tiles - 1) - c0 + 1;
+      // the CTAs whose boundaries lie inside the item and stay there, and the one before them
+      const FewRanges ranges(units, ctas);
+      const int c0 = whole ? 0 : ranges.owner(c.at + kFewSnap);
+      const int pieces = whole ? 1 : ranges.owner(c.at + c.tiles - kFewSnap - 1) - c0 + 1;
       const size_t pf = few_part_floats(D);
       // the part of the item's p-th CTA: an item begins in its CTA's last piece (slot 1), goes on in the
       // next one's first (slot 0)
@@ -566,21 +593,36 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
             sh.l[0][tid] = sum;
           }
           __syncthreads();
+          // four vectors of four parts in flight
 #pragma unroll 1
-          for (int e = tid; e < elems; e += kFewThreads) {
-            const int r = e / (D / 4), col = (e - r * (D / 4)) * 4;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(at(first + i * by)) + e);
-              const float f = wm[i * rows + r];
-              acc.x += f * v.x;
-              acc.y += f * v.y;
-              acc.z += f * v.z;
-              acc.w += f * v.w;
+          for (int e0 = tid; e0 < elems; e0 += 4 * kFewThreads) {
+            float4 acc[4];
+            int e[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              acc[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              e[q] = e0 + q * kFewThreads < elems ? e0 + q * kFewThreads : e0;
             }
-            if (level == 1) finish(r, col, acc, sh.m[0][r], sh.l[0][r]);
-            else leave(at(first), r, col, acc, sh.m[0][r], sh.l[0][r]);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+              const float4* const x = reinterpret_cast<const float4*>(at(first + i * by));
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 v = __ldcg(x + e[q]);
+                const float f = wm[i * rows + e[q] / (D / 4)];
+                acc[q].x += f * v.x;
+                acc[q].y += f * v.y;
+                acc[q].z += f * v.z;
+                acc[q].w += f * v.w;
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (e0 + q * kFewThreads >= elems) break;
+              const int r = e[q] / (D / 4), col = (e[q] - r * (D / 4)) * 4;
+              if (level == 1) finish(r, col, acc[q], sh.m[0][r], sh.l[0][r]);
+              else leave(at(first), r, col, acc[q], sh.m[0][r], sh.l[0][r]);
+            }
           }
           counter = counters + 2 * gridDim.x + c0;
           first = 0;
@@ -588,7 +630,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
           n = groups;
         }
       }
-      if (done) break;
       begin = true;
       __syncthreads();  // the stages go back to the loads
       if (hurt) {
@@ -597,8 +638,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         __syncthreads();
       }
     }
-    ++u;
-    c.advance(A, alone);
+    if (!c.advance(A, alone)) break;
+    if (begin) tile0 = 0;
   }
 }
 
