@@ -237,10 +237,19 @@ def _p(x):
     return x.data_ptr()
 
 
+_current_raw_stream = None
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch's current stream as the raw handle, without building a Stream object around it
+        global _current_raw_stream
+        if _current_raw_stream is None:
+            import torch
+            torch.cuda.init()
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _current_raw_stream = lambda: raw(device())
+        return _current_raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -329,15 +338,14 @@ def tp3d_layer_bwd(ctx, cfg: tp3d_layer_cfg, params: dict, X, workspace, dY, dX,
 # tensors here: their shapes and strides are what the C call takes.
 # ---------------------------------------------------------------------------
 
+_dtypes = {}
+
+
 def _dtype_of(x):
-    import torch
-    return {torch.float32: TP3D_F32, torch.bfloat16: TP3D_BF16}.get(x.dtype, -1)
-
-
-def _rows(x, what):
-    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
-        raise ValueError(f"{what}: a (token, head, column) tensor with contiguous columns")
-    return tp3d_row_strides(x.stride(0), x.stride(1))
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: TP3D_F32, torch.bfloat16: TP3D_BF16})
+    return _dtypes.get(x.dtype, -1)
 
 
 def kv_cache(k, v) -> tp3d_kv_cache:
@@ -373,27 +381,32 @@ def tp3d_paged_plan(ctx, page, requests, tokens, cached, fresh, free_pages, free
 
 def tp3d_paged_store(ctx, cache: tp3d_kv_cache, K, V, slots, stream=None) -> int:
     """K, V: (token, head, column) tensors of the same strides."""
-    st = _rows(K, "tp3d_paged_store")
-    if V.shape != K.shape or V.stride() != K.stride() or tuple(K.shape[1:]) != (cache.kv_heads, cache.head_dim):
-        raise ValueError("tp3d_paged_store: K and V (tokens, kv_heads, head_dim) of the same strides")
-    if _dtype_of(K) != cache.dtype or _dtype_of(V) != cache.dtype or slots.numel() < K.shape[0] or \
-            slots.element_size() != 8 or not slots.is_contiguous():
+    shape, st = K.shape, K.stride()
+    if len(shape) != 3 or st[2] != 1 or V.shape != shape or V.stride() != st or shape[1] != cache.kv_heads or \
+            shape[2] != cache.head_dim:
+        raise ValueError("tp3d_paged_store: K and V (tokens, kv_heads, head_dim) of the same strides, "
+                         "contiguous columns")
+    dt = cache.dtype
+    if _dtype_of(K) != dt or _dtype_of(V) != dt or slots.numel() < shape[0] or slots.element_size() != 8 or \
+            not slots.is_contiguous():
         raise ValueError("tp3d_paged_store: K and V of the cache's type, an int64 slot for each token")
-    return lib().tp3d_paged_store(ctx, ctypes.byref(cache), K.shape[0], _p(K), _p(V), st.token_stride,
-                                  st.head_stride, _p(slots), _s(stream))
+    return lib().tp3d_paged_store(ctx, ctypes.byref(cache), shape[0], K.data_ptr(), V.data_ptr(), st[0], st[1],
+                                  slots.data_ptr(), _s(stream))
 
 
 def tp3d_paged_attn(ctx, cache: tp3d_kv_cache, batch: tp3d_paged_batch, Q, O, lse, scale, workspace,
                     stream=None) -> int:
     """Q, O: (token, head, column) tensors; lse: dense (token, head) float32 or None."""
-    qs, os_ = _rows(Q, "tp3d_paged_attn"), _rows(O, "tp3d_paged_attn")
-    if lse is not None and (not lse.is_contiguous() or tuple(lse.shape) != tuple(Q.shape[:2]) or lse.element_size() != 4):
+    shape, qs, os_ = Q.shape, Q.stride(), O.stride()
+    dt = cache.dtype
+    if len(shape) != 3 or O.shape != shape or qs[2] != 1 or os_[2] != 1 or shape[0] < batch.tokens or \
+            shape[2] != cache.head_dim or _dtype_of(Q) != dt or _dtype_of(O) != dt:
+        raise ValueError("tp3d_paged_attn: Q and O (tokens, heads, head_dim) of the cache's type, contiguous columns")
+    if lse is not None and (not lse.is_contiguous() or lse.shape != shape[:2] or lse.element_size() != 4):
         raise ValueError("tp3d_paged_attn: lse dense (tokens, heads) float32")
-    if O.shape != Q.shape or Q.shape[0] < batch.tokens or Q.shape[2] != cache.head_dim or \
-            _dtype_of(Q) != cache.dtype or _dtype_of(O) != cache.dtype:
-        raise ValueError("tp3d_paged_attn: Q and O (tokens, heads, head_dim) of the cache's type")
-    return lib().tp3d_paged_attn(ctx, ctypes.byref(cache), ctypes.byref(batch), Q.shape[1], scale, _p(Q), qs, _p(O),
-                                 os_, _p(lse), _p(workspace), _s(stream))
+    return lib().tp3d_paged_attn(ctx, ctypes.byref(cache), ctypes.byref(batch), shape[1], scale, Q.data_ptr(),
+                                 tp3d_row_strides(qs[0], qs[1]), O.data_ptr(), tp3d_row_strides(os_[0], os_[1]),
+                                 _p(lse), _p(workspace), _s(stream))
 
 
 def tp3d_paged_attn_workspace_bytes(ctx, cache: tp3d_kv_cache, heads: int) -> int:

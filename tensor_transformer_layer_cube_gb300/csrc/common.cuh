@@ -31,6 +31,7 @@ struct tp3d_ctx {
   size_t scratch_bytes;
   // arrival counters of the paged attention's split items (zero between calls)
   unsigned* d_paged;
+  int paged_ready;  // head sizes whose paged attention kernels are set up (bits)
   // CUDA graphs of whole layer calls keyed by their arguments (graph.cu), the
   // stream they run on, and the events that order it with the caller's stream
   void* graphs;

@@ -1486,10 +1486,25 @@ tp3d_status row_map(CUtensorMap* m, const void* ptr, int rank, const int64_t* di
   return r == CUDA_SUCCESS ? TP3D_OK : TP3D_ECUDA;
 }
 
+// The kernels' shared-memory limits, set once per context (a context has one
+// device), and the register split checked: setmaxnreg.inc waits until the
+// block's launch registers cover it.
 template <int D>
-tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool alone, void* workspace, cudaStream_t s) {
+tp3d_status ready(tp3d_ctx* ctx) {
+  const int bit = D == 128 ? 1 : 2;
+  if (ctx->paged_ready & bit) return TP3D_OK;
   TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)few_smem(D)));
+  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem));
+  cudaFuncAttributes fa;
+  TP3D_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_attn_many_kernel<D>));
+  if (fa.numRegs * kManyThreads < 128 * kManyRegsLow + 256 * kManyRegsHigh) return TP3D_EUNSUPPORTED;
+  ctx->paged_ready |= bit;
+  return TP3D_OK;
+}
+
+template <int D>
+tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool alone, void* workspace, cudaStream_t s) {
   paged_attn_few_kernel<D><<<ctx->num_sms * kFewPerSm, kFewThreads, few_smem(D), s>>>(
       A, alone, static_cast<float*>(workspace), ctx->d_paged);
   return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
@@ -1506,11 +1521,6 @@ tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, bool after, void* wor
   const uint32_t cb[4] = {64, (uint32_t)(A.c.page < TR ? A.c.page : TR), 1, 1};
   TP3D_TRY(row_map(&mk, A.c.k, 4, cd, cs, cb));
   TP3D_TRY(row_map(&mv, A.c.v, 4, cd, cs, cb));
-  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem));
-  // setmaxnreg.inc waits until the block's launch registers cover the split
-  cudaFuncAttributes fa;
-  TP3D_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_attn_many_kernel<D>));
-  if (fa.numRegs * kManyThreads < 128 * kManyRegsLow + 256 * kManyRegsHigh) return TP3D_EUNSUPPORTED;
   // launched while the kernel before still runs, to have its prologue behind it
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctx->num_sms);
@@ -1545,6 +1555,7 @@ tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* wo
   // (all its rows are computed there all the same, and a launch is saved).
   const bool one = !alone && A.requests == 1;
   if (one) A.few_rows = 0;
+  TP3D_TRY(d128 ? ready<128>(ctx) : ready<64>(ctx));
   if (!one) TP3D_TRY(d128 ? launch_few<128>(ctx, A, alone, workspace, s) : launch_few<64>(ctx, A, alone, workspace, s));
   if (alone) return TP3D_OK;
   return d128 ? launch_many<128>(ctx, A, !one, workspace, s) : launch_many<64>(ctx, A, !one, workspace, s);
