@@ -110,10 +110,16 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t a) {
 __device__ __forceinline__ void st_shared4(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// some of the eight bf16 of x are not finite: an exponent of all ones carries when one is added to it
-__device__ __forceinline__ unsigned not_finite(const uint4& x) {
-  return (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-          ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) & 0x80008000u;
+// Adds 0 times each of the eight bf16 of x to acc (two sums): they stay zeros
+// while the values are finite and become NaN, for good, with one that is not.
+__device__ __forceinline__ void watch_finite(__nv_bfloat162& acc, const uint4& x) {
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc = __hfma2(h[i], zero, acc);
+}
+__device__ __forceinline__ bool saw_not_finite(const __nv_bfloat162& acc) {
+  return (*reinterpret_cast<const uint32_t*>(&acc) & 0x7fff7fffu) != 0;
 }
 // Sets the non-finite ones of the eight bf16 of x to zero; note(i) for each.
 template <class Note>
@@ -139,22 +145,12 @@ __device__ __forceinline__ uint4 make_finite(const uint4& x, const Note& note) {
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The equal contiguous ranges of `units` units over `n` CTAs, and the CTA that unit u belongs to.
+// The CTAs' equal contiguous shares of a sequence of units, and the CTA whose
+// share unit u falls in.  In 32 bits: a call of 2^31 tiles or more raises
+// TP3D_EPAGES instead (64-bit division costs a short call a microsecond).
 struct Ranges {
-  int64_t base, rem;
-  __device__ Ranges(int64_t units, int64_t n) : base(units / n), rem(units % n) {}
-  __device__ int64_t begin(int64_t c) const { return c * base + (c < rem ? c : rem); }
-  __device__ int64_t owner(int64_t u) const {
-    const int64_t big = rem * (base + 1);
-    return u < big ? u / (base + 1) : rem + (u - big) / base;
-  }
-};
-
-// The CTAs' equal shares of the sequence, in 32 bits (a call has fewer than
-// 2^31 tiles; see the kernel), and the CTA whose share unit u falls in.
-struct FewRanges {
   unsigned base, rem;
-  __device__ FewRanges(unsigned units, unsigned n) : base(units / n), rem(units % n) {}
+  __device__ Ranges(unsigned units, unsigned n) : base(units / n), rem(units % n) {}
   __device__ int begin(unsigned c) const { return (int)(c * base + (c < rem ? c : rem)); }
   __device__ int owner(unsigned u) const {
     const unsigned big = rem * (base + 1);
@@ -221,7 +217,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
   FewShared& sh = *reinterpret_cast<FewShared*>(ring_ptr + kFewWarps * kFewStages * kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = smem_u32(ring_ptr) + (uint32_t)warp * kFewStages * kStage;  // this warp's stages
-  grid_launch_dependents();
 
   // ---- this CTA's range of the tile sequence
   FewCursor c;
@@ -257,15 +252,19 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         }
         if (u0 < 0 && base + kFewThreads >= A.requests) {  // the total is known
           const long long total = carry * A.c.kv_heads;
-          if (total > INT32_MAX) {  // 2^31 tiles of 64 keys: no cache holds them
+          if (total > INT32_MAX) {
             if (tid == 0) raise_error(A.err, TP3D_EPAGES);
+            grid_wait();
             return;
           }
           units = (unsigned)total;
           ctas = (units + kFewMinTiles - 1) / kFewMinTiles;
           ctas = ctas < gridDim.x ? ctas : gridDim.x;
-          if (blockIdx.x >= ctas) return;
-          const FewRanges R(units, ctas);
+          if (blockIdx.x >= ctas) {
+            grid_wait();
+            return;
+          }
+          const Ranges R(units, ctas);
           u0 = R.begin(blockIdx.x);
           c.u1 = R.begin(blockIdx.x + 1);
         }
@@ -290,7 +289,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     const int into = off - c.h * c.tiles;
     c.at = u0 - into;
     c.tile = into == 0 ? 0 : c.snap(into);
-    if (!(c.tile == c.tiles ? c.next_item(A, alone) : c.share())) return;
+    if (!(c.tile == c.tiles ? c.next_item(A, alone) : c.share())) {
+      grid_wait();
+      return;
+    }
   }
 
   const float sl2 = A.scale * kLog2e;
@@ -384,7 +386,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
           const int r = i / RV, v = i & (RV - 1);
           const uint32_t at = sv + (uint32_t)(r * RV + (v ^ (r & 7))) * 16u;
           const uint4 x = ld_shared4(at);
-          if (key0 + r <= c.kv - c.n || !not_finite(x)) continue;
+          __nv_bfloat162 seen = __floats2bfloat162_rn(0.0f, 0.0f);
+          watch_finite(seen, x);
+          if (key0 + r <= c.kv - c.n || !saw_not_finite(seen)) continue;
           st_shared4(at, make_finite(x, [&](int e) { atomicMin(&sh.poison[v * 8 + e], key0 + r); }));
           sh.poisoned = 1;
         }
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
       }
       __syncthreads();
       // the CTAs whose boundaries lie inside the item and stay there, and the one before them
-      const FewRanges ranges(units, ctas);
+      const Ranges ranges(units, ctas);
       const int c0 = whole ? 0 : ranges.owner(c.at + kFewSnap);
       const int pieces = whole ? 1 : ranges.owner(c.at + c.tiles - kFewSnap - 1) - c0 + 1;
       const size_t pf = few_part_floats(D);
@@ -641,6 +645,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     if (!c.advance(A, alone)) break;
     if (begin) tile0 = 0;
   }
+  grid_wait();  // so that this kernel's end is the end of the one before, too
 }
 
 // ------------------------------------------------------------------ many rows
@@ -678,19 +683,30 @@ struct ManyShared {
   int noted[kNotes][2];          // by value-check warp
   int last;
   long long scan[kManyThreads / 32];
-  long long before;
+  int before, per_head;
   int b0;
 };
 constexpr int kManySmem = 7 * (int)kTile + 512 + (int)sizeof(ManyShared) + 1024;
 static_assert(kManySmem <= 232448, "shared memory of one CTA");
 TP3D_HD constexpr size_t many_part_floats(int d) { return (size_t)2 * TR * (d + 2); }
 
-// sum of floor((a i + b) / m) for i < n (the Euclidean recursion); a n + b
-// stays in 32 bits
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-  int64_t s = 0;
+// sum of floor((a i + b) / TR) for i < n, with a, b < TR; a n + b stays in 32 bits
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+  if ((a & (a - 1)) == 0) {  // groups of 2^k heads
+    if (a == 0) return 0;
+    // a = TR / 2^s: floor((i + floor(b / a)) / 2^s)
+    const int s = 7 - (31 - __clz(a));
+    const auto upto = [s](int64_t x) {  // sum of floor(i / 2^s) for i < x
+      const int64_t q = x >> s;
+      return (q * (q - 1) / 2 << s) + q * (x - (q << s));
+    };
+    const uint32_t off = b >> (7 - s);
+    return upto((int64_t)n + off) - upto(off);
+  }
+  int64_t sum = 0;  // the Euclidean recursion
+  uint32_t m = TR;
   while (n > 0) {
-    s += (int64_t)(a / m) * ((int64_t)n * (n - 1) / 2) + (int64_t)(b / m) * n;
+    sum += (int64_t)(a / m) * ((int64_t)n * (n - 1) / 2) + (int64_t)(b / m) * n;
     a %= m;
     b %= m;
     const uint32_t top = a * n + b;
@@ -701,7 +717,7 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
     a = m;
     m = t;
   }
-  return s;
+  return sum;
 }
 
 // The pairs of query tiles of a request: pair k holds tokens [2 k tt, +2 tt).
@@ -717,11 +733,12 @@ struct ManyRequest {
   // key tiles of the pairs before pair k (the last pair's are not among them)
   __device__ int64_t before(int k) const {
     const int w = 2 * tt, ctx = kv - n;
-    int z = ctx < 0 ? -ctx / w : 0;  // pairs whose tokens all see nothing
+    int z = ctx < 0 ? (int)((unsigned)-ctx / (unsigned)w) : 0;  // pairs whose tokens all see nothing
     if (z > k) z = k;
-    // whole tiles of the shared part first: what is left stays below n + a few tiles
     const int b = ctx + (z + 1) * w + TR - 1;
-    return z + (int64_t)(b / TR) * (k - z) + floor_sum((uint32_t)(k - z), TR, (uint32_t)w, (uint32_t)(b % TR));
+    const int64_t left = k - z;
+    return z + (int64_t)(b / TR) * left + (int64_t)(w / TR) * (left * (left - 1) / 2) +
+           floor_sum((uint32_t)left, (uint32_t)(w % TR), (uint32_t)(b % TR));
   }
   __device__ int64_t total() const {
     const int p = pairs();
@@ -750,7 +767,7 @@ struct ManyCursor {
   ManyRequest r;
   int b, h, i, k, pairs;
   int j0, j1, nkv;  // nkv: the pair's key tiles
-  int64_t u, u1;    // the piece's first unit, the range's end (before it is moved)
+  int u, u1;        // the piece's first unit, the range's end (before it is moved)
   __device__ static int fold(int i, int pairs) { return i & 1 ? i >> 1 : pairs - 1 - (i >> 1); }
   // where a boundary `off` tiles into a pair of n comes to lie
   __device__ static int snap(int off, int n) {
@@ -761,8 +778,8 @@ struct ManyCursor {
   __device__ bool enter() {
     k = fold(i, pairs);
     nkv = r.tiles(k);
-    const int64_t end = u1 - (u - j0);
-    j1 = end >= nkv ? nkv : end > 0 ? snap((int)end, nkv) : 0;
+    const int end = u1 - (u - j0);
+    j1 = end >= nkv ? nkv : end > 0 ? snap(end, nkv) : 0;
     return j1 > j0;
   }
   __device__ bool following(const PagedAttn& A) {
@@ -939,6 +956,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                            unsigned* __restrict__ counters) {
   constexpr int NCH = D / 64;
   extern __shared__ uint8_t smem_raw[];
+  grid_launch_dependents();
   const Ctx c = setup_smem(smem_raw);
   ManyShared& sh = *reinterpret_cast<ManyShared*>(c.base_ptr + 7 * kTile + 512);
   auto sQ = [&](int sl) { return c.base + (uint32_t)sl * kTile; };
@@ -957,52 +975,60 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- this CTA's range of the tile sequence (as in the kernel above)
-  int64_t units = 0;
+  unsigned units = 0;
   ManyCursor cur;
   {
-    long long carry = 0;
-    auto chunk = [&](int base, long long& mine, long long& tiles) {
-      const int b = base + (int)threadIdx.x;
-      tiles = 0;
-      if (b < A.requests) {
-        const ManyRequest r = many_request(A, b);
-        if (r.n > 0) tiles = r.total();
-      }
-      long long x = tiles;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) sh.scan[warp] = x;
-      __syncthreads();
-      mine = carry + x - tiles;
-      for (int w = 0; w < kManyThreads / 32; ++w) {
-        if (w < warp) mine += sh.scan[w];
-        carry += sh.scan[w];
-      }
-    };
-    long long mine = 0, tiles = 0;
-    for (int base = 0; base < A.requests; base += kManyThreads) chunk(base, mine, tiles);
-    units = carry * A.c.kv_heads;
-    const Ranges R(units, gridDim.x);
-    cur.u = R.begin(blockIdx.x);
-    cur.u1 = R.begin(blockIdx.x + 1);
-    if (cur.u >= cur.u1) {
-      grid_wait();
-      return;
-    }
     const bool one = A.requests <= kManyThreads;
-    carry = 0;
-    for (int base = 0; base < A.requests; base += kManyThreads) {
-      if (!one) chunk(base, mine, tiles);
-      const long long at = mine * A.c.kv_heads;
-      if (tiles > 0 && at <= cur.u && cur.u < at + tiles * A.c.kv_heads) {
-        sh.b0 = base + (int)threadIdx.x;
-        sh.before = at;
+    cur.u = -1;
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+      long long carry = 0;
+#pragma unroll 1
+      for (int base = 0; base < A.requests; base += kManyThreads) {
+        const int b = base + (int)threadIdx.x;
+        long long tiles = 0;
+        if (b < A.requests) {
+          const ManyRequest r = many_request(A, b);
+          if (r.n > 0) tiles = r.total();
+        }
+        long long x = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) sh.scan[warp] = x;
+        __syncthreads();
+        long long at = carry + x - tiles;
+#pragma unroll 4
+        for (int w = 0; w < kManyThreads / 32; ++w) {
+          if (w < warp) at += sh.scan[w];
+          carry += sh.scan[w];
+        }
+        if (cur.u < 0 && base + kManyThreads >= A.requests) {  // the total is known
+          const long long total = carry * A.c.kv_heads;
+          if (total > INT32_MAX) {
+            if (threadIdx.x == 0) raise_error(A.err, TP3D_EPAGES);
+            return;
+          }
+          units = (unsigned)total;
+          const Ranges R(units, gridDim.x);
+          cur.u = R.begin(blockIdx.x);
+          cur.u1 = R.begin(blockIdx.x + 1);
+          if (cur.u >= cur.u1) return;
+        }
+        if (one || round == 1) {
+          at *= A.c.kv_heads;
+          if (tiles > 0 && at <= cur.u && cur.u < at + tiles * A.c.kv_heads) {
+            sh.b0 = b;
+            sh.before = (int)at;
+            sh.per_head = (int)tiles;
+          }
+          if (carry * A.c.kv_heads > cur.u) break;
+        }
       }
-      if (one || carry * A.c.kv_heads > cur.u) break;
+      if (one) break;
     }
   }
   __syncthreads();
@@ -1010,32 +1036,29 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   cur.r = many_request(A, cur.b);
   cur.pairs = cur.r.pairs();
   {
-    int64_t off = cur.u - sh.before;
-    const int64_t per_head = cur.r.total();
-    cur.h = (int)(off / per_head);
+    const int per_head = sh.per_head;
+    int off = cur.u - sh.before;
+    cur.h = off / per_head;
     off -= cur.h * per_head;
-    // tiles before position i of the folded pairs: those of the last (i + 1) / 2 and the first i / 2
-    const auto folded = [&](int i) {
-      return i == 0 ? (int64_t)0 : per_head - cur.r.before(cur.pairs - (i + 1) / 2) + cur.r.before(i / 2);
-    };
-    // the last position that begins at or before `off`: 32 candidates at a time, one a lane
-    int lo = 0, hi = cur.pairs;
+    // the last position of the folded pairs that begins at or before `off`:
+    // 32 candidates at a time, one a lane.  Before position i lie the tiles of
+    // the last (i + 1) / 2 pairs and of the first i / 2.
+    int lo = 0, hi = cur.pairs, begins = 0;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-      const int n = __popc(__ballot_sync(0xffffffffu, i < hi && folded(i) <= off));  // one at least: lo itself
+      int at = 0;
+      if (i > 0 && i < hi) at = per_head - (int)cur.r.before(cur.pairs - (i + 1) / 2) + (int)cur.r.before(i / 2);
+      const int n = __popc(__ballot_sync(0xffffffffu, i < hi && at <= off));  // one at least: lo itself
+      begins = __shfl_sync(0xffffffffu, at, n - 1);
       lo += (n - 1) * step;
       hi = lo + step < hi ? lo + step : hi;
     }
     cur.i = lo;
-    const int into = (int)(off - folded(lo)), n = cur.r.tiles(ManyCursor::fold(lo, cur.pairs));
+    const int into = off - begins, n = cur.r.tiles(ManyCursor::fold(lo, cur.pairs));
     cur.j0 = into == 0 ? 0 : ManyCursor::snap(into, n);
     cur.u += cur.j0 - into;
-    if (!(cur.j0 == n ? cur.following(A) : cur.enter())) {
-      grid_wait();
-      return;
-    }
+    if (!(cur.j0 == n ? cur.following(A) : cur.enter())) return;
   }
-  grid_wait();  // the kernel before shares the workspace
   if (threadIdx.x == 0) {
     for (int k = 0; k < 32; ++k) {
       // p_half, p_full, o_empty: one arrival per row warp of the slot; r_empty: the
@@ -1259,10 +1282,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const int end = cur.r.kv - k0 < TR ? cur.r.kv - k0 : TR;
 #pragma unroll 1
           for (int key = (end > 0 ? end : 0) + row; key < TR; key += RG) st_shared4(at(key), make_uint4(0, 0, 0, 0));
-          unsigned bad = 0;
+          __nv_bfloat162 sum0 = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll 4
-          for (int key = from + row; key < end; key += RG) bad |= not_finite(ld_shared4(at(key)));
-          if (__any_sync(0xffffffffu, bad != 0)) {
+          for (int key = from + row; key < end; key += RG) watch_finite(sum0, ld_shared4(at(key)));
+          if (__any_sync(0xffffffffu, saw_not_finite(sum0))) {
 #pragma unroll 1
             for (int key = from + row; key < end; key += RG) {
               const unsigned rel = (unsigned)(k0 + key - seen < 0xfffe ? k0 + key - seen : 0xfffe);
@@ -1379,9 +1402,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         warp_arrive(part_full, lane);
         const Ranges ranges(units, gridDim.x);
         // the CTAs whose boundaries lie inside the item and stay there, and the one before them
-        const int64_t item0 = cur.u - cur.j0;
-        const int c0 = (int)ranges.owner(item0 + kSnap),
-                  pieces = (int)ranges.owner(item0 + cur.nkv - kSnap - 1) - c0 + 1;
+        const int item0 = cur.u - cur.j0;
+        const int c0 = ranges.owner(item0 + kSnap), pieces = ranges.owner(item0 + cur.nkv - kSnap - 1) - c0 + 1;
         if (warp == 4 && lane == 0) {
           if ((ok = mbar_wait(part_full, xc & 1, c.abort_flag, A.err))) {
             __threadfence();
@@ -1451,6 +1473,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   }
 }
 
+constexpr int kManyCounters = 1024;  // of the context's counters; the kernel for few rows has the others
+
+size_t few_workspace_floats(const tp3d_ctx* ctx, int d) {
+  return (size_t)ctx->num_sms * kFewPerSm * 2 * few_part_floats(d);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
@@ -1503,15 +1531,28 @@ tp3d_status ready(tp3d_ctx* ctx) {
   return TP3D_OK;
 }
 
+// `after`: right after the other kernel of this call.  It is then launched
+// while that one still runs and takes the SMs that one leaves: the two write
+// different rows, parts and counters, and it ends only when that one has ended.
 template <int D>
-tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool alone, void* workspace, cudaStream_t s) {
-  paged_attn_few_kernel<D><<<ctx->num_sms * kFewPerSm, kFewThreads, few_smem(D), s>>>(
-      A, alone, static_cast<float*>(workspace), ctx->d_paged);
-  return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
+tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool after, float* parts, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(ctx->num_sms * kFewPerSm));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = few_smem(D);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_attn_few_kernel<D>, A, !after, parts, ctx->d_paged + kManyCounters) == cudaSuccess
+             ? TP3D_OK
+             : TP3D_ECUDA;
 }
 
 template <int D>
-tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, bool after, void* workspace, cudaStream_t s) {
+tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, float* parts, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   const int64_t qd[3] = {D, (int64_t)A.group * A.c.kv_heads, A.tokens}, qs[2] = {A.q_head, A.q_token};
   const uint32_t qb[3] = {64, (uint32_t)A.group, (uint32_t)(TR / A.group)};
@@ -1521,44 +1562,35 @@ tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, bool after, void* wor
   const uint32_t cb[4] = {64, (uint32_t)(A.c.page < TR ? A.c.page : TR), 1, 1};
   TP3D_TRY(row_map(&mk, A.c.k, 4, cd, cs, cb));
   TP3D_TRY(row_map(&mv, A.c.v, 4, cd, cs, cb));
-  // launched while the kernel before still runs, to have its prologue behind it
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctx->num_sms);
-  cfg.blockDim = dim3(kManyThreads);
-  cfg.dynamicSmemBytes = kManySmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_attn_many_kernel<D>, mq, mk, mv, A, static_cast<float*>(workspace),
-                            ctx->d_paged) == cudaSuccess
-             ? TP3D_OK
-             : TP3D_ECUDA;
+  paged_attn_many_kernel<D><<<ctx->num_sms, kManyThreads, kManySmem, s>>>(mq, mk, mv, A, parts, ctx->d_paged);
+  return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
+}
+
+template <int D>
+tp3d_status launch(tp3d_ctx* ctx, const PagedAttn& A, bool few, bool many, void* workspace, cudaStream_t s) {
+  float* const few_parts = static_cast<float*>(workspace);
+  TP3D_TRY(ready<D>(ctx));
+  if (many) TP3D_TRY(launch_many<D>(ctx, A, few_parts + few_workspace_floats(ctx, D), s));
+  return few ? launch_few<D>(ctx, A, many, few_parts, s) : TP3D_OK;
 }
 
 }  // namespace
 
 size_t paged_attn_workspace(const tp3d_ctx* ctx, int d) {
-  const size_t few = (size_t)ctx->num_sms * kFewPerSm * 2 * few_part_floats(d);
-  const size_t many = (size_t)ctx->num_sms * 2 * many_part_floats(d);
-  return (few > many ? few : many) * sizeof(float);
+  return (few_workspace_floats(ctx, d) + (size_t)ctx->num_sms * 2 * many_part_floats(d)) * sizeof(float);
 }
 
 tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* workspace, cudaStream_t s) {
-  if (ctx->num_sms * kFewPerSm * 3 > kPagedCounters) return TP3D_EUNSUPPORTED;
+  if (ctx->num_sms > kManyCounters || kManyCounters + ctx->num_sms * kFewPerSm * 3 > kPagedCounters)
+    return TP3D_EUNSUPPORTED;
   const int64_t most = (max_new > 0 && max_new < A.tokens ? max_new : A.tokens) * A.group;
-  A.few_rows = kFewRows;
-  const bool alone = most <= kFewRows, d128 = A.c.head_dim == 128;
+  const bool many = most > kFewRows;
   // One request that may have many rows goes to that kernel whatever it has
   // (all its rows are computed there all the same, and a launch is saved).
-  const bool one = !alone && A.requests == 1;
-  if (one) A.few_rows = 0;
-  TP3D_TRY(d128 ? ready<128>(ctx) : ready<64>(ctx));
-  if (!one) TP3D_TRY(d128 ? launch_few<128>(ctx, A, alone, workspace, s) : launch_few<64>(ctx, A, alone, workspace, s));
-  if (alone) return TP3D_OK;
-  return d128 ? launch_many<128>(ctx, A, !one, workspace, s) : launch_many<64>(ctx, A, !one, workspace, s);
+  const bool few = !many || A.requests > 1;
+  A.few_rows = few ? kFewRows : 0;
+  return A.c.head_dim == 128 ? launch<128>(ctx, A, few, many, workspace, s)
+                             : launch<64>(ctx, A, few, many, workspace, s);
 }
 
 }  // namespace tp3d
