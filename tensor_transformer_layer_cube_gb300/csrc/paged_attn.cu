@@ -52,6 +52,7 @@ constexpr int kFewStages = 3;
 constexpr int kFewMinTiles = 4;  // a CTA's range, where there is little work
 constexpr int kFewSnap = 2;      // a range boundary this near an item's edge moves there: parts cost more
 constexpr int kJoinOnce = 16;    // parts of an item joined in one step
+constexpr int kFewSlots = 4;     // parts that a CTA has room for in the workspace
 constexpr float kMoveLog2 = 8.0f;
 
 struct FewShared {
@@ -347,8 +348,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     if (step < kFewStages - 1) continue;
 
     // ---- compute the tile in the oldest stage
-    cp_wait<kFewStages - 1>();
-    __syncwarp();
     const int rows = c.n * A.group;
     if (begin) {
       begin = false;
@@ -372,6 +371,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
     }
+    cp_wait<kFewStages - 1>();
+    __syncwarp();
     const uint32_t sk = ring + (uint32_t)stage * kStage, sv = sk + kStage / 2;
     const int key0 = c.tile * kFewKeys + warp * 16;
     if (key0 < c.kv) {
@@ -505,8 +506,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
       const int pieces = whole ? 1 : ranges.owner(c.at + c.tiles - kFewSnap - 1) - c0 + 1;
       const size_t pf = few_part_floats(D);
       // the part of the item's p-th CTA: an item begins in its CTA's last piece (slot 1), goes on in the
-      // next one's first (slot 0)
-      const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * pf; };
+      // next one's first (slot 0); what a group of parts came to (below) has slots of its own
+      const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * kFewSlots + (p == 0 ? 1 : 0)) * pf; };
       const auto finish = [&](int r, int col, float4 v, float top, float sum) {
         const int tok = r / A.group;
         const int64_t t = c.q0 + tok;
@@ -564,7 +565,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         const int gsize = pieces <= kJoinOnce ? pieces : (int)ceilf(sqrtf((float)pieces));
         const int groups = (pieces + gsize - 1) / gsize, g = ((int)blockIdx.x - c0) / gsize;
         unsigned* counter = counters + (g == 0 ? 0 : gridDim.x) + c0 + g * gsize;
-        int first = g * gsize, by = 1, n = pieces - first < gsize ? pieces - first : gsize;
+        const auto group_at = [&](int k) { return parts + ((size_t)(c0 + k * gsize) * kFewSlots + (k == 0 ? 2 : 3)) * pf; };
+        const int first = g * gsize;
+        int n = pieces - first < gsize ? pieces - first : gsize;
+        bool of_groups = false;
 #pragma unroll 1
         for (int level = groups == 1 ? 1 : 0; level < 2; ++level) {
           __threadfence();
@@ -573,64 +577,60 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
           __syncthreads();
           if (!sh.last) break;
           __threadfence();
-          // the parts' maxima and sums, then each part's weight, in this CTA's read stages
-          float* const wm = reinterpret_cast<float*>(ring_ptr + (size_t)stage * kStage);
-          float* const wl = wm + kFewStages * kStage / 4;  // the next warp's stage
-          for (int i = tid; i < n * rows; i += kFewThreads) {
-            const float* x = at(first + i / rows * by) + kFewRows * D + i % rows;
-            wm[i] = __ldcg(x);
-            wl[i] = __ldcg(x + kFewRows);
-          }
-          __syncthreads();
-          if (tid < rows) {
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) top = fmaxf(top, wm[i * rows + tid]);
-            const float tb = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-              const float f = ex2_approx(wm[i * rows + tid] - tb);
-              sum += f * wl[i * rows + tid];
-              wm[i * rows + tid] = f;
-            }
-            sh.m[0][tid] = top;
-            sh.l[0][tid] = sum;
-          }
-          __syncthreads();
-          // four vectors of four parts in flight
+          // four parts' maxima, sums and vectors in flight, of two vectors of the result
 #pragma unroll 1
-          for (int e0 = tid; e0 < elems; e0 += 4 * kFewThreads) {
-            float4 acc[4];
-            int e[4];
+          for (int e0 = tid; e0 < elems; e0 += 2 * kFewThreads) {
+            const int e[2] = {e0, e0 + kFewThreads < elems ? e0 + kFewThreads : e0};
+            const int r[2] = {e[0] / (D / 4), e[1] / (D / 4)};
+            float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
+            float4 acc[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+#pragma unroll 1
+            for (int i0 = 0; i0 < n; i0 += 4) {
+              float pm[4][2], ps[4][2];
+              float4 pv[4][2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              acc[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              e[q] = e0 + q * kFewThreads < elems ? e0 + q * kFewThreads : e0;
-            }
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-              const float4* const x = reinterpret_cast<const float4*>(at(first + i * by));
+              for (int i = 0; i < 4; ++i) {
+                if (i0 + i >= n) break;
+                const float* const x = of_groups ? group_at(i0 + i) : at(first + i0 + i);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float4 v = __ldcg(x + e[q]);
-                const float f = wm[i * rows + e[q] / (D / 4)];
-                acc[q].x += f * v.x;
-                acc[q].y += f * v.y;
-                acc[q].z += f * v.z;
-                acc[q].w += f * v.w;
+                for (int q = 0; q < 2; ++q) {
+                  pm[i][q] = __ldcg(x + kFewRows * D + r[q]);
+                  ps[i][q] = __ldcg(x + kFewRows * (D + 1) + r[q]);
+                  pv[i][q] = __ldcg(reinterpret_cast<const float4*>(x) + e[q]);
+                }
+              }
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                float now = top[q];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (i0 + i < n) now = fmaxf(now, pm[i][q]);
+                const float base = now == -INFINITY ? 0.0f : now, keep = ex2_approx(top[q] - base);
+                sum[q] *= keep;
+                acc[q] = make_float4(acc[q].x * keep, acc[q].y * keep, acc[q].z * keep, acc[q].w * keep);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if (i0 + i >= n) break;
+                  const float f = ex2_approx(pm[i][q] - base);
+                  sum[q] += f * ps[i][q];
+                  acc[q].x += f * pv[i][q].x;
+                  acc[q].y += f * pv[i][q].y;
+                  acc[q].z += f * pv[i][q].z;
+                  acc[q].w += f * pv[i][q].w;
+                }
+                top[q] = now;
               }
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               if (e0 + q * kFewThreads >= elems) break;
-              const int r = e[q] / (D / 4), col = (e[q] - r * (D / 4)) * 4;
-              if (level == 1) finish(r, col, acc[q], sh.m[0][r], sh.l[0][r]);
-              else leave(at(first), r, col, acc[q], sh.m[0][r], sh.l[0][r]);
+              const int col = (e[q] - r[q] * (D / 4)) * 4;
+              if (level == 1) finish(r[q], col, acc[q], top[q], sum[q]);
+              else leave(group_at(g), r[q], col, acc[q], top[q], sum[q]);
             }
           }
           counter = counters + 2 * gridDim.x + c0;
-          first = 0;
-          by = gsize;
+          of_groups = true;
           n = groups;
         }
       }
@@ -1476,7 +1476,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 constexpr int kManyCounters = 1024;  // of the context's counters; the kernel for few rows has the others
 
 size_t few_workspace_floats(const tp3d_ctx* ctx, int d) {
-  return (size_t)ctx->num_sms * kFewPerSm * 2 * few_part_floats(d);
+  return (size_t)ctx->num_sms * kFewPerSm * kFewSlots * few_part_floats(d);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode() {
