@@ -501,6 +501,80 @@ def test_a_step_end_to_end(ctx):
         cached, count = kv_len, left
 
 
+@pytest.mark.parametrize("heads,kv_heads,new", [(4, 2, 5), (16, 2, 2), (1, 1, 16), (1, 1, 17), (8, 1, 3), (2, 2, 64)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_chunks(ctx, heads, kv_heads, new, d):
+    # a few tokens each, on both sides of the row count where the kernel changes; some rows see nothing
+    kv = [new, 1, new + 70, 515, 2]
+    c = Case(kv, [new] * 5, heads, kv_heads, d, 16, True, seed=new * heads, v_mean=0.5)
+    o, l = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    compare(c, o, l)
+
+
+@pytest.mark.parametrize("requests", [127, 129, 385, 1000])
+@pytest.mark.parametrize("long_every", [0, 7])
+def test_many_requests(ctx, requests, long_every):
+    # more requests than a CTA looks at in one round; some idle, some with many rows
+    rng = np.random.default_rng(requests)
+    kv = rng.integers(1, 40, requests)
+    new = (rng.random(requests) < 0.8).astype(np.int64)
+    if long_every:
+        new[3::long_every] = np.minimum(kv[3::long_every], 20)
+    c = Case(kv, new, 4, 1, 64, seed=requests)
+    o, l = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    compare(c, o, l)
+
+
+@pytest.mark.parametrize("new", [3, 9, 140])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_in_masked_places(ctx, new, d, value):
+    # in the values of later tokens of the chunk: rows before them are what they are without them, bit for bit
+    kv = [260, new, 333]
+    c = Case(kv, [new] * 3, 4, 2, d, seed=13)
+    clean, cl = c.run(ctx)
+    at = [(0, 260 - new + new // 2, 0, 3), (0, 259, 1, d - 1), (1, new - 1, 0, 17), (2, 333 - new + 1, 1, 40)]
+    for b, pos, head, col in at:
+        c.vp[int(c.table[b, pos // 16]), pos % 16, head, col] = value
+    o, l = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    assert torch.equal(l, cl)
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    for b, pos, head, col in at:
+        first = int(c.q_start[b]) + pos - (kv[b] - new)  # the token at that position sees it, as all after it
+        hit[first:int(c.q_start[b + 1]), 2 * head:2 * head + 2, col] = True
+    assert torch.equal(o[~hit], clean[~hit])
+    assert not bool(o[hit].isfinite().any())
+
+
+def test_values_that_are_not_finite_in_split_work(ctx):
+    # the same where the last keys are one CTA's part of a row and the first ones another's
+    for new, heads, kv_heads in ((4, 4, 1), (150, 2, 1)):
+        c = Case([5000], [new], heads, kv_heads, 128, 64, seed=14)
+        clean, _ = c.run(ctx)
+        pos = 5000 - new // 2
+        c.vp[int(c.table[0, pos // 64]), pos % 64, 0, 5] = float("nan")
+        o, _ = c.run(ctx)
+        assert t.tp3d_sync_status(ctx) == 0
+        sees = pos - (5000 - new)
+        hit = torch.zeros_like(o, dtype=torch.bool)
+        hit[sees:, :, 5] = True
+        assert torch.equal(o[~hit], clean[~hit]) and bool(o[hit].isnan().all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_no_store_outside_the_output(ctx, d):
+    c = Case([300, 40, 1], [200, 17, 1], 4, 2, d, extra_tokens=3)
+    whole, flat = guarded(c.tokens * 4 * d, torch.bfloat16)
+    o, l = c.run(ctx, o=flat.view(c.tokens, 4, d))
+    assert t.tp3d_sync_status(ctx) == 0
+    compare(c, o, l)
+    assert bool(o[218:].isnan().all()) and bool(l[218:].isnan().all())
+    assert_guards_intact(whole)
+
+
 # ------------------------------------------------------------------ refusals
 def test_refusals(ctx):
     EINVAL, ESHAPE, EALIGN, EDTYPE, EUNSUP, EOVER = 1, 2, 3, 4, 7, 8
