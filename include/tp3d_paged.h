@@ -45,8 +45,8 @@ extern "C" {
  *   page      tokens per page: a power of two, 16 to 4096 (else
  *             TP3D_EUNSUPPORTED)
  *   k, v      16-byte aligned, strides multiples of 8 elements (else
- *             TP3D_EALIGN); strides positive and rows not overlapping is the
- *             caller's to keep                                              */
+ *             TP3D_EALIGN), positive, and below 2^39 (else TP3D_EUNSUPPORTED);
+ *             that rows do not overlap is the caller's to keep              */
 typedef struct {
   int32_t dtype, kv_heads, head_dim, page;
   int64_t pages;
@@ -115,14 +115,18 @@ tp3d_status tp3d_paged_store(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t 
  *   lse = log(sum_k exp(scale q . k_k)).
  * A row with no key (kv_b - n_b + j < 0) gets O = 0 and lse = -infinity.  Keys and
  * values past kv_b, and whatever else lies in a page, have no effect on the
- * result (NaN and infinities among it).  Q and O rows: token t, head i at
+ * result (NaN and infinities among it); nor has a later token's value on the
+ * rows before it in its chunk.  A row that does see a value that is not finite
+ * gets NaN or an infinity in its column.  Q and O rows: token t, head i at
  * element t * token_stride + i * head_stride of each; O is written in bf16,
  * lse (or NULL) as float32 [tokens][heads].  Rows from q_start[requests] on
  * are not written.  A block table entry outside the pool raises TP3D_EPAGES;
  * its tokens then read as zeros.
  * Statistics and sums are fp32; the probabilities of the second product are
- * bf16.  The result does not depend on timing: sums that several CTAs
+ * two bf16 terms (16 bits).  The result does not depend on timing: sums that several CTAs
  * contribute to are added in a fixed order.
+ * Work is counted in tiles (64 keys of a request and key/value head; 128 keys
+ * for 256 rows of one); a call of 2^31 tiles or more raises TP3D_EPAGES.
  * heads a multiple of kv_heads (TP3D_ESHAPE), heads / kv_heads <= 128
  * (TP3D_EUNSUPPORTED); scale finite and positive (TP3D_EINVAL); Q, O 16-byte
  * aligned, strides multiples of 8 (TP3D_EALIGN).  `workspace`:

@@ -192,9 +192,8 @@ tp3d_status tp3d_sync_status(tp3d_ctx* ctx, void* stream) {
   int e = 0;
   if (cudaMemcpy(&e, ctx->d_err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return TP3D_ECUDA;
   if (e != 0 && cudaMemset(ctx->d_err, 0, sizeof(int)) != cudaSuccess) return TP3D_ECUDA;
-  // a launch that gave up leaves its split items' counts unfinished
-  if (e == TP3D_ETIMEOUT && cudaMemset(ctx->d_paged, 0, kPagedCounters * sizeof(unsigned)) != cudaSuccess)
-    return TP3D_ECUDA;
+  // a launch that gave up (and perhaps raised something else before) leaves its split items' counts unfinished
+  if (e != 0 && cudaMemset(ctx->d_paged, 0, kPagedCounters * sizeof(unsigned)) != cudaSuccess) return TP3D_ECUDA;
   return static_cast<tp3d_status>(e);
 }
 

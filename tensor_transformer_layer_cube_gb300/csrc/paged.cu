@@ -176,9 +176,10 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs P) 
 }
 
 // ------------------------------------------------------------------ store
-// A copy of 16-byte vectors: consecutive threads take the consecutive
-// vectors of a (token, head) row, K's rows and V's in one launch.  HBM-bound
-// for many tokens, launch latency for few.
+// A copy of 16-byte vectors, K and V in one launch: consecutive threads take
+// the consecutive vectors of a (token, head) row, and each has kStoreVecs
+// vectors of K and of V in flight.  HBM-bound for many tokens, launch latency
+// for few.
 struct StoreArgs {
   tp3d_kv_cache c;
   int page_log2, vec_log2;  // 16-byte vectors of a row: 1 << vec_log2
@@ -188,26 +189,41 @@ struct StoreArgs {
   int* err;
 };
 
+constexpr int kStoreVecs = 4;  // of K and of V each, in flight per thread
+
 __global__ void __launch_bounds__(kThreads) paged_store_kernel(const StoreArgs S) {
-  const int64_t rows = S.tokens * S.c.kv_heads, total = rows << (S.vec_log2 + 1);
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    const int vec = (int)(i & ((1 << S.vec_log2) - 1)) * 8;
-    const int64_t r = i >> S.vec_log2;
-    const bool is_v = r >= rows;
-    const int64_t row = is_v ? r - rows : r;
-    const int64_t t = row / S.c.kv_heads;
-    const int h = (int)(row - t * S.c.kv_heads);
-    const int64_t slot = __ldg(S.slots + t);
-    if (slot < 0) continue;
-    const int64_t page = slot >> S.page_log2, off = slot & ((1 << S.page_log2) - 1);
-    if (page >= S.c.pages) {
-      raise_error(S.err, TP3D_EPAGES);
-      continue;
+  const int64_t rows = S.tokens * S.c.kv_heads, total = rows << S.vec_log2;
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += kStoreVecs * step) {
+    uint4 k[kStoreVecs], v[kStoreVecs];
+    int64_t to[kStoreVecs];
+#pragma unroll
+    for (int q = 0; q < kStoreVecs; ++q) {
+      const int64_t i = i0 + q * step;
+      to[q] = -1;
+      if (i >= total) continue;
+      const int vec = (int)(i & ((1 << S.vec_log2) - 1)) * 8;
+      const int64_t row = i >> S.vec_log2;
+      // 32-bit division where it fits: a 64-bit one costs as much as the copy
+      const int64_t t = row >> 32 ? row / S.c.kv_heads : (int64_t)((uint32_t)row / (uint32_t)S.c.kv_heads);
+      const int h = (int)(row - t * S.c.kv_heads);
+      const int64_t slot = __ldg(S.slots + t), page = slot >> S.page_log2;
+      if (slot < 0) continue;
+      if (page >= S.c.pages) {
+        raise_error(S.err, TP3D_EPAGES);
+        continue;
+      }
+      to[q] = page * S.c.page_stride + (slot & ((1 << S.page_log2) - 1)) * S.c.token_stride + h * S.c.head_stride + vec;
+      const int64_t from = t * S.token_stride + h * S.head_stride + vec;
+      k[q] = __ldg(reinterpret_cast<const uint4*>(S.k + from));
+      v[q] = __ldg(reinterpret_cast<const uint4*>(S.v + from));
     }
-    const __nv_bfloat16* src = (is_v ? S.v : S.k) + t * S.token_stride + h * S.head_stride + vec;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? S.c.v : S.c.k) + page * S.c.page_stride +
-                         off * S.c.token_stride + h * S.c.head_stride + vec;
-    *reinterpret_cast<uint4*>(dst) = __ldg(reinterpret_cast<const uint4*>(src));
+#pragma unroll
+    for (int q = 0; q < kStoreVecs; ++q) {
+      if (to[q] < 0) continue;
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(S.c.k) + to[q]) = k[q];
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(S.c.v) + to[q]) = v[q];
+    }
   }
 }
 
@@ -226,6 +242,7 @@ tp3d_status check_cache(const tp3d_kv_cache* c) {
   if ((c->head_dim != 64 && c->head_dim != 128) || page_log2(c->page) < 0 || c->pages > INT32_MAX)
     return TP3D_EUNSUPPORTED;
   if (c->page_stride < 1 || c->token_stride < 1 || c->head_stride < 1) return TP3D_EINVAL;
+  if ((c->page_stride | c->token_stride | c->head_stride) >> 39) return TP3D_EUNSUPPORTED;  // a tensor map's strides
   if (!aligned16(c->k) || !aligned16(c->v) || (c->page_stride | c->token_stride | c->head_stride) % 8)
     return TP3D_EALIGN;
   return TP3D_OK;
@@ -320,8 +337,8 @@ tp3d_status tp3d_paged_store(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t 
       if (overlaps(o.p, o.n, i.p, i.n)) return TP3D_EOVERLAP;
   const StoreArgs S{*cache, page_log2(cache->page), cache->head_dim == 128 ? 4 : 3, tokens, token_stride, head_stride,
                     static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), slots, ctx->d_err};
-  const int64_t vecs = tokens * cache->kv_heads * (cache->head_dim / 8) * 2;
-  paged_store_kernel<<<blocks(ctx, vecs, 16), kThreads, 0, as_stream(stream)>>>(S);
+  const int64_t vecs = tokens * cache->kv_heads * (cache->head_dim / 8);
+  paged_store_kernel<<<blocks(ctx, vecs, 8), kThreads, 0, as_stream(stream)>>>(S);
   return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
 }
 
@@ -346,6 +363,7 @@ tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3
   if (q_strides.token_stride < 1 || q_strides.head_stride < 1 || o_strides.token_stride < 1 ||
       o_strides.head_stride < 1)
     return TP3D_EINVAL;
+  if ((q_strides.token_stride | q_strides.head_stride) >> 39) return TP3D_EUNSUPPORTED;
   if (!aligned16(Q) || !aligned16(O) || !aligned(workspace, 256) || !aligned(lse, 4) ||
       !aligned(batch->q_start, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->block_table, 4))
     return TP3D_EALIGN;

@@ -1283,8 +1283,21 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll 1
           for (int key = (end > 0 ? end : 0) + row; key < TR; key += RG) st_shared4(at(key), make_uint4(0, 0, 0, 0));
           __nv_bfloat162 sum0 = __floats2bfloat162_rn(0.0f, 0.0f);
-#pragma unroll 4
-          for (int key = from + row; key < end; key += RG) watch_finite(sum0, ld_shared4(at(key)));
+          // rows 8 apart are 1024 bytes apart; eight loads in flight, since the
+          // tensor core's own reads of shared memory hold each of them up
+#pragma unroll 1
+          for (int key = from + row; key < from + row + 8; key += RG) {
+            const uint32_t p = at(key);
+#pragma unroll 1
+            for (int m = 0; key + 8 * m < end; m += 8) {
+              uint4 x[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                x[q] = key + 8 * (m + q) < end ? ld_shared4(p + 1024u * (uint32_t)(m + q)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) watch_finite(sum0, x[q]);
+            }
+          }
           if (__any_sync(0xffffffffu, saw_not_finite(sum0))) {
 #pragma unroll 1
             for (int key = from + row; key < end; key += RG) {
@@ -1503,8 +1516,6 @@ tp3d_status row_map(CUtensorMap* m, const void* ptr, int rank, const int64_t* di
     bx[i] = box[i];
     es[i] = 1;
     if (i > 0) {
-      // a tensor map's strides are below 2^40 bytes
-      if (strides[i - 1] >= ((int64_t)1 << 39)) return TP3D_EUNSUPPORTED;
       st[i - 1] = (cuuint64_t)strides[i - 1] * 2;
     }
   }
