@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs P) 
   __shared__ long long warp_f[kThreads / 32], warp_p[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool first = blockIdx.x == 0;
+  grid_begin();
   const int64_t count0 = __ldg(P.free_count);
   const int64_t count = count0 < 0 ? 0 : count0 > P.free_cap ? P.free_cap : count0;
 
@@ -192,6 +193,7 @@ struct StoreArgs {
 constexpr int kStoreVecs = 4;  // of K and of V each, in flight per thread
 
 __global__ void __launch_bounds__(kThreads) paged_store_kernel(const StoreArgs S) {
+  grid_begin();
   const int64_t rows = S.tokens * S.c.kv_heads, total = rows << S.vec_log2;
   const int64_t step = (int64_t)gridDim.x * kThreads;
   for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += kStoreVecs * step) {
@@ -316,8 +318,7 @@ tp3d_status tp3d_paged_plan(tp3d_ctx* ctx, int page, int requests, int64_t token
   const size_t smem = ((size_t)requests + 1) * 8;
   if (smem > 48 * 1024)
     TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  paged_plan_kernel<<<blocks(ctx, tokens, 1), kThreads, smem, as_stream(stream)>>>(P);
-  return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
+  return launch_dependent(paged_plan_kernel, blocks(ctx, tokens, 1), kThreads, smem, as_stream(stream), P);
 }
 
 tp3d_status tp3d_paged_store(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t tokens, const void* K, const void* V,
@@ -338,8 +339,7 @@ tp3d_status tp3d_paged_store(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t 
   const StoreArgs S{*cache, page_log2(cache->page), cache->head_dim == 128 ? 4 : 3, tokens, token_stride, head_stride,
                     static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), slots, ctx->d_err};
   const int64_t vecs = tokens * cache->kv_heads * (cache->head_dim / 8);
-  paged_store_kernel<<<blocks(ctx, vecs, 8), kThreads, 0, as_stream(stream)>>>(S);
-  return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
+  return launch_dependent(paged_store_kernel, blocks(ctx, vecs, 8), kThreads, 0, as_stream(stream), S);
 }
 
 size_t tp3d_paged_attn_workspace_bytes(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int heads) {

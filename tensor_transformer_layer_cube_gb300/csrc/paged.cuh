@@ -33,6 +33,34 @@ size_t paged_attn_workspace(const tp3d_ctx* ctx, int head_dim);
 
 #if defined(__CUDACC__)
 
+// Programmatic dependent launch.  The paged kernels follow one another in a
+// server's step and are short, so each is launched while the one before it on
+// the stream still runs, and begins by waiting for that one's end (its memory
+// is then visible); it lets the next one come as soon as it has.  All of a
+// kernel's CTAs have begun by then, so those of the next never hold up its own.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_begin() {
+  grid_wait();
+  grid_launch_dependents();
+}
+
+template <class... Params, class... Args>
+tp3d_status launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...) == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
+}
+
 // A request as the attention kernels see it: rows [q0, q0 + n) of Q, kv keys.
 // Lengths that do not fit are clamped, so that whatever the buffers hold, no
 // access leaves them; a request that was clamped raises TP3D_EPAGES.

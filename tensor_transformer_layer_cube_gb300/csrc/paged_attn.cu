@@ -141,11 +141,6 @@ __device__ __forceinline__ uint4 make_finite(const uint4& x, const Note& note) {
   return make_uint4(e[0], e[1], e[2], e[3]);
 }
 
-// Programmatic dependent launch: the kernel that follows may start its
-// prologue now / wait until the one before has finished.
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The CTAs' equal contiguous shares of a sequence of units, and the CTA whose
 // share unit u falls in.  In 32 bits: a call of 2^31 tiles or more raises
 // TP3D_EPAGES instead (64-bit division costs a short call a microsecond).
@@ -218,6 +213,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
   FewShared& sh = *reinterpret_cast<FewShared*>(ring_ptr + kFewWarps * kFewStages * kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = smem_u32(ring_ptr) + (uint32_t)warp * kFewStages * kStage;  // this warp's stages
+  if (alone) grid_wait();  // else the call's other kernel has waited, and this one's end waits for that one
+  grid_launch_dependents();
 
   // ---- this CTA's range of the tile sequence
   FewCursor c;
@@ -956,7 +953,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                            unsigned* __restrict__ counters) {
   constexpr int NCH = D / 64;
   extern __shared__ uint8_t smem_raw[];
-  grid_launch_dependents();
+  grid_begin();
   const Ctx c = setup_smem(smem_raw);
   ManyShared& sh = *reinterpret_cast<ManyShared*>(c.base_ptr + 7 * kTile + 512);
   auto sQ = [&](int sl) { return c.base + (uint32_t)sl * kTile; };
@@ -1542,24 +1539,13 @@ tp3d_status ready(tp3d_ctx* ctx) {
   return TP3D_OK;
 }
 
-// `after`: right after the other kernel of this call.  It is then launched
-// while that one still runs and takes the SMs that one leaves: the two write
-// different rows, parts and counters, and it ends only when that one has ended.
+// `after`: right after the other kernel of this call.  It then works beside
+// that one, on the SMs that one leaves: the two write different rows, parts
+// and counters, and it ends only when that one has ended.
 template <int D>
 tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool after, float* parts, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(ctx->num_sms * kFewPerSm));
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = few_smem(D);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_attn_few_kernel<D>, A, !after, parts, ctx->d_paged + kManyCounters) == cudaSuccess
-             ? TP3D_OK
-             : TP3D_ECUDA;
+  return launch_dependent(paged_attn_few_kernel<D>, (unsigned)(ctx->num_sms * kFewPerSm), kFewThreads, few_smem(D), s,
+                          A, !after, parts, ctx->d_paged + kManyCounters);
 }
 
 template <int D>
@@ -1573,8 +1559,8 @@ tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, float* parts, cudaStr
   const uint32_t cb[4] = {64, (uint32_t)(A.c.page < TR ? A.c.page : TR), 1, 1};
   TP3D_TRY(row_map(&mk, A.c.k, 4, cd, cs, cb));
   TP3D_TRY(row_map(&mv, A.c.v, 4, cd, cs, cb));
-  paged_attn_many_kernel<D><<<ctx->num_sms, kManyThreads, kManySmem, s>>>(mq, mk, mv, A, parts, ctx->d_paged);
-  return cudaGetLastError() == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
+  return launch_dependent(paged_attn_many_kernel<D>, (unsigned)ctx->num_sms, kManyThreads, kManySmem, s, mq, mk, mv, A,
+                          parts, ctx->d_paged);
 }
 
 template <int D>
