@@ -1322,7 +1322,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const float sl2 = A.scale * kLog2e;
     const uint32_t s_col = (uint32_t)(sl * TR), o_col = 256u + (uint32_t)(sl * D);
     const size_t pf = many_part_floats(D);
-    uint32_t sc = 0, oc = 0, ic = 0, xc = 0;  // score tiles, finished accumulators, pieces, split pieces
+    uint32_t sc = 0, oc = 0, ic = 0;  // score tiles, finished accumulators, pieces
+    uint32_t xc = 0;                  // questions about split pieces
     bool ok = true;
     do {
       const int cnt = cur.count(sl);
@@ -1380,97 +1381,125 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             if (hurt) spoil(ov, cc);
             if (live) store_row32(dst + cc * 32, ov, inv);
           }
-          tc_fence_before();
-          warp_arrive(o_empty(sl), lane);
         }
         if (live) put_lse(m, l);
       } else {
-        // element (column block of 4, row) of a part: rows consecutive, so that a warp's accesses are
-        float* const part = parts + ((size_t)blockIdx.x * 2 + (cur.j0 == 0 ? 1 : 0)) * pf;
+        // The CTAs whose boundaries lie inside the item and stay there, and the
+        // one before them, each have a part of it.  The last to come adds them
+        // in order, its own out of tensor memory; the others leave theirs in
+        // the workspace: element (column block of 4, row), rows consecutive,
+        // so that a warp's accesses are.
+        const Ranges ranges(units, gridDim.x);
+        const int item0 = cur.u - cur.j0;
+        const int c0 = ranges.owner(item0 + kSnap), pieces = ranges.owner(item0 + cur.nkv - kSnap - 1) - c0 + 1;
+        const int own = (int)blockIdx.x - c0;
         const int prow = sl * TR + r;
-        if (cnt > 0) {
+        const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * pf; };
+        // All row warps meet, one asks, and all hear the answer: `count` is
+        // whether the CTA arrives at the item's count (which returns to zero
+        // with the last arrival) or only looks whether it would be the last.
+        const auto ask = [&](bool count, bool& answer) -> bool {
+          warp_arrive(part_full, lane);
+          if (warp == 4 && lane == 0 && wait_on(part_full, xc & 1, c, A.err)) {
+            if (count) {
+              __threadfence();
+              sh.last = atomicInc(counters + c0, (unsigned)pieces - 1) == (unsigned)pieces - 1;
+            } else {
+              sh.last = counter_load_acquire(reinterpret_cast<const int*>(counters + c0)) == pieces - 1;
+              if (sh.last) counters[c0] = 0;
+            }
+            mbar_arrive(part_last);
+          }
+          if (!warp_wait_on(part_last, xc & 1, c, A.err, lane)) return false;
+          ++xc;
+          answer = *reinterpret_cast<volatile int*>(&sh.last) != 0;
+          return true;
+        };
+        // where all others have left theirs, this CTA's part need not be written at all
+        bool last = false;
+        if (!(ok = ask(false, last))) break;
+        if (!last) {
+          float* const part = at(own);
+          if (cnt > 0) {
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t ov[32];
+              tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
+              tmem_ld_wait();
+              if (hurt) spoil(ov, cc);
+              if (live)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  __stcg(reinterpret_cast<uint4*>(part) + (size_t)(cc * 8 + e) * (2 * TR) + prow,
+                         make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]));
+            }
+          }
+          if (live) {
+            __stcg(part + (size_t)2 * TR * D + prow, m);
+            __stcg(part + (size_t)2 * TR * (D + 1) + prow, l);
+          }
+          __threadfence();
+          if (!(ok = ask(true, last))) break;
+        }
+        if (last) {
+          __threadfence();
+          float top = m, sum = 0.0f;
+          if (live)
+#pragma unroll 4
+            for (int p = 0; p < pieces; ++p)
+              if (p != own) top = fmaxf(top, __ldcg(at(p) + (size_t)2 * TR * D + prow));
+          const float tb = top == -INFINITY ? 0.0f : top;
+          // 32 columns at a time, all their loads of a part in flight at once
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t ov[32];
-            tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
-            tmem_ld_wait();
-            if (hurt) spoil(ov, cc);
-            if (live)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                __stcg(reinterpret_cast<uint4*>(part) + (size_t)(cc * 8 + e) * (2 * TR) + prow,
-                       make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]));
-          }
-          tc_fence_before();
-          warp_arrive(o_empty(sl), lane);
-        }
-        if (live) {
-          __stcg(part + (size_t)2 * TR * D + prow, m);
-          __stcg(part + (size_t)2 * TR * (D + 1) + prow, l);
-        }
-        __threadfence();
-        warp_arrive(part_full, lane);
-        const Ranges ranges(units, gridDim.x);
-        // the CTAs whose boundaries lie inside the item and stay there, and the one before them
-        const int item0 = cur.u - cur.j0;
-        const int c0 = ranges.owner(item0 + kSnap), pieces = ranges.owner(item0 + cur.nkv - kSnap - 1) - c0 + 1;
-        if (warp == 4 && lane == 0) {
-          if ((ok = mbar_wait(part_full, xc & 1, c.abort_flag, A.err))) {
-            __threadfence();
-            // the count returns to zero with the item's last arrival
-            sh.last = atomicInc(counters + c0, (unsigned)pieces - 1) == (unsigned)pieces - 1;
-            mbar_arrive(part_last);
-          }
-        }
-        if (!(ok = warp_wait_on(part_last, xc & 1, c, A.err, lane))) break;
-        ++xc;
-        if (*reinterpret_cast<volatile int*>(&sh.last)) {
-          __threadfence();
-          if (live) {
-            const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * pf; };
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll 4
-            for (int p = 0; p < pieces; ++p) top = fmaxf(top, __ldcg(at(p) + (size_t)2 * TR * D + prow));
-            const float tb = top == -INFINITY ? 0.0f : top;
-            // half of the row at a time, all its loads of a part in flight at once
-#pragma unroll 1
-            for (int hc = 0; hc < 2; ++hc) {
-              constexpr int H = D / 2;
-              float acc[H];
-#pragma unroll
-              for (int e = 0; e < H; ++e) acc[e] = 0.0f;
-              sum = 0.0f;
-#pragma unroll 1
-              for (int p = 0; p < pieces; ++p) {
-                const float lp = __ldcg(at(p) + (size_t)2 * TR * (D + 1) + prow);
-                const float mp = __ldcg(at(p) + (size_t)2 * TR * D + prow);
-                float4 v[H / 4];
-#pragma unroll
-                for (int e = 0; e < H / 4; ++e)
-                  v[e] = __ldcg(reinterpret_cast<const float4*>(at(p)) + (size_t)(hc * (H / 4) + e) * (2 * TR) + prow);
-                if (lp == 0.0f) continue;  // no key of this row in the part, which may hold no O then
-                const float f = ex2_approx(mp - tb);
-                sum += f * lp;
-#pragma unroll
-                for (int e = 0; e < H / 4; ++e) {
-                  acc[4 * e] += f * v[e].x;
-                  acc[4 * e + 1] += f * v[e].y;
-                  acc[4 * e + 2] += f * v[e].z;
-                  acc[4 * e + 3] += f * v[e].w;
-                }
-              }
-              const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-              for (int e = 0; e < H / 8; ++e)
-                *reinterpret_cast<uint4*>(dst + hc * H + e * 8) =
-                    make_uint4(pack_bf16(acc[8 * e] * inv, acc[8 * e + 1] * inv),
-                               pack_bf16(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
-                               pack_bf16(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
-                               pack_bf16(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
+            if (cnt > 0) {
+              tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
+              tmem_ld_wait();
+              if (hurt) spoil(ov, cc);
             }
-            put_lse(top, sum);
+            if (!live) continue;
+            float acc[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[e] = 0.0f;
+            sum = 0.0f;
+#pragma unroll 1
+            for (int p = 0; p < pieces; ++p) {
+              float lp = l, mp = m;
+              float4 v[8];
+              if (p == own) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  v[e] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                     __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+              } else {
+                lp = __ldcg(at(p) + (size_t)2 * TR * (D + 1) + prow);
+                mp = __ldcg(at(p) + (size_t)2 * TR * D + prow);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  v[e] = __ldcg(reinterpret_cast<const float4*>(at(p)) + (size_t)(cc * 8 + e) * (2 * TR) + prow);
+              }
+              if (lp == 0.0f) continue;  // no key of this row in the part, which may hold no O then
+              const float f = ex2_approx(mp - tb);
+              sum += f * lp;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                acc[4 * e] += f * v[e].x;
+                acc[4 * e + 1] += f * v[e].y;
+                acc[4 * e + 2] += f * v[e].z;
+                acc[4 * e + 3] += f * v[e].w;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(acc[e]);
+            store_row32(dst + cc * 32, ov, sum == 0.0f ? 0.0f : 1.0f / sum);
           }
+          if (live) put_lse(top, sum);
         }
+      }
+      if (cnt > 0) {
+        tc_fence_before();
+        warp_arrive(o_empty(sl), lane);
       }
       ++ic;
     } while (cur.next(A));
