@@ -685,6 +685,9 @@ struct ManyShared {
 };
 constexpr int kManySmem = 7 * (int)kTile + 512 + (int)sizeof(ManyShared) + 1024;
 static_assert(kManySmem <= 232448, "shared memory of one CTA");
+constexpr int kManyByRow = 4;     // parts of an item joined by row
+constexpr int kManyJoinOnce = 8;  // parts of an item joined in one step
+constexpr int kManySlots = 4;     // parts that a CTA has room for in the workspace
 TP3D_HD constexpr size_t many_part_floats(int d) { return (size_t)2 * TR * (d + 2); }
 
 // sum of floor((a i + b) / TR) for i < n, with a, b < TR; a n + b stays in 32 bits
@@ -1385,28 +1388,27 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (live) put_lse(m, l);
       } else {
         // The CTAs whose boundaries lie inside the item and stay there, and the
-        // one before them, each have a part of it.  The last to come adds them
-        // in order, its own out of tensor memory; the others leave theirs in
-        // the workspace: element (column block of 4, row), rows consecutive,
-        // so that a warp's accesses are.
+        // one before them, each have a part of it, and leave it in the
+        // workspace: element (column block of 4, row), rows consecutive, so
+        // that a warp's accesses are.
         const Ranges ranges(units, gridDim.x);
         const int item0 = cur.u - cur.j0;
         const int c0 = ranges.owner(item0 + kSnap), pieces = ranges.owner(item0 + cur.nkv - kSnap - 1) - c0 + 1;
         const int own = (int)blockIdx.x - c0;
         const int prow = sl * TR + r;
-        const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * pf; };
+        const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * kManySlots + (p == 0 ? 1 : 0)) * pf; };
         // All row warps meet, one asks, and all hear the answer: `count` is
         // whether the CTA arrives at the item's count (which returns to zero
         // with the last arrival) or only looks whether it would be the last.
-        const auto ask = [&](bool count, bool& answer) -> bool {
+        const auto ask = [&](bool count, unsigned* counter, int of, bool& answer) -> bool {
           warp_arrive(part_full, lane);
           if (warp == 4 && lane == 0 && wait_on(part_full, xc & 1, c, A.err)) {
             if (count) {
               __threadfence();
-              sh.last = atomicInc(counters + c0, (unsigned)pieces - 1) == (unsigned)pieces - 1;
+              sh.last = atomicInc(counter, (unsigned)of - 1) == (unsigned)of - 1;
             } else {
-              sh.last = counter_load_acquire(reinterpret_cast<const int*>(counters + c0)) == pieces - 1;
-              if (sh.last) counters[c0] = 0;
+              sh.last = counter_load_acquire(reinterpret_cast<const int*>(counter)) == of - 1;
+              if (sh.last) *counter = 0;
             }
             mbar_arrive(part_last);
           }
@@ -1415,9 +1417,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           answer = *reinterpret_cast<volatile int*>(&sh.last) != 0;
           return true;
         };
-        // where all others have left theirs, this CTA's part need not be written at all
+        // Few parts: the last CTA to come adds them in order, its own out of
+        // tensor memory, each row by its thread.  Where all others have left
+        // theirs before it asks, its part need not be written at all.
+        const bool by_row = pieces <= kManyByRow;
         bool last = false;
-        if (!(ok = ask(false, last))) break;
+        if (by_row && !(ok = ask(false, counters + c0, pieces, last))) break;
         if (!last) {
           float* const part = at(own);
           if (cnt > 0) {
@@ -1439,7 +1444,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             __stcg(part + (size_t)2 * TR * (D + 1) + prow, l);
           }
           __threadfence();
-          if (!(ok = ask(true, last))) break;
+          if (by_row && !(ok = ask(true, counters + c0, pieces, last))) break;
         }
         if (last) {
           __threadfence();
@@ -1495,6 +1500,106 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             store_row32(dst + cc * 32, ov, sum == 0.0f ? 0.0f : 1.0f / sum);
           }
           if (live) put_lse(top, sum);
+        } else if (!by_row) {
+          // Many parts: the last arrival at a group's counter adds the group's
+          // parts, the last at the item's the groups', in order, as in the kernel
+          // above; the elements of the live rows are dealt to all row threads.
+          const int gsize = pieces <= kManyJoinOnce ? pieces : (int)ceilf(sqrtf((float)pieces));
+          const int groups = (pieces + gsize - 1) / gsize, g = ((int)blockIdx.x - c0) / gsize;
+          const auto group_at = [&](int k) { return parts + ((size_t)(c0 + k * gsize) * kManySlots + (k == 0 ? 2 : 3)) * pf; };
+          unsigned* counter = counters + (g == 0 ? 0 : gridDim.x) + c0 + g * gsize;
+          const int first = g * gsize;
+          int n = pieces - first < gsize ? pieces - first : gsize;
+          // the rows of the item that are any token's: slot 0's first `live0`, slot 1's first `live1`
+          const int live0 = (cur.r.n - cur.tok(0) < cur.r.tt ? cur.r.n - cur.tok(0) : cur.r.tt) * A.group;
+          const int live1 = !cur.two() ? 0 : (cur.r.n - cur.tok(1) < cur.r.tt ? cur.r.n - cur.tok(1) : cur.r.tt) * A.group;
+          const int work = (live0 + live1) * (D / 16);
+  #pragma unroll 1
+          for (int level = groups == 1 ? 1 : 0; level < 2; ++level) {
+            __threadfence();
+            last = true;
+            if (!(ok = ask(true, counter, n, last)) || !last) break;
+            __threadfence();
+            const bool of_groups = groups > 1 && level == 1;
+            // 16 columns of a row to a thread (consecutive threads: rows), of two parts at a time
+  #pragma unroll 1
+            for (int w = (int)threadIdx.x - 128; w < work; w += 256) {
+              const int q = w % (live0 + live1), col4 = w / (live0 + live1) * 4;
+              const int qs = q >= live0 ? 1 : 0, qr = q - (qs ? live0 : 0);
+              float top = -INFINITY, sum = 0.0f;
+              float4 acc[4];
+  #pragma unroll
+              for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  #pragma unroll 1
+              for (int x0 = 0; x0 < n; x0 += 2) {
+                float pm[2], pl[2];
+                float4 pv[2][4];
+  #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  pm[i] = -INFINITY;
+                  pl[i] = 0.0f;
+                  const int x = x0 + i;
+                  if (x >= n) break;
+                  const float* const part = of_groups ? group_at(x) : at(first + x);
+                  const int prow = qs * TR + qr;
+                  pm[i] = __ldcg(part + (size_t)2 * TR * D + prow);
+                  pl[i] = __ldcg(part + (size_t)2 * TR * (D + 1) + prow);
+  #pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    pv[i][e] = __ldcg(reinterpret_cast<const float4*>(part) + (size_t)(col4 + e) * (2 * TR) + prow);
+                }
+                float now = top;
+  #pragma unroll
+                for (int i = 0; i < 2; ++i) now = fmaxf(now, pm[i]);
+                const float base = now == -INFINITY ? 0.0f : now, keep = ex2_approx(top - base);
+                sum *= keep;
+  #pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
+  #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  if (pl[i] == 0.0f) continue;  // no key of this row in the part, which may hold no O then
+                  const float f = ex2_approx(pm[i] - base);
+                  sum += f * pl[i];
+  #pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    acc[e].x += f * pv[i][e].x;
+                    acc[e].y += f * pv[i][e].y;
+                    acc[e].z += f * pv[i][e].z;
+                    acc[e].w += f * pv[i][e].w;
+                  }
+                }
+                top = now;
+              }
+              if (level == 1) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const int qt = qr / A.group, qg = qr - qt * A.group, qh = cur.h * A.group + qg;
+                const int64_t qrow = (int64_t)cur.r.q0 + cur.tok(qs) + qt;
+                uint4* const to = reinterpret_cast<uint4*>(A.o + qrow * A.o_token + (int64_t)qh * A.o_head + col4 * 4);
+  #pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  to[e] = make_uint4(pack_bf16(acc[2 * e].x * inv, acc[2 * e].y * inv),
+                                     pack_bf16(acc[2 * e].z * inv, acc[2 * e].w * inv),
+                                     pack_bf16(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
+                                     pack_bf16(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
+                if (A.lse && col4 == 0)
+                  A.lse[qrow * (int64_t)(A.group * A.c.kv_heads) + qh] =
+                      sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * kLn2;
+              } else {
+                float* const to = group_at(g);
+                const int prow = qs * TR + qr;
+  #pragma unroll
+                for (int e = 0; e < 4; ++e) __stcg(reinterpret_cast<float4*>(to) + (size_t)(col4 + e) * (2 * TR) + prow, acc[e]);
+                if (col4 == 0) {
+                  __stcg(to + (size_t)2 * TR * D + prow, top);
+                  __stcg(to + (size_t)2 * TR * (D + 1) + prow, sum);
+                }
+              }
+            }
+            counter = counters + 2 * gridDim.x + c0;
+            n = groups;
+          }
+          if (!ok) break;
         }
       }
       if (cnt > 0) {
@@ -1603,11 +1708,11 @@ tp3d_status launch(tp3d_ctx* ctx, const PagedAttn& A, bool few, bool many, void*
 }  // namespace
 
 size_t paged_attn_workspace(const tp3d_ctx* ctx, int d) {
-  return (few_workspace_floats(ctx, d) + (size_t)ctx->num_sms * 2 * many_part_floats(d)) * sizeof(float);
+  return (few_workspace_floats(ctx, d) + (size_t)ctx->num_sms * kManySlots * many_part_floats(d)) * sizeof(float);
 }
 
 tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* workspace, cudaStream_t s) {
-  if (ctx->num_sms > kManyCounters || kManyCounters + ctx->num_sms * kFewPerSm * 3 > kPagedCounters)
+  if (ctx->num_sms * 3 > kManyCounters || kManyCounters + ctx->num_sms * kFewPerSm * 3 > kPagedCounters)
     return TP3D_EUNSUPPORTED;
   const int64_t most = (max_new > 0 && max_new < A.tokens ? max_new : A.tokens) * A.group;
   const bool many = most > kFewRows;
