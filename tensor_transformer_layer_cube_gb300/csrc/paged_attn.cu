@@ -686,13 +686,18 @@ struct ManyShared {
   long long scan[kManyThreads / 32];
   int before, per_head;
   int b0;
+  // split pieces joined after the CTA's range (0: one that it goes on behind, 1: its last): row warps that have
+  // left their rows, whether this CTA is to join, the piece's place in the sequence
+  int left[2], join[2], place[2][5];
 };
 constexpr int kManySmem = 7 * (int)kTile + 512 + (int)sizeof(ManyShared) + 1024;
 static_assert(kManySmem <= 232448, "shared memory of one CTA");
-// Parts of an item joined by row.  The two ways, row | element: 2-3 parts (2048
-// tokens over 6145 keys, 16 heads) 143 | 150 us; 6 parts (64 tokens, 30000 keys,
-// 32 heads) 135 | 128 us; 19 parts (5 tokens, 65536 keys, 8 heads) 122 | 76 us.
-constexpr int kManyByRow = 4;
+// Parts of an item joined by row, by the thread that has the CTA's own part in
+// tensor memory; more by element, dealt to all row threads.  Row | element: 2
+// parts (2048 tokens over 6145 keys, 16 heads) 143 | 150 us; 3-4 parts (4 x 200
+// tokens over 3000) 47.1 | 45.9 us; 19 parts (5 tokens, 65536 keys, 8 heads)
+// 122 | 77 us.
+constexpr int kManyByRow = 3;
 constexpr int kManyJoinOnce = 8;  // parts of an item joined in one step
 constexpr int kManySlots = 4;     // parts that a CTA has room for in the workspace
 TP3D_HD constexpr size_t many_part_floats(int d) { return (size_t)2 * TR * (d + 2); }
@@ -819,6 +824,33 @@ struct ManyCursor {
   __device__ bool partial(int j) const { return (j + 1) * TR - 1 > r.kv - r.n + tok(0); }
 };
 
+// How an item cut by range boundaries is joined: its parts are those of CTAs
+// [c0, c0 + pieces); groups of gsize of them are joined first, where there are
+// many, and then the groups.
+struct ManySplit {
+  int c0, pieces, gsize, groups;
+  __device__ ManySplit(const ManyCursor& cur, unsigned units) {
+    const Ranges ranges(units, gridDim.x);
+    const int item0 = cur.u - cur.j0;
+    c0 = ranges.owner(item0 + kSnap);
+    pieces = ranges.owner(item0 + cur.nkv - kSnap - 1) - c0 + 1;
+    gsize = pieces <= kManyJoinOnce ? pieces : (int)ceilf(sqrtf((float)pieces));
+    groups = (pieces + gsize - 1) / gsize;
+  }
+  __device__ int group() const { return ((int)blockIdx.x - c0) / gsize; }
+  __device__ int members(int g) const { return pieces - g * gsize < gsize ? pieces - g * gsize : gsize; }
+  // a CTA can be an item's first and another's later part: counters and slots of their own
+  __device__ unsigned* counter(unsigned* counters, int g) const {
+    return counters + (g == 0 ? 0 : gridDim.x) + c0 + g * gsize;
+  }
+  __device__ float* part(float* parts, size_t floats, int p) const {
+    return parts + ((size_t)(c0 + p) * kManySlots + (p == 0 ? 1 : 0)) * floats;
+  }
+  __device__ float* group_part(float* parts, size_t floats, int g) const {
+    return parts + ((size_t)(c0 + g * gsize) * kManySlots + (g == 0 ? 2 : 3)) * floats;
+  }
+};
+
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
                                             int c3) {
   asm volatile(
@@ -845,6 +877,23 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+
+// 16 columns of a row, scaled and rounded
+__device__ __forceinline__ void store_row16(bf16* to, const float* x, float scale) {
+  uint32_t p[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = pack_bf16(x[2 * e] * scale, x[2 * e + 1] * scale);
+  if ((reinterpret_cast<uintptr_t>(to) & 31u) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(p[0]), "r"(p[1]), "r"(p[2]),
+                 "r"(p[3]), "r"(p[4]), "r"(p[5]), "r"(p[6]), "r"(p[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+  }
+}
+
+__device__ __forceinline__ void row_warps_meet() { asm volatile("barrier.sync 1, 256;" ::: "memory"); }
 
 // A position in the ring: slot, and the parity of the slot's phase.
 struct RingPos {
@@ -1075,6 +1124,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(bar(k), four ? 4 : ring_empty ? 3 : k >= 23 && k < 28 ? 2 : k == 28 ? 8 : 1);
     }
     *c.abort_flag = 0;
+    sh.left[0] = sh.left[1] = sh.join[0] = sh.join[1] = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -1334,13 +1384,52 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const size_t pf = many_part_floats(D);
     uint32_t sc = 0, oc = 0, ic = 0;  // score tiles, finished accumulators, pieces
     uint32_t xc = 0;                  // questions about split pieces
-    bool ok = true;
+    bool ok = true, more = true;
+    // of the piece just finished (the last one's are used after the loop)
+    ManyCursor at = cur;
+    float m = -INFINITY, l = 0.0f;
+    int cnt = 0;
+    bool live = false, hurt = false, by_row = false, last = false;
+    // columns whose notes say that this row sees a value that is not finite
+    const auto spoil = [&](auto& ov, int col) {
+      const unsigned* const notes = sh.notes[ic % kNotes];
+      const unsigned rel = (unsigned)(at.tok(sl) + tok - at.tok(0));  // the row's last key - the pair's first row's
+#pragma unroll
+      for (int e = 0; e < (int)(sizeof(ov) / 4); ++e)
+        if (((notes[(col + e) >> 1] >> (16 * (e & 1))) & 0xffffu) <= rel) ov[e] = 0x7fffffffu;
+    };
+    const auto put_lse = [&](int64_t row, int head, float top, float sum) {
+      if (A.lse)
+        A.lse[row * (int64_t)(A.group * A.c.kv_heads) + head] =
+            sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * kLn2;
+    };
+    // All row warps meet, one asks, and all hear the answer: `count` is whether
+    // the CTA arrives at the item's count (which returns to zero with the last
+    // arrival) or only looks whether it would be the last.
+    const auto ask = [&](bool count, unsigned* counter, int of, bool& answer) -> bool {
+      warp_arrive(part_full, lane);
+      if (warp == 4 && lane == 0 && wait_on(part_full, xc & 1, c, A.err)) {
+        if (count) {
+          __threadfence();
+          sh.last = atomicInc(counter, (unsigned)of - 1) == (unsigned)of - 1;
+        } else {
+          sh.last = counter_load_acquire(reinterpret_cast<const int*>(counter)) == of - 1;
+          if (sh.last) *counter = 0;
+        }
+        mbar_arrive(part_last);
+      }
+      if (!warp_wait_on(part_last, xc & 1, c, A.err, lane)) return false;
+      ++xc;
+      answer = *reinterpret_cast<volatile int*>(&sh.last) != 0;
+      return true;
+    };
     do {
-      const int cnt = cur.count(sl);
+      cnt = cur.count(sl);
       const int token = cur.tok(sl) + tok;  // of the request
-      const bool live = tok < cur.r.tt && token < cur.r.n;
+      live = tok < cur.r.tt && token < cur.r.n;
       const int lim = cur.r.kv - cur.r.n + token;  // the row's last key
-      float m = -INFINITY, l = 0.0f;
+      m = -INFINITY;
+      l = 0.0f;
       for (int j = cur.j0; j < cur.j0 + cnt && ok; ++j) {
         // new scores; they also mean the slot's previous P V has finished
         if (!(ok = warp_wait_on(s_full(sl), sc & 1, c, A.err, lane))) break;
@@ -1362,251 +1451,77 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         ++oc;
         tc_fence_after();
       }
-      const bool whole = cur.j0 == 0 && cur.j1 == cur.nkv;
-      // columns whose notes say that this row sees a value that is not finite
-      const unsigned* const notes = sh.notes[ic % kNotes];
-      const unsigned rel = (unsigned)(token - cur.tok(0));  // the row's last key - the pair's first row's
-      const bool hurt = cnt > 0 && cur.partial(cur.j0 + cnt - 1) && (sh.noted[ic % kNotes][0] | sh.noted[ic % kNotes][1]) != 0;
-      const auto spoil = [&](uint32_t (&ov)[32], int cc) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (((notes[(cc * 32 + e) >> 1] >> (16 * (e & 1))) & 0xffffu) <= rel) ov[e] = 0x7fffffffu;
-      };
-      const int head = cur.h * A.group + g;
-      const int64_t row = (int64_t)cur.r.q0 + token;
-      bf16* const dst = A.o + row * A.o_token + (int64_t)head * A.o_head;
-      const auto put_lse = [&](float top, float sum) {
-        if (A.lse)
-          A.lse[row * (int64_t)(A.group * A.c.kv_heads) + head] =
-              sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * kLn2;
-      };
-      if (whole) {
+      hurt = cnt > 0 && cur.partial(cur.j0 + cnt - 1) && (sh.noted[ic % kNotes][0] | sh.noted[ic % kNotes][1]) != 0;
+      at = cur;
+      more = cur.next(A);
+      if (at.j0 == 0 && at.j1 == at.nkv) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t row = (int64_t)at.r.q0 + token;
+        const int head = at.h * A.group + g;
+        bf16* const dst = A.o + row * A.o_token + (int64_t)head * A.o_head;
         if (cnt > 0) {
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t ov[32];
             tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
             tmem_ld_wait();
-            if (hurt) spoil(ov, cc);
+            if (hurt) spoil(ov, cc * 32);
             if (live) store_row32(dst + cc * 32, ov, inv);
           }
         }
-        if (live) put_lse(m, l);
+        if (live) put_lse(row, head, m, l);
       } else {
         // The CTAs whose boundaries lie inside the item and stay there, and the
         // one before them, each have a part of it, and leave it in the
         // workspace: element (column block of 4, row), rows consecutive, so
         // that a warp's accesses are.
-        const Ranges ranges(units, gridDim.x);
-        const int item0 = cur.u - cur.j0;
-        const int c0 = ranges.owner(item0 + kSnap), pieces = ranges.owner(item0 + cur.nkv - kSnap - 1) - c0 + 1;
-        const int own = (int)blockIdx.x - c0;
+        const ManySplit split(at, units);
+        // Few parts: the last CTA to come adds them, its own out of tensor
+        // memory, each row by its thread.  It is nearly always one whose range
+        // ends here, and where all others have left theirs before it looks, its
+        // part need not be written at all.  Where the range goes on, no warp
+        // waits for an answer, and in case it was the last the joining is put
+        // off until after the range.
+        by_row = !more && split.pieces <= kManyByRow;
+        if (by_row && !(ok = ask(false, counters + split.c0, split.pieces, last))) break;
+        if (last) break;
+        float* const part = split.part(parts, pf, (int)blockIdx.x - split.c0);
         const int prow = sl * TR + r;
-        const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * kManySlots + (p == 0 ? 1 : 0)) * pf; };
-        // All row warps meet, one asks, and all hear the answer: `count` is
-        // whether the CTA arrives at the item's count (which returns to zero
-        // with the last arrival) or only looks whether it would be the last.
-        const auto ask = [&](bool count, unsigned* counter, int of, bool& answer) -> bool {
-          warp_arrive(part_full, lane);
-          if (warp == 4 && lane == 0 && wait_on(part_full, xc & 1, c, A.err)) {
-            if (count) {
-              __threadfence();
-              sh.last = atomicInc(counter, (unsigned)of - 1) == (unsigned)of - 1;
-            } else {
-              sh.last = counter_load_acquire(reinterpret_cast<const int*>(counter)) == of - 1;
-              if (sh.last) *counter = 0;
-            }
-            mbar_arrive(part_last);
-          }
-          if (!warp_wait_on(part_last, xc & 1, c, A.err, lane)) return false;
-          ++xc;
-          answer = *reinterpret_cast<volatile int*>(&sh.last) != 0;
-          return true;
-        };
-        // Few parts: the last CTA to come adds them in order, its own out of
-        // tensor memory, each row by its thread.  Where all others have left
-        // theirs before it asks, its part need not be written at all.
-        const bool by_row = pieces <= kManyByRow;
-        bool last = false;
-        if (by_row && !(ok = ask(false, counters + c0, pieces, last))) break;
-        if (!last) {
-          float* const part = at(own);
-          if (cnt > 0) {
-#pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t ov[32];
-              tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
-              tmem_ld_wait();
-              if (hurt) spoil(ov, cc);
-              if (live)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  __stcg(reinterpret_cast<uint4*>(part) + (size_t)(cc * 8 + e) * (2 * TR) + prow,
-                         make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]));
-            }
-          }
-          if (live) {
-            __stcg(part + (size_t)2 * TR * D + prow, m);
-            __stcg(part + (size_t)2 * TR * (D + 1) + prow, l);
-          }
-          __threadfence();
-          if (by_row && !(ok = ask(true, counters + c0, pieces, last))) break;
-        }
-        if (last) {
-          __threadfence();
-          float top = m, sum = 0.0f;
-          if (live)
-#pragma unroll 4
-            for (int p = 0; p < pieces; ++p)
-              if (p != own) top = fmaxf(top, __ldcg(at(p) + (size_t)2 * TR * D + prow));
-          const float tb = top == -INFINITY ? 0.0f : top;
-          // 32 columns at a time, all their loads of a part in flight at once
+        if (cnt > 0) {
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t ov[32];
-            if (cnt > 0) {
-              tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
-              tmem_ld_wait();
-              if (hurt) spoil(ov, cc);
-            }
-            if (!live) continue;
-            float acc[32];
+            tmem_ld_32x32b_x32(tmem_row(tmem, quarter, o_col + (uint32_t)(cc * 32)), ov);
+            tmem_ld_wait();
+            if (hurt) spoil(ov, cc * 32);
+            if (live)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[e] = 0.0f;
-            sum = 0.0f;
-#pragma unroll 1
-            for (int p = 0; p < pieces; ++p) {
-              float lp = l, mp = m;
-              float4 v[8];
-              if (p == own) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  v[e] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
-                                     __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
-              } else {
-                lp = __ldcg(at(p) + (size_t)2 * TR * (D + 1) + prow);
-                mp = __ldcg(at(p) + (size_t)2 * TR * D + prow);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  v[e] = __ldcg(reinterpret_cast<const float4*>(at(p)) + (size_t)(cc * 8 + e) * (2 * TR) + prow);
-              }
-              if (lp == 0.0f) continue;  // no key of this row in the part, which may hold no O then
-              const float f = ex2_approx(mp - tb);
-              sum += f * lp;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                acc[4 * e] += f * v[e].x;
-                acc[4 * e + 1] += f * v[e].y;
-                acc[4 * e + 2] += f * v[e].z;
-                acc[4 * e + 3] += f * v[e].w;
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(acc[e]);
-            store_row32(dst + cc * 32, ov, sum == 0.0f ? 0.0f : 1.0f / sum);
+              for (int e = 0; e < 8; ++e)
+                __stcg(reinterpret_cast<uint4*>(part) + (size_t)(cc * 8 + e) * (2 * TR) + prow,
+                       make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]));
           }
-          if (live) put_lse(top, sum);
-        } else if (!by_row) {
-          // Many parts: the last arrival at a group's counter adds the group's
-          // parts, the last at the item's the groups', in order, as in the kernel
-          // above; the elements of the live rows are dealt to all row threads.
-          const int gsize = pieces <= kManyJoinOnce ? pieces : (int)ceilf(sqrtf((float)pieces));
-          const int groups = (pieces + gsize - 1) / gsize, g = ((int)blockIdx.x - c0) / gsize;
-          const auto group_at = [&](int k) { return parts + ((size_t)(c0 + k * gsize) * kManySlots + (k == 0 ? 2 : 3)) * pf; };
-          unsigned* counter = counters + (g == 0 ? 0 : gridDim.x) + c0 + g * gsize;
-          const int first = g * gsize;
-          int n = pieces - first < gsize ? pieces - first : gsize;
-          // the rows of the item that are any token's: slot 0's first `live0`, slot 1's first `live1`
-          const int live0 = (cur.r.n - cur.tok(0) < cur.r.tt ? cur.r.n - cur.tok(0) : cur.r.tt) * A.group;
-          const int live1 = !cur.two() ? 0 : (cur.r.n - cur.tok(1) < cur.r.tt ? cur.r.n - cur.tok(1) : cur.r.tt) * A.group;
-          const int work = (live0 + live1) * (D / 16);
-  #pragma unroll 1
-          for (int level = groups == 1 ? 1 : 0; level < 2; ++level) {
+        }
+        if (live) {
+          __stcg(part + (size_t)2 * TR * D + prow, m);
+          __stcg(part + (size_t)2 * TR * (D + 1) + prow, l);
+        }
+        if (by_row) break;
+        __syncwarp();
+        const int which = more ? 0 : 1;
+        if (lane == 0) {
+          __threadfence_block();
+          if (atomicAdd(&sh.left[which], 1) == 7) {  // the last row warp arrives for the CTA
             __threadfence();
-            last = true;
-            if (!(ok = ask(true, counter, n, last)) || !last) break;
-            __threadfence();
-            const bool of_groups = groups > 1 && level == 1;
-            // 16 columns of a row to a thread (consecutive threads: rows), of two parts at a time
-  #pragma unroll 1
-            for (int w = (int)threadIdx.x - 128; w < work; w += 256) {
-              const int q = w % (live0 + live1), col4 = w / (live0 + live1) * 4;
-              const int qs = q >= live0 ? 1 : 0, qr = q - (qs ? live0 : 0);
-              float top = -INFINITY, sum = 0.0f;
-              float4 acc[4];
-  #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  #pragma unroll 1
-              for (int x0 = 0; x0 < n; x0 += 2) {
-                float pm[2], pl[2];
-                float4 pv[2][4];
-  #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  pm[i] = -INFINITY;
-                  pl[i] = 0.0f;
-                  const int x = x0 + i;
-                  if (x >= n) break;
-                  const float* const part = of_groups ? group_at(x) : at(first + x);
-                  const int prow = qs * TR + qr;
-                  pm[i] = __ldcg(part + (size_t)2 * TR * D + prow);
-                  pl[i] = __ldcg(part + (size_t)2 * TR * (D + 1) + prow);
-  #pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    pv[i][e] = __ldcg(reinterpret_cast<const float4*>(part) + (size_t)(col4 + e) * (2 * TR) + prow);
-                }
-                float now = top;
-  #pragma unroll
-                for (int i = 0; i < 2; ++i) now = fmaxf(now, pm[i]);
-                const float base = now == -INFINITY ? 0.0f : now, keep = ex2_approx(top - base);
-                sum *= keep;
-  #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
-  #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  if (pl[i] == 0.0f) continue;  // no key of this row in the part, which may hold no O then
-                  const float f = ex2_approx(pm[i] - base);
-                  sum += f * pl[i];
-  #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    acc[e].x += f * pv[i][e].x;
-                    acc[e].y += f * pv[i][e].y;
-                    acc[e].z += f * pv[i][e].z;
-                    acc[e].w += f * pv[i][e].w;
-                  }
-                }
-                top = now;
-              }
-              if (level == 1) {
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const int qt = qr / A.group, qg = qr - qt * A.group, qh = cur.h * A.group + qg;
-                const int64_t qrow = (int64_t)cur.r.q0 + cur.tok(qs) + qt;
-                uint4* const to = reinterpret_cast<uint4*>(A.o + qrow * A.o_token + (int64_t)qh * A.o_head + col4 * 4);
-  #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  to[e] = make_uint4(pack_bf16(acc[2 * e].x * inv, acc[2 * e].y * inv),
-                                     pack_bf16(acc[2 * e].z * inv, acc[2 * e].w * inv),
-                                     pack_bf16(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
-                                     pack_bf16(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
-                if (A.lse && col4 == 0)
-                  A.lse[qrow * (int64_t)(A.group * A.c.kv_heads) + qh] =
-                      sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * kLn2;
-              } else {
-                float* const to = group_at(g);
-                const int prow = qs * TR + qr;
-  #pragma unroll
-                for (int e = 0; e < 4; ++e) __stcg(reinterpret_cast<float4*>(to) + (size_t)(col4 + e) * (2 * TR) + prow, acc[e]);
-                if (col4 == 0) {
-                  __stcg(to + (size_t)2 * TR * D + prow, top);
-                  __stcg(to + (size_t)2 * TR * (D + 1) + prow, sum);
-                }
-              }
-            }
-            counter = counters + 2 * gridDim.x + c0;
-            n = groups;
+            const int gr = split.group();
+            const unsigned n = (unsigned)split.members(gr);
+            sh.join[which] = atomicInc(split.counter(counters, gr), n - 1) == n - 1;
+            int* const place = sh.place[which];
+            place[0] = at.b;
+            place[1] = at.h;
+            place[2] = at.k;
+            place[3] = at.nkv;
+            place[4] = at.u - at.j0;
           }
-          if (!ok) break;
         }
       }
       if (cnt > 0) {
@@ -1614,13 +1529,202 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         warp_arrive(o_empty(sl), lane);
       }
       ++ic;
-    } while (cur.next(A));
+    } while (more);
+    if (ok && by_row) {
+      const ManySplit split(at, units);
+      const int own = (int)blockIdx.x - split.c0, prow = sl * TR + r;
+      if (!last) ok = ask(true, counters + split.c0, split.pieces, last);
+      if (ok && last) {
+        __threadfence();
+        const int64_t row = (int64_t)at.r.q0 + at.tok(sl) + tok;
+        const int head = at.h * A.group + g;
+        bf16* const dst = A.o + row * A.o_token + (int64_t)head * A.o_head;
+        // the weights of this row's parts first (0: without a key, and perhaps without O)
+        constexpr int kOthers = kManyByRow - 1;
+        const auto other = [&](int i) { return split.part(parts, pf, i + (i >= own ? 1 : 0)); };
+        float om[kOthers], ol[kOthers], top = m, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kOthers; ++i) {
+          const bool in = live && i < split.pieces - 1;
+          om[i] = in ? __ldcg(other(i) + (size_t)2 * TR * D + prow) : -INFINITY;
+          ol[i] = in ? __ldcg(other(i) + (size_t)2 * TR * (D + 1) + prow) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kOthers; ++i) top = fmaxf(top, om[i]);
+        const float tb = top == -INFINITY ? 0.0f : top, of = ex2_approx(m - tb);
+#pragma unroll
+        for (int i = 0; i <= kOthers; ++i) {  // in order, this CTA's in its place
+          if (own == i && l != 0.0f) sum = fmaf(of, l, sum);
+          if (i == kOthers) break;
+          om[i] = ex2_approx(om[i] - tb);
+          if (ol[i] != 0.0f) sum = fmaf(om[i], ol[i], sum);
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        // 32 columns at a time, all their loads in flight at once
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          float4 v[kOthers][8];
+#pragma unroll
+          for (int i = 0; i < kOthers; ++i)
+            if (ol[i] != 0.0f)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[i][e] = __ldcg(reinterpret_cast<const float4*>(other(i)) + (size_t)(cc * 8 + e) * (2 * TR) + prow);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int col = cc * 32 + half * 16;
+            uint32_t ov[16];
+            if (cnt > 0) {
+              tmem_ld_32x32b_x16(tmem_row(tmem, quarter, o_col + (uint32_t)col), ov);
+              tmem_ld_wait();
+              if (hurt) spoil(ov, col);
+            }
+            float acc[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+#pragma unroll
+            for (int i = 0; i <= kOthers; ++i) {
+              if (own == i && l != 0.0f)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[e] = fmaf(of, __uint_as_float(ov[e]), acc[e]);
+              if (i < kOthers && ol[i] != 0.0f)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float4 x = v[i][half * 4 + e];
+                  acc[4 * e] = fmaf(om[i], x.x, acc[4 * e]);
+                  acc[4 * e + 1] = fmaf(om[i], x.y, acc[4 * e + 1]);
+                  acc[4 * e + 2] = fmaf(om[i], x.z, acc[4 * e + 2]);
+                  acc[4 * e + 3] = fmaf(om[i], x.w, acc[4 * e + 3]);
+                }
+            }
+            if (live) store_row16(dst + col, acc, inv);
+          }
+        }
+        if (live) put_lse(row, head, top, sum);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  if (warp < 4 || *c.abort_flag) return;
+  // ---- split pieces left to be joined here: the last arrival at a group's
+  // counter adds the group's parts, the last at the item's the groups', in
+  // order and with the same operations as above; the elements of the live rows
+  // are dealt to all row threads.
+  const size_t pf = many_part_floats(D);
+  float* const weights = reinterpret_cast<float*>(c.base_ptr);  // [top, sum, parts][row]: the tiles are done with
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    if (!sh.join[which]) continue;
+    cur.b = sh.place[which][0];
+    cur.h = sh.place[which][1];
+    cur.k = sh.place[which][2];
+    cur.nkv = sh.place[which][3];
+    cur.u = sh.place[which][4];
+    cur.j0 = 0;
+    cur.r = many_request(A, cur.b);
+    const ManySplit split(cur, units);
+    const int g = split.group();
+    // the rows of the item that are any token's: slot 0's first live0, slot 1's first live1
+    const int live0 = (cur.r.n - cur.tok(0) < cur.r.tt ? cur.r.n - cur.tok(0) : cur.r.tt) * A.group;
+    const int live1 = !cur.two() ? 0 : (cur.r.n - cur.tok(1) < cur.r.tt ? cur.r.n - cur.tok(1) : cur.r.tt) * A.group;
+    const int work = (live0 + live1) * (D / 16);
+    bool of_groups = false;
+#pragma unroll 1
+    for (;;) {
+      const bool final = of_groups || split.groups == 1;
+      const int n = of_groups ? split.groups : split.members(g);
+      const auto source = [&](int x) {
+        return of_groups ? split.group_part(parts, pf, x) : split.part(parts, pf, g * split.gsize + x);
+      };
+      __threadfence();
+      // the weights of each row's parts (-1: without a key, and perhaps without O), its maximum and sum
+      {
+        const int prow = (int)threadIdx.x - 128;
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
+        for (int x = 0; x < n; ++x) top = fmaxf(top, __ldcg(source(x) + (size_t)2 * TR * D + prow));
+        const float tb = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+        for (int x = 0; x < n; ++x) {
+          const float pl = __ldcg(source(x) + (size_t)2 * TR * (D + 1) + prow);
+          const float f = ex2_approx(__ldcg(source(x) + (size_t)2 * TR * D + prow) - tb);
+          weights[(2 + x) * 2 * TR + prow] = pl == 0.0f ? -1.0f : f;
+          if (pl != 0.0f) sum = fmaf(f, pl, sum);
+        }
+        weights[prow] = top;
+        weights[2 * TR + prow] = sum;
+      }
+      row_warps_meet();
+      // 16 columns of a row to a thread (consecutive threads: rows), of four parts at a time
+#pragma unroll 1
+      for (int w = (int)threadIdx.x - 128; w < work; w += 256) {
+        const int q = w % (live0 + live1), col4 = w / (live0 + live1) * 4;
+        const int qs = q >= live0 ? 1 : 0, qr = q - (qs ? live0 : 0), prow = qs * TR + qr;
+        float acc[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+#pragma unroll 1
+        for (int x0 = 0; x0 < n; x0 += 4) {
+          float f[4];
+          float4 v[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[i] = x0 + i < n ? weights[(2 + x0 + i) * 2 * TR + prow] : -1.0f;
+            if (f[i] == -1.0f) continue;
+            const float* const from = source(x0 + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[i][e] = __ldcg(reinterpret_cast<const float4*>(from) + (size_t)(col4 + e) * (2 * TR) + prow);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (f[i] == -1.0f) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[4 * e] = fmaf(f[i], v[i][e].x, acc[4 * e]);
+              acc[4 * e + 1] = fmaf(f[i], v[i][e].y, acc[4 * e + 1]);
+              acc[4 * e + 2] = fmaf(f[i], v[i][e].z, acc[4 * e + 2]);
+              acc[4 * e + 3] = fmaf(f[i], v[i][e].w, acc[4 * e + 3]);
+            }
+          }
+        }
+        const float top = weights[prow], sum = weights[2 * TR + prow];
+        if (final) {
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          const int tok = qr / A.group, head = cur.h * A.group + (qr - tok * A.group);
+          const int64_t row = (int64_t)cur.r.q0 + cur.tok(qs) + tok;
+          store_row16(A.o + row * A.o_token + (int64_t)head * A.o_head + col4 * 4, acc, inv);
+          if (A.lse && col4 == 0)
+            A.lse[row * (int64_t)(A.group * A.c.kv_heads) + head] =
+                sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * kLn2;
+        } else {
+          float* const to = split.group_part(parts, pf, g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            __stcg(reinterpret_cast<float4*>(to) + (size_t)(col4 + e) * (2 * TR) + prow,
+                   make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]));
+          if (col4 == 0) {
+            __stcg(to + (size_t)2 * TR * D + prow, top);
+            __stcg(to + (size_t)2 * TR * (D + 1) + prow, sum);
+          }
+        }
+      }
+      if (final) break;
+      row_warps_meet();
+      if (threadIdx.x == 128) {
+        __threadfence();
+        const unsigned n2 = (unsigned)split.groups;
+        sh.last = atomicInc(counters + 2 * gridDim.x + split.c0, n2 - 1) == n2 - 1;
+      }
+      row_warps_meet();
+      if (!*reinterpret_cast<volatile int*>(&sh.last)) break;
+      of_groups = true;
+    }
   }
 }
 

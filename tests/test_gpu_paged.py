@@ -654,3 +654,24 @@ def test_refusals(ctx):
         t.tp3d_paged_attn(ctx, c.cache, c.batch(), c.q.float(), o.float(), None, 1.0, ws)
     with pytest.raises(ValueError):
         t.tp3d_paged_store(ctx, c.cache, c.q, c.q, torch.zeros(1, dtype=torch.int64, device=device()))
+
+
+@pytest.mark.parametrize("kv,new,heads,d", [
+    # items in two and three parts, CTAs whose range goes on behind one, and items in many parts
+    ([9000, 7000, 8000], [200, 130, 256], 8, 128), ([4000, 900, 3000, 600], [700, 120, 900, 64], 12, 64),
+    ([20000, 300], [64, 140], 2, 64)])
+def test_order_of_arrival_does_not_change_the_result(ctx, kv, new, heads, d):
+    c = Case(kv, new, heads, heads, d, 64, seed=heads)
+    o, l = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    compare(c, o, l)
+    # long blocks beside it hold a good part of the SMs: CTAs start after the ones before them have ended
+    x = torch.rand(140, 1 << 22, device=device())
+    side = torch.cuda.Stream()
+    for i in range(24):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            x[:20 * (i % 8)].softmax(1)
+        o2, l2 = c.run(ctx)
+        assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(l, l2)
+    assert t.tp3d_sync_status(ctx) == 0
