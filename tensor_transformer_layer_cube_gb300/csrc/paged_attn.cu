@@ -23,10 +23,10 @@ namespace {
 // instructions (mma.sync, 16 rows x 8 keys x 16 columns) do several times
 // faster than HBM delivers them.
 //
-// Work is counted in tiles of 64 keys of one (request, key/value head),
+// Work is counted in tiles of 64 or 128 keys of one (request, key/value head),
 // request by request, head by head; the CTAs take equal contiguous ranges of
 // that sequence, so one long request and many short ones balance alike and
-// nothing about the lengths is needed on the host.  Each of a CTA's four warps
+// nothing about the lengths is needed on the host.  Each of a CTA's warps
 // takes 16 keys of every tile - one page holds them all - through a ring of
 // its own, with 16-byte asynchronous copies and no barrier between the warps:
 // a warp refills a stage as soon as it has read it, which keeps two of three
@@ -43,21 +43,32 @@ namespace {
 // A short call spends most of its time on instructions fetched for the first
 // time, so what runs once is written as rolled loops, and loads are issued in
 // one place.
-constexpr int kFewThreads = 128;
-constexpr int kFewWarps = kFewThreads / 32;
+//
+// W warps a CTA, 8 / W CTAs an SM.  Four: one CTA's end of an item falls
+// together with another's loads.  Eight: fewer parts to an item and fewer steps
+// to a part, where the items are too few to give every SM its own.  4 | 8
+// warps: 16 items of 1024 keys 9.8 | 8.4 us, 16 of 3000 13.0 | 10.5, 8 of
+// 131072 95.4 | 92.3; 128 items of 1024 13.5 | 14.8, 512 of 4096 96.6 | 110.
+template <int W>
+struct FewShape {
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kKeys = 16 * W;  // of a tile
+  static constexpr int kPerSm = 8 / W;
+  // tiles of a CTA's range, where there is little work (16 items of 1024 keys, four warps: 9.8 us; with 2 10.3, with
+  // 6 12.6; eight warps: 8.4 us; with 1 9.2, with 3 10.1)
+  static constexpr int kMinTiles = 16 / W;
+  static constexpr int kSnap = 8 / W;  // a range boundary this near an item's edge moves there: parts cost more
+};
 constexpr int kFewRows = 16;
-constexpr int kFewKeys = 64;  // keys of a tile
-constexpr int kFewPerSm = 2;
 constexpr int kFewStages = 3;
-constexpr int kFewMinTiles = 4;  // a CTA's range, where there is little work (16 heads over 1024 keys: 9.8 us; with 2 10.3, with 6 12.6)
-constexpr int kFewSnap = 2;      // a range boundary this near an item's edge moves there: parts cost more
 constexpr int kJoinOnce = 16;    // parts of an item joined in one step
 constexpr int kFewSlots = 4;     // parts that a CTA has room for in the workspace
 constexpr float kMoveLog2 = 8.0f;
 
+template <int W>
 struct FewShared {
-  float m[kFewWarps][16], l[kFewWarps][16];
-  long long scan[kFewWarps];
+  float m[W][16], l[W][16];
+  long long scan[W];
   int before;  // units before request `b0` (the CTA's first)
   int b0;
   int last;
@@ -66,8 +77,9 @@ struct FewShared {
 };
 
 TP3D_HD constexpr uint32_t few_stage_bytes(int d) { return 16u * 4u * (uint32_t)d; }  // 16 keys, then 16 values
+template <int W>
 constexpr size_t few_smem(int d) {
-  return (size_t)kFewWarps * kFewStages * few_stage_bytes(d) + sizeof(FewShared) + 128;
+  return (size_t)W * kFewStages * few_stage_bytes(d) + sizeof(FewShared<W>) + 128;
 }
 TP3D_HD constexpr size_t few_part_floats(int d) { return (size_t)kFewRows * (d + 2); }
 
@@ -156,7 +168,9 @@ struct Ranges {
 
 // A position in a CTA's range: tile `tile`, below `end`, of the `tiles` of
 // (request b, head h), whose first is unit `at`.
+template <int W>
 struct FewCursor {
+  using Shape = FewShape<W>;
   int b, h, tile, end, tiles, n, kv, at, u1;  // u1: the range's end (before it is moved)
   int64_t q0;
   // takes request b; tiles = 0 where it is not this kernel's
@@ -166,7 +180,7 @@ struct FewCursor {
     kv = r.kv;
     q0 = r.q0;
     const int64_t rows = (int64_t)n * A.group;
-    tiles = kv > 0 ? (kv - 1) / kFewKeys + 1 : 1;  // a request without keys still has rows to write
+    tiles = kv > 0 ? (kv - 1) / Shape::kKeys + 1 : 1;  // a request without keys still has rows to write
     if (rows == 0 || rows > A.few_rows) {
       tiles = 0;
       if (alone && rows) raise_error(A.err, TP3D_EPAGES);
@@ -175,7 +189,7 @@ struct FewCursor {
   // where a boundary `off` tiles into an item comes to lie
   __device__ int snap(int off) const {
     const int rest = tiles - off;
-    return (off < rest ? off : rest) > kFewSnap ? off : off <= rest ? 0 : tiles;
+    return (off < rest ? off : rest) > Shape::kSnap ? off : off <= rest ? 0 : tiles;
   }
   // the range's share of this item: false when it ends before it
   __device__ bool share() {
@@ -203,33 +217,35 @@ struct FewCursor {
 };
 
 // `alone`: no other kernel of the call takes the requests with more rows
-template <int D>
-__global__ void __launch_bounds__(kFewThreads, kFewPerSm)
+template <int D, int W>
+__global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
     paged_attn_few_kernel(const PagedAttn A, bool alone, float* __restrict__ parts, unsigned* __restrict__ counters) {
+  using Shape = FewShape<W>;
+  constexpr int kThreads = Shape::kThreads, kKeys = Shape::kKeys;
   constexpr int RV = D / 8, NT = D / 8;  // 16-byte vectors of a row, 8-column tiles of O
   constexpr uint32_t kStage = few_stage_bytes(D);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const ring_ptr = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
-  FewShared& sh = *reinterpret_cast<FewShared*>(ring_ptr + kFewWarps * kFewStages * kStage);
+  FewShared<W>& sh = *reinterpret_cast<FewShared<W>*>(ring_ptr + W * kFewStages * kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = smem_u32(ring_ptr) + (uint32_t)warp * kFewStages * kStage;  // this warp's stages
   if (alone) grid_wait();  // else the call's other kernel has waited, and this one's end waits for that one
   grid_launch_dependents();
 
   // ---- this CTA's range of the tile sequence
-  FewCursor c;
+  FewCursor<W> c;
   unsigned units = 0, ctas = 0;
   {
-    // sums of the tiles over the requests, kFewThreads at a time; a second
+    // sums of the tiles over the requests, kThreads at a time; a second
     // round (only with more requests than that) finds the request of the
     // range's first tile
-    const bool one = A.requests <= kFewThreads;
+    const bool one = A.requests <= kThreads;
     int u0 = -1;
 #pragma unroll 1
     for (int round = 0; round < 2; ++round) {
       long long carry = 0;
 #pragma unroll 1
-      for (int base = 0; base < A.requests; base += kFewThreads) {
+      for (int base = 0; base < A.requests; base += kThreads) {
         c.b = base + tid;
         c.tiles = 0;
         if (c.b < A.requests) c.take(A, alone);
@@ -244,11 +260,11 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         __syncthreads();
         long long at = carry + x - c.tiles;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
           if (w < warp) at += sh.scan[w];
           carry += sh.scan[w];
         }
-        if (u0 < 0 && base + kFewThreads >= A.requests) {  // the total is known
+        if (u0 < 0 && base + kThreads >= A.requests) {  // the total is known
           const long long total = carry * A.c.kv_heads;
           if (total > INT32_MAX) {
             if (tid == 0) raise_error(A.err, TP3D_EPAGES);
@@ -256,10 +272,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
             return;
           }
           units = (unsigned)total;
-          // kFewMinTiles tiles each, or an item each where items are shorter (16 heads over 61 keys: 4.7 us, four
+          // kMinTiles tiles each, or an item each where items are shorter (16 heads over 61 keys: 4.7 us, four
           // items to a CTA: 10.3)
           const unsigned items = (unsigned)A.requests * (unsigned)A.c.kv_heads;
-          ctas = (units + kFewMinTiles - 1) / kFewMinTiles;
+          ctas = (units + Shape::kMinTiles - 1) / Shape::kMinTiles;
           ctas = ctas > items ? ctas : items < units ? items : units;
           ctas = ctas < gridDim.x ? ctas : gridDim.x;
           if (blockIdx.x >= ctas) {
@@ -281,7 +297,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
       }
       if (one) break;
     }
-    sh.poison[tid] = INT32_MAX;
+    if (tid < 128) sh.poison[tid] = INT32_MAX;
     if (tid == 0) sh.poisoned = 0;
     __syncthreads();
     c.b = sh.b0;
@@ -301,7 +317,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
   uint32_t qf[D / 16][4];
   float o[NT][4], m[2], l[2];
   int lim[2];  // the last key that this thread's two rows see
-  FewCursor ld = c;        // the tile to load next; c: to compute next
+  FewCursor<W> ld = c;        // the tile to load next; c: to compute next
   bool begin = true, fetch = true;
   int tile0 = c.tile;      // where this CTA's share of the item begins
   int stage = 0;           // to load into; the next one is the oldest
@@ -313,11 +329,11 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
       if (ld.b != pages_b || (unsigned)(ld.tile - pages_at) >= 32u) {
         pages_b = ld.b;
         pages_at = ld.tile;
-        const int64_t key = (int64_t)(ld.tile + lane) * kFewKeys + warp * 16;
+        const int64_t key = (int64_t)(ld.tile + lane) * kKeys + warp * 16;
         pages = key < ld.kv ? __ldg(A.table + (int64_t)ld.b * A.width + (key >> A.page_log2)) : -1;
       }
       const int page = __shfl_sync(0xffffffffu, pages, ld.tile - pages_at);
-      const int key = ld.tile * kFewKeys + warp * 16, left = ld.kv - key;
+      const int key = ld.tile * kKeys + warp * 16, left = ld.kv - key;
       if (left > 0) {
         const bool in = page >= 0 && page < A.c.pages;
         if (!in) raise_error(A.err, TP3D_EPAGES);
@@ -375,7 +391,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     cp_wait<kFewStages - 1>();
     __syncwarp();
     const uint32_t sk = ring + (uint32_t)stage * kStage, sv = sk + kStage / 2;
-    const int key0 = c.tile * kFewKeys + warp * 16;
+    const int key0 = c.tile * kKeys + warp * 16;
     if (key0 < c.kv) {
       // keys that some row does not see: past kv - n
       const bool partial = key0 + 15 > c.kv - c.n;
@@ -503,8 +519,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
       __syncthreads();
       // the CTAs whose boundaries lie inside the item and stay there, and the one before them
       const Ranges ranges(units, ctas);
-      const int c0 = whole ? 0 : ranges.owner(c.at + kFewSnap);
-      const int pieces = whole ? 1 : ranges.owner(c.at + c.tiles - kFewSnap - 1) - c0 + 1;
+      const int c0 = whole ? 0 : ranges.owner(c.at + Shape::kSnap);
+      const int pieces = whole ? 1 : ranges.owner(c.at + c.tiles - Shape::kSnap - 1) - c0 + 1;
       const size_t pf = few_part_floats(D);
       // the part of the item's p-th CTA: an item begins in its CTA's last piece (slot 1), goes on in the
       // next one's first (slot 0); what a group of parts came to (below) has slots of its own
@@ -529,15 +545,15 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
       };
       const int elems = rows * (D / 4);
 #pragma unroll 1
-      for (int i = tid; i < elems; i += kFewThreads) {
+      for (int i = tid; i < elems; i += kThreads) {
         const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, sh.m[w][r]);
+        for (int w = 0; w < W; ++w) top = fmaxf(top, sh.m[w][r]);
         const float tb = top == -INFINITY ? 0.0f : top;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
           const float f = ex2_approx(sh.m[w][r] - tb);
           const float4 v = *reinterpret_cast<const float4*>(so + (w - warp) * (int)(kFewStages * kStage / 4) + r * D +
                                                            (col ^ ((r & 3) << 3)));
@@ -580,8 +596,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
           __threadfence();
           // four parts' maxima, sums and vectors in flight, of two vectors of the result
 #pragma unroll 1
-          for (int e0 = tid; e0 < elems; e0 += 2 * kFewThreads) {
-            const int e[2] = {e0, e0 + kFewThreads < elems ? e0 + kFewThreads : e0};
+          for (int e0 = tid; e0 < elems; e0 += 2 * kThreads) {
+            const int e[2] = {e0, e0 + kThreads < elems ? e0 + kThreads : e0};
             const int r[2] = {e[0] / (D / 4), e[1] / (D / 4)};
             float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
             float4 acc[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
@@ -624,7 +640,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              if (e0 + q * kFewThreads >= elems) break;
+              if (e0 + q * kThreads >= elems) break;
               const int col = (e[q] - r[q] * (D / 4)) * 4;
               if (level == 1) finish(r[q], col, acc[q], top[q], sum[q]);
               else leave(group_at(g), r[q], col, acc[q], top[q], sum[q]);
@@ -638,7 +654,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
       begin = true;
       __syncthreads();  // the stages go back to the loads
       if (hurt) {
-        sh.poison[tid] = INT32_MAX;
+        if (tid < 128) sh.poison[tid] = INT32_MAX;
         if (tid == 0) sh.poisoned = 0;
         __syncthreads();
       }
@@ -1731,7 +1747,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 constexpr int kManyCounters = 1024;  // of the context's counters; the kernel for few rows has the others
 
 size_t few_workspace_floats(const tp3d_ctx* ctx, int d) {
-  return (size_t)ctx->num_sms * kFewPerSm * kFewSlots * few_part_floats(d);
+  return (size_t)ctx->num_sms * FewShape<4>::kPerSm * kFewSlots * few_part_floats(d);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode() {
@@ -1774,8 +1790,10 @@ template <int D>
 tp3d_status ready(tp3d_ctx* ctx) {
   const int bit = D == 128 ? 1 : 2;
   if (ctx->paged_ready & bit) return TP3D_OK;
-  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)few_smem(D)));
+  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)few_smem<4>(D)));
+  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)few_smem<8>(D)));
   TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem));
   cudaFuncAttributes fa;
   TP3D_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_attn_many_kernel<D>));
@@ -1787,10 +1805,10 @@ tp3d_status ready(tp3d_ctx* ctx) {
 // `after`: right after the other kernel of this call.  It then works beside
 // that one, on the SMs that one leaves: the two write different rows, parts
 // and counters, and it ends only when that one has ended.
-template <int D>
+template <int D, int W>
 tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool after, float* parts, cudaStream_t s) {
-  return launch_dependent(paged_attn_few_kernel<D>, (unsigned)(ctx->num_sms * kFewPerSm), kFewThreads, few_smem(D), s,
-                          A, !after, parts, ctx->d_paged + kManyCounters);
+  return launch_dependent(paged_attn_few_kernel<D, W>, (unsigned)(ctx->num_sms * FewShape<W>::kPerSm),
+                          FewShape<W>::kThreads, few_smem<W>(D), s, A, !after, parts, ctx->d_paged + kManyCounters);
 }
 
 template <int D>
@@ -1813,7 +1831,10 @@ tp3d_status launch(tp3d_ctx* ctx, const PagedAttn& A, bool few, bool many, void*
   float* const few_parts = static_cast<float*>(workspace);
   TP3D_TRY(ready<D>(ctx));
   if (many) TP3D_TRY(launch_many<D>(ctx, A, few_parts + few_workspace_floats(ctx, D), s));
-  return few ? launch_few<D>(ctx, A, many, few_parts, s) : TP3D_OK;
+  if (!few) return TP3D_OK;
+  // items (requests x key/value heads) that leave half of the SMs without one: see FewShape
+  return (int64_t)A.requests * A.c.kv_heads * 2 <= ctx->num_sms ? launch_few<D, 8>(ctx, A, many, few_parts, s)
+                                                                 : launch_few<D, 4>(ctx, A, many, few_parts, s);
 }
 
 }  // namespace
@@ -1823,7 +1844,7 @@ size_t paged_attn_workspace(const tp3d_ctx* ctx, int d) {
 }
 
 tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* workspace, cudaStream_t s) {
-  if (ctx->num_sms * 3 > kManyCounters || kManyCounters + ctx->num_sms * kFewPerSm * 3 > kPagedCounters)
+  if (ctx->num_sms * 3 > kManyCounters || kManyCounters + ctx->num_sms * FewShape<4>::kPerSm * 3 > kPagedCounters)
     return TP3D_EUNSUPPORTED;
   const int64_t most = (max_new > 0 && max_new < A.tokens ? max_new : A.tokens) * A.group;
   const bool many = most > kFewRows;

@@ -675,3 +675,26 @@ def test_order_of_arrival_does_not_change_the_result(ctx, kv, new, heads, d):
         o2, l2 = c.run(ctx)
         assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(l, l2)
     assert t.tp3d_sync_status(ctx) == 0
+
+
+@pytest.mark.parametrize("heads,kv_heads,new", [(4, 2, 5), (16, 2, 2), (1, 1, 16), (8, 1, 2), (14, 2, 1), (3, 3, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_of_many_requests(ctx, heads, kv_heads, new, d):
+    # enough of them for every SM; lengths at the tiles' edges, one long enough to be split
+    kv = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 257, 300, new, new + 1] * 10 + [6000]
+    c = Case(kv, [new] * len(kv), heads, kv_heads, d, 32, seed=heads + new)
+    o, l = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    compare(c, o, l)
+    if new == 1:
+        return
+    # a value that is not finite in a masked place changes the rows that see its key, and no other
+    b = next(i for i, n in enumerate(kv) if n == 257)
+    pos = 257 - new + new // 2
+    c.vp[int(c.table[b, pos // 32]), pos % 32, kv_heads - 1, 9] = float("inf")
+    got, _ = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    group = heads // kv_heads
+    hit[int(c.q_start[b]) + new // 2:int(c.q_start[b + 1]), heads - group:, 9] = True
+    assert torch.equal(got[~hit], o[~hit]) and not bool(got[hit].isfinite().any())
