@@ -23,7 +23,9 @@ constexpr int kThreads = 256;
 // entry or, for a new page, the free list entry again.
 //
 // It moves 16 bytes per request and 12 per token, so launch latency and the
-// two dependent reads (lengths, then free list or table) bound it.
+// two dependent reads (lengths, then free list or table) bound it: 256 requests
+// of one token 3.4 us on the GPU, 64 prompts (48467 tokens) 3.9 us; the
+// host takes 5.9 us a call.
 constexpr int kScanItems = 4;
 constexpr int kScanChunk = kThreads * kScanItems;
 constexpr int kPlanMaxRequests = 16384;
@@ -179,8 +181,9 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs P) 
 // ------------------------------------------------------------------ store
 // A copy of 16-byte vectors, K and V in one launch: consecutive threads take
 // the consecutive vectors of a (token, head) row, and each has kStoreVecs
-// vectors of K and of V in flight.  HBM-bound for many tokens, launch latency
-// for few.
+// vectors of K and of V in flight.  HBM-bound for many tokens (16385 of 8 heads
+// of 128, 134 MB: 22.8 us, 0.88 of the copy rate; with one vector in flight
+// 24.5), launch latency for few (64 tokens: 1.5 us on the GPU, 5.1 us a call).
 struct StoreArgs {
   tp3d_kv_cache c;
   int page_log2, vec_log2;  // 16-byte vectors of a row: 1 << vec_log2
