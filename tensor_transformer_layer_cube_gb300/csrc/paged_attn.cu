@@ -16,15 +16,15 @@ namespace tp3d {
 namespace {
 
 // ------------------------------------------------------------------ few rows
-// Requests with at most kFewRows rows (new tokens x query heads) per key/value
+// Requests with few rows (new tokens x query heads; see kRows) per key/value
 // head: generation steps and short chunks.  Every row of a key/value head
 // shares one read of its keys and values, so the cache's bytes bound the
 // kernel: per key, 4 D bytes against 4 D rows FLOP, which the legacy tensor
 // instructions (mma.sync, 16 rows x 8 keys x 16 columns) do several times
 // faster than HBM delivers them.
 //
-// Work is counted in tiles of 64 or 128 keys of one (request, key/value head),
-// request by request, head by head; the CTAs take equal contiguous ranges of
+// Work is counted in tiles of 64 or 128 keys of one item (request, key/value
+// head, 16 rows), request by request, head by head; the CTAs take equal contiguous ranges of
 // that sequence, so one long request and many short ones balance alike and
 // nothing about the lengths is needed on the host.  Each of a CTA's warps
 // takes 16 keys of every tile - one page holds them all - through a ring of
@@ -64,13 +64,17 @@ struct FewShape {
   // tiles of a CTA's range, where there is little work (16 items of 1024 keys, four warps: 9.8 us; with 2 10.3, with
   // 6 12.6; eight warps: 8.4 us; with 1 9.2, with 3 10.1)
   static constexpr int kMinTiles = 16 / W;
+  // Rows of a request that this kernel takes, in blocks of 16 (items of their
+  // own, side by side, so that a block finds the others' keys in L2).  Here | in
+  // the kernel for many rows, eight warps: 4 requests of 2000 keys, 4 heads, 24
+  // rows 12.4 | 25.3 us, 48 rows 11.6 | 26.7; one of 65536, 4 heads, 24 rows 41 |
+  // 58, 48 rows 60.9 | 61.1, 64 rows 72.6 | 61.5.  Four warps: 64 of 500, 8 heads
+  // of 64, 16 rows 21.8 | 38.2, 20 rows 25.3 | 27.4; 32 of 4000, 8 heads, 32 rows
+  // 106.7 | 94.8; 16 of 2000, 16 heads, 30 rows 68.8 | 52.9.
+  static constexpr int kRows = W == 8 ? 48 : 16;
   static constexpr int kSnap = 8 / W;  // a range boundary this near an item's edge moves there: parts cost more
 };
-// The rows of one mma.sync tile.  16 rows here | in the kernel for many rows: 4
-// requests of 2000 keys, 4 heads 11.1 | 25.1 us; 8 of 1000, 16 heads 16.8 |
-// 25.5; 64 of 500, 8 heads of 64 21.8 | 38.2; one of 65536, 4 heads 39.3 | 56.9.
-// A second tile of rows would need the registers twice, or the keys.
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 16;  // of an item: one mma.sync tile
 constexpr int kFewStages = 3;
 constexpr int kJoinOnce = 16;    // parts of an item joined in one step
 constexpr int kFewSlots = 4;     // parts that a CTA has room for in the workspace
@@ -178,11 +182,11 @@ struct Ranges {
 };
 
 // A position in a CTA's range: tile `tile`, below `end`, of the `tiles` of
-// (request b, head h), whose first is unit `at`.
+// (request b, head h, rows from row0), whose first is unit `at`.
 template <int W>
 struct FewCursor {
   using Shape = FewShape<W>;
-  int b, h, tile, end, tiles, n, kv, at, u1;  // u1: the range's end (before it is moved)
+  int b, h, row0, tile, end, tiles, n, kv, at, u1;  // u1: the range's end (before it is moved)
   int64_t q0;
   // takes request b; tiles = 0 where it is not this kernel's
   __device__ void take(const PagedAttn& A, bool alone) {
@@ -197,6 +201,8 @@ struct FewCursor {
       if (alone && rows) raise_error(A.err, TP3D_EPAGES);
     }
   }
+  // blocks of 16 rows (of a request that is this kernel's)
+  __device__ int blocks(const PagedAttn& A) const { return Shape::kRows > 16 ? (n * A.group + 15) / 16 : 1; }
   // where a boundary `off` tiles into an item comes to lie
   __device__ int snap(int off) const {
     const int rest = tiles - off;
@@ -212,6 +218,9 @@ struct FewCursor {
     tile = 0;
     at += tiles;
     if (at >= u1) return false;
+    row0 += 16;
+    if (Shape::kRows > 16 && row0 < n * A.group) return share();
+    row0 = 0;
     if (++h == A.c.kv_heads) {
       h = 0;
       do {
@@ -258,9 +267,12 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
 #pragma unroll 1
       for (int base = 0; base < A.requests; base += kThreads) {
         c.b = base + tid;
-        c.tiles = 0;
-        if (c.b < A.requests) c.take(A, alone);
-        long long x = c.tiles;
+        int tiles = 0;  // of the request, per head
+        if (c.b < A.requests) {
+          c.take(A, alone);
+          tiles = c.tiles * c.blocks(A);
+        }
+        long long x = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -269,7 +281,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
         __syncthreads();
         if (lane == 31) sh.scan[warp] = x;
         __syncthreads();
-        long long at = carry + x - c.tiles;
+        long long at = carry + x - tiles;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           if (w < warp) at += sh.scan[w];
@@ -299,7 +311,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
         }
         if (one || round == 1) {
           at *= A.c.kv_heads;
-          if (c.tiles > 0 && at <= u0 && u0 < at + (long long)c.tiles * A.c.kv_heads) {
+          if (tiles > 0 && at <= u0 && u0 < at + (long long)tiles * A.c.kv_heads) {
             sh.b0 = c.b;
             sh.before = (int)at;
           }
@@ -314,8 +326,10 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
     c.b = sh.b0;
     c.take(A, alone);
     const int off = u0 - sh.before;
-    c.h = off / c.tiles;
-    const int into = off - c.h * c.tiles;
+    const int item = off / c.tiles, blocks = c.blocks(A);
+    c.h = Shape::kRows > 16 ? item / blocks : item;
+    c.row0 = (item - c.h * blocks) * 16;
+    const int into = off - item * c.tiles;
     c.at = u0 - into;
     c.tile = into == 0 ? 0 : c.snap(into);
     if (!(c.tile == c.tiles ? c.next_item(A, alone) : c.share())) {
@@ -376,14 +390,14 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
     if (step < kFewStages - 1) continue;
 
     // ---- compute the tile in the oldest stage
-    const int rows = c.n * A.group;
+    const int rows = c.n * A.group - c.row0 < 16 ? c.n * A.group - c.row0 : 16;  // of the block
     if (begin) {
       begin = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = (lane >> 2) + 8 * e;
         const bool in = r < rows;
-        const int tok = in ? r / A.group : 0, g = in ? r - tok * A.group : 0;
+        const int tok = in ? (c.row0 + r) / A.group : 0, g = in ? c.row0 + r - tok * A.group : 0;
         lim[e] = in ? c.kv - c.n + tok : c.kv - 1;
         const bf16* src = A.q + (c.q0 + tok) * A.q_token + (int64_t)(c.h * A.group + g) * A.q_head + (lane & 3) * 2;
 #pragma unroll
@@ -537,9 +551,9 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
       // next one's first (slot 0); what a group of parts came to (below) has slots of its own
       const auto at = [&](int p) { return parts + ((size_t)(c0 + p) * kFewSlots + (p == 0 ? 1 : 0)) * pf; };
       const auto finish = [&](int r, int col, float4 v, float top, float sum) {
-        const int tok = r / A.group;
+        const int tok = (c.row0 + r) / A.group;
         const int64_t t = c.q0 + tok;
-        const int head = c.h * A.group + (r - tok * A.group);
+        const int head = c.h * A.group + (c.row0 + r - tok * A.group);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         *reinterpret_cast<uint2*>(A.o + t * A.o_token + (int64_t)head * A.o_head + col) =
             make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
@@ -575,7 +589,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
           acc.w += f * v.w;
         }
         if (hurt) {
-          const int lr = c.kv - c.n + r / A.group;
+          const int lr = c.kv - c.n + (c.row0 + r) / A.group;
           float* const x = reinterpret_cast<float*>(&acc);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -677,7 +691,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
 }
 
 // ------------------------------------------------------------------ many rows
-// Requests with more than kFewRows rows per key/value head: prompts and their
+// Requests with more rows per key/value head than that: prompts and their
 // chunks.  4 D FLOP per (row, key) pair against 4 D bytes per key: tensor
 // work bounds it.  One CTA per SM takes pairs of 128-row query tiles (rows are
 // new token x query head of the group, so grouped heads fill a tile with few
@@ -1848,14 +1862,12 @@ tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, float* parts, cudaStr
 }
 
 template <int D>
-tp3d_status launch(tp3d_ctx* ctx, const PagedAttn& A, bool few, bool many, void* workspace, cudaStream_t s) {
+tp3d_status launch(tp3d_ctx* ctx, const PagedAttn& A, bool few, bool many, bool wide, void* workspace, cudaStream_t s) {
   float* const few_parts = static_cast<float*>(workspace);
   TP3D_TRY(ready<D>(ctx));
   if (many) TP3D_TRY(launch_many<D>(ctx, A, few_parts + few_workspace_floats(ctx, D), s));
   if (!few) return TP3D_OK;
-  // items (requests x key/value heads) that leave half of the SMs without one: see FewShape
-  return (int64_t)A.requests * A.c.kv_heads * 2 <= ctx->num_sms ? launch_few<D, 8>(ctx, A, many, few_parts, s)
-                                                                 : launch_few<D, 4>(ctx, A, many, few_parts, s);
+  return wide ? launch_few<D, 8>(ctx, A, many, few_parts, s) : launch_few<D, 4>(ctx, A, many, few_parts, s);
 }
 
 }  // namespace
@@ -1867,14 +1879,17 @@ size_t paged_attn_workspace(const tp3d_ctx* ctx, int d) {
 tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* workspace, cudaStream_t s) {
   if (ctx->num_sms * 3 > kManyCounters || kManyCounters + ctx->num_sms * FewShape<4>::kPerSm * 3 > kPagedCounters)
     return TP3D_EUNSUPPORTED;
+  // items (requests x key/value heads) that leave half of the SMs without one: see FewShape
+  const bool wide = (int64_t)A.requests * A.c.kv_heads * 2 <= ctx->num_sms;
+  const int few_rows = wide ? FewShape<8>::kRows : FewShape<4>::kRows;
   const int64_t most = (max_new > 0 && max_new < A.tokens ? max_new : A.tokens) * A.group;
-  const bool many = most > kFewRows;
+  const bool many = most > few_rows;
   // One request that may have many rows goes to that kernel whatever it has
   // (all its rows are computed there all the same, and a launch is saved).
   const bool few = !many || A.requests > 1;
-  A.few_rows = few ? kFewRows : 0;
-  return A.c.head_dim == 128 ? launch<128>(ctx, A, few, many, workspace, s)
-                             : launch<64>(ctx, A, few, many, workspace, s);
+  A.few_rows = few ? few_rows : 0;
+  return A.c.head_dim == 128 ? launch<128>(ctx, A, few, many, wide, workspace, s)
+                             : launch<64>(ctx, A, few, many, wide, workspace, s);
 }
 
 }  // namespace tp3d

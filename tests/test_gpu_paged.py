@@ -698,3 +698,29 @@ def test_few_rows_of_many_requests(ctx, heads, kv_heads, new, d):
     group = heads // kv_heads
     hit[int(c.q_start[b]) + new // 2:int(c.q_start[b + 1]), heads - group:, 9] = True
     assert torch.equal(got[~hit], o[~hit]) and not bool(got[hit].isfinite().any())
+
+
+@pytest.mark.parametrize("heads,kv_heads,new", [(8, 2, 11), (8, 2, 12), (6, 2, 16), (6, 2, 17), (32, 1, 1), (48, 1, 1),
+                                                (7, 1, 5), (33, 1, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_rows_than_one_block(ctx, heads, kv_heads, new, d):
+    # rows of a token in two blocks; on both sides of the row count where the kernel changes; split and short items
+    kv = [5000, new, 300, 128, 129, 1]
+    c = Case(kv, [new] * 6, heads, kv_heads, d, 64, True, seed=heads * new, v_mean=0.5)
+    o, l = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    compare(c, o, l)
+    o2, l2 = c.run(ctx)
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(l, l2)
+    if new == 1:
+        return
+    # a value that is not finite in a masked place changes the rows that see its key, and no other
+    for b, n in ((0, 5000), (2, 300)):
+        pos = n - new + new // 2
+        c.vp[int(c.table[b, pos // 64]), pos % 64, kv_heads - 1, 7] = float("nan")
+    got, _ = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    for b in (0, 2):
+        hit[int(c.q_start[b]) + new // 2:int(c.q_start[b + 1]), heads - heads // kv_heads:, 7] = True
+    assert torch.equal(got[~hit], o[~hit]) and bool(got[hit].isnan().all())
