@@ -822,20 +822,27 @@ __device__ __forceinline__ ManyRequest many_request(const PagedAttn& A, int b) {
 //
 // The pairs of a head come folded - last, first, last but one, second, ... -
 // so that neighbours in the sequence add up to like amounts of work, and a
-// range boundary within kSnap tiles of a pair's edge is moved there: leaving a
-// part and joining it costs about as much as that many tiles (4 prompts of up
-// to 1024: 42.1 us; with 2 42.8, with 1 46.6).
+// range boundary within `near` tiles of a pair's edge is moved there: leaving a
+// part and joining it costs about as much as kSnap tiles (4 prompts of up to
+// 1024: 42.1 us; with 2 42.8, with 1 46.6).  Where ranges are short, moving by
+// as much would leave CTAs without work beside others with twice theirs, so it
+// is two tiles less than a range, one at least.  With that | always by kSnap: 4
+// requests of 2000 keys, 128 rows a head, 4 heads 24.9 | 30.9 us; 8 chunks of
+// up to 100 over 1000, 16 heads of 64 22.1 | 25.5; one prompt of 1000, 16 heads
+// 30.3 | 28.6; 4 x 200 over 3000 the same.
 constexpr int kSnap = 4;
+constexpr int kManyMinTiles = 2;  // of a CTA's range, where there is little work (the first case above; with 1 27.2)
 struct ManyCursor {
   ManyRequest r;
   int b, h, i, k, pairs;
   int j0, j1, nkv;  // nkv: the pair's key tiles
   int u, u1;        // the piece's first unit, the range's end (before it is moved)
+  int near;         // boundaries this near a pair's edge are moved
   __device__ static int fold(int i, int pairs) { return i & 1 ? i >> 1 : pairs - 1 - (i >> 1); }
   // where a boundary `off` tiles into a pair of n comes to lie
-  __device__ static int snap(int off, int n) {
+  __device__ int snap(int off, int n) const {
     const int rest = n - off;
-    return (off < rest ? off : rest) > kSnap ? off : off <= rest ? 0 : n;
+    return (off < rest ? off : rest) > near ? off : off <= rest ? 0 : n;
   }
   // enters position i of the folded pairs at tile j0 (unit u): false when the range ends before it
   __device__ bool enter() {
@@ -880,11 +887,11 @@ struct ManyCursor {
 // many, and then the groups.
 struct ManySplit {
   int c0, pieces, gsize, groups;
-  __device__ ManySplit(const ManyCursor& cur, unsigned units) {
-    const Ranges ranges(units, gridDim.x);
+  __device__ ManySplit(const ManyCursor& cur, unsigned units, unsigned ctas) {
+    const Ranges ranges(units, ctas);
     const int item0 = cur.u - cur.j0;
-    c0 = ranges.owner(item0 + kSnap);
-    pieces = ranges.owner(item0 + cur.nkv - kSnap - 1) - c0 + 1;
+    c0 = ranges.owner(item0 + cur.near);
+    pieces = ranges.owner(item0 + cur.nkv - cur.near - 1) - c0 + 1;
     gsize = pieces <= kManyJoinOnce ? pieces : (int)ceilf(sqrtf((float)pieces));
     groups = (pieces + gsize - 1) / gsize;
   }
@@ -1082,7 +1089,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- this CTA's range of the tile sequence (as in the kernel above)
-  unsigned units = 0;
+  unsigned units = 0, ctas = 0;
   ManyCursor cur;
   {
     const bool one = A.requests <= kManyThreads;
@@ -1120,8 +1127,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             return;
           }
           units = (unsigned)total;
-          const Ranges R(units, gridDim.x);
+          ctas = (units + kManyMinTiles - 1) / kManyMinTiles;
+          ctas = ctas < gridDim.x ? ctas : gridDim.x;
+          if (blockIdx.x >= ctas) return;
+          const Ranges R(units, ctas);
           cur.u = R.begin(blockIdx.x);
+          const int near = (int)(units / ctas) - 2;
+          cur.near = near < 1 ? 1 : near < kSnap ? near : kSnap;
           cur.u1 = R.begin(blockIdx.x + 1);
           if (cur.u >= cur.u1) return;
         }
@@ -1162,7 +1174,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
     cur.i = lo;
     const int into = off - begins, n = cur.r.tiles(ManyCursor::fold(lo, cur.pairs));
-    cur.j0 = into == 0 ? 0 : ManyCursor::snap(into, n);
+    cur.j0 = into == 0 ? 0 : cur.snap(into, n);
     cur.u += cur.j0 - into;
     if (!(cur.j0 == n ? cur.following(A) : cur.enter())) return;
   }
@@ -1526,7 +1538,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         // one before them, each have a part of it, and leave it in the
         // workspace: element (column block of 4, row), rows consecutive, so
         // that a warp's accesses are.
-        const ManySplit split(at, units);
+        const ManySplit split(at, units, ctas);
         // Few parts: the last CTA to come adds them, its own out of tensor
         // memory, each row by its thread.  It is nearly always one whose range
         // ends here, and where all others have left theirs before it looks, its
@@ -1582,7 +1594,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       ++ic;
     } while (more);
     if (ok && by_row) {
-      const ManySplit split(at, units);
+      const ManySplit split(at, units, ctas);
       const int own = (int)blockIdx.x - split.c0, prow = sl * TR + r;
       if (!last) ok = ask(true, counters + split.c0, split.pieces, last);
       if (ok && last) {
@@ -1678,7 +1690,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     cur.u = sh.place[which][4];
     cur.j0 = 0;
     cur.r = many_request(A, cur.b);
-    const ManySplit split(cur, units);
+    const ManySplit split(cur, units, ctas);
     const int g = split.group();
     // the rows of the item that are any token's: slot 0's first live0, slot 1's first live1
     const int live0 = (cur.r.n - cur.tok(0) < cur.r.tt ? cur.r.n - cur.tok(0) : cur.r.tt) * A.group;
