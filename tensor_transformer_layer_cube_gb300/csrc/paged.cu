@@ -51,7 +51,7 @@ struct Lengths {
 };
 // The lengths of request b; bad ones take no new tokens.
 __device__ __forceinline__ Lengths plan_lengths(const PlanArgs& P, int b) {
-  Lengths l{__ldg(P.cached + b), __ldg(P.fresh + b), false};
+  Lengths l{ld_plain(P.cached + b), ld_plain(P.fresh + b), false};
   const int64_t cap = P.width << P.page_log2, kv = (int64_t)l.cached + l.fresh;
   if (l.cached < 0 || l.fresh < 0 || kv > cap || kv > kPagedMaxTokens) {
     l.bad = true;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs P) 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool first = blockIdx.x == 0;
   grid_begin();
-  const int64_t count0 = __ldg(P.free_count);
+  const int64_t count0 = ld_plain(P.free_count);
   const int64_t count = count0 < 0 ? 0 : count0 > P.free_cap ? P.free_cap : count0;
 
   bool bad = count != count0;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs P) 
     const int b = last_at_most(sp, P.requests, (int32_t)i);
     const Lengths l = plan_lengths(P, b);
     const int64_t col = pages_of(l.cached, P.page_log2) + (i - sp[b]);
-    P.table[(int64_t)b * P.width + col] = i < count ? __ldg(P.free_pages + (count - 1 - i)) : -1;
+    P.table[(int64_t)b * P.width + col] = i < count ? ld_plain(P.free_pages + (count - 1 - i)) : -1;
   }
   for (int64_t t = tid; t < P.tokens; t += step) {
     int64_t slot = -1;
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs P) 
       const int32_t col = pos >> P.page_log2, old = pages_of(l.cached, P.page_log2);
       const int64_t i = (int64_t)sp[b] + (col - old);  // the step's new page number, if new
       const int32_t page = col < old ? P.table[(int64_t)b * P.width + col]
-                                     : i < count ? __ldg(P.free_pages + (count - 1 - i)) : -1;
+                                     : i < count ? ld_plain(P.free_pages + (count - 1 - i)) : -1;
       if (page >= 0) slot = ((int64_t)page << P.page_log2) + (pos & ((1 << P.page_log2) - 1));
     }
     P.slots[t] = slot;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) paged_store_kernel(const StoreArgs S
       // 32-bit division where it fits: a 64-bit one costs as much as the copy
       const int64_t t = row >> 32 ? row / S.c.kv_heads : (int64_t)((uint32_t)row / (uint32_t)S.c.kv_heads);
       const int h = (int)(row - t * S.c.kv_heads);
-      const int64_t slot = __ldg(S.slots + t), page = slot >> S.page_log2;
+      const int64_t slot = ld_plain(S.slots + t), page = slot >> S.page_log2;
       if (slot < 0) continue;
       if (page >= S.c.pages) {
         raise_error(S.err, TP3D_EPAGES);
@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(kThreads) paged_store_kernel(const StoreArgs S
       }
       to[q] = page * S.c.page_stride + (slot & ((1 << S.page_log2) - 1)) * S.c.token_stride + h * S.c.head_stride + vec;
       const int64_t from = t * S.token_stride + h * S.head_stride + vec;
-      k[q] = __ldg(reinterpret_cast<const uint4*>(S.k + from));
-      v[q] = __ldg(reinterpret_cast<const uint4*>(S.v + from));
+      k[q] = ld_plain(reinterpret_cast<const uint4*>(S.k + from));
+      v[q] = ld_plain(reinterpret_cast<const uint4*>(S.v + from));
     }
 #pragma unroll
     for (int q = 0; q < kStoreVecs; ++q) {

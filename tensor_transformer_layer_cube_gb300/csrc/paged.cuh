@@ -40,6 +40,13 @@ size_t paged_attn_workspace(const tp3d_ctx* ctx, int head_dim);
 // kernel's CTAs have begun by then, so those of the next never hold up its own.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// What an earlier kernel of the stream may have written is read with ordinary
+// loads, which stay behind grid_wait; a read-only one (__ldg) may be moved, and
+// wants data that nothing writes while the kernel runs, which begins early.
+template <class T>
+__device__ __forceinline__ T ld_plain(const T* p) {
+  return *p;
+}
 __device__ __forceinline__ void grid_begin() {
   grid_wait();
   grid_launch_dependents();
@@ -69,7 +76,7 @@ struct PagedRequest {
   int32_t n, kv;
 };
 __device__ __forceinline__ PagedRequest paged_request(const PagedAttn& A, int b) {
-  const int32_t s0 = __ldg(A.q_start + b), s1 = __ldg(A.q_start + b + 1), len = __ldg(A.kv_len + b);
+  const int32_t s0 = ld_plain(A.q_start + b), s1 = ld_plain(A.q_start + b + 1), len = ld_plain(A.kv_len + b);
   const int64_t width = A.width << A.page_log2, cap = width < kPagedMaxTokens ? width : kPagedMaxTokens;
   PagedRequest r;
   const int64_t q0 = s0 < 0 ? 0 : s0 > A.tokens ? A.tokens : s0;

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
         int tiles = 0;  // of the request, per head
         if (c.b < A.requests) {
           c.take(A, alone);
-          tiles = c.tiles * c.blocks(A);
+          if (c.tiles > 0) tiles = c.tiles * c.blocks(A);
         }
         long long x = tiles;
 #pragma unroll
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
         pages_b = ld.b;
         pages_at = ld.tile;
         const int64_t key = (int64_t)(ld.tile + lane) * kKeys + warp * 16;
-        pages = key < ld.kv ? __ldg(A.table + (int64_t)ld.b * A.width + (key >> A.page_log2)) : -1;
+        pages = key < ld.kv ? ld_plain(A.table + (int64_t)ld.b * A.width + (key >> A.page_log2)) : -1;
       }
       const int page = __shfl_sync(0xffffffffu, pages, ld.tile - pages_at);
       const int key = ld.tile * kKeys + warp * 16, left = ld.kv - key;
@@ -402,8 +402,8 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
         const bf16* src = A.q + (c.q0 + tok) * A.q_token + (int64_t)(c.h * A.group + g) * A.q_head + (lane & 3) * 2;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          qf[k][e] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16)) : 0u;
-          qf[k][2 + e] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + k * 16 + 8)) : 0u;
+          qf[k][e] = in ? ld_plain(reinterpret_cast<const uint32_t*>(src + k * 16)) : 0u;
+          qf[k][2 + e] = in ? ld_plain(reinterpret_cast<const uint32_t*>(src + k * 16 + 8)) : 0u;
         }
         m[e] = -INFINITY;
         l[e] = 0.0f;
@@ -1234,7 +1234,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const int key = j * TR + (pi << bl2);
           int32_t page = (int32_t)A.c.pages;
           if (mine && key < cur.r.kv) {
-            page = __ldg(A.table + (int64_t)cur.b * A.width + (key >> A.page_log2));
+            page = ld_plain(A.table + (int64_t)cur.b * A.width + (key >> A.page_log2));
             if (page < 0 || page >= A.c.pages) {
               raise_error(A.err, TP3D_EPAGES);
               page = (int32_t)A.c.pages;

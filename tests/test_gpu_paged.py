@@ -724,3 +724,45 @@ def test_more_rows_than_one_block(ctx, heads, kv_heads, new, d):
     for b in (0, 2):
         hit[int(c.q_start[b]) + new // 2:int(c.q_start[b + 1]), heads - heads // kv_heads:, 7] = True
     assert torch.equal(got[~hit], o[~hit]) and bool(got[hit].isnan().all())
+
+
+@pytest.mark.parametrize("new", [1, 3, 90])
+def test_steps_that_follow_each_other_at_once(ctx, new):
+    # each call reads what the one before it writes (lengths, free count, table, slots, cache, then its output as the
+    # next step's input): back to back they give what they give with the stream drained between any two
+    page, requests, heads, kv_heads, d, steps = 16, 40, 4, 2, 64, 12
+    width = -(-new * steps // page)
+    pages, tokens = requests * width, requests * new
+    fresh, order = i32([new] * requests), np.random.default_rng(new).permutation(pages)
+    free = i32(order)
+    x0 = values(np.random.default_rng(9), (tokens, heads, d)).to(device())
+
+    def run(drain):
+        kp, vp = pool(pages, page, kv_heads, d), pool(pages, page, kv_heads, d)
+        cache = t.kv_cache(kp, vp)
+        table = i32(np.full((requests, width), -1))
+        lens = [i32([0] * requests) for _ in range(steps + 1)]
+        left = [i32([pages]) for _ in range(steps + 1)]
+        q_start, pos = i32([0] * (requests + 1)), i32([0] * tokens)
+        slots = torch.full((tokens,), -1, dtype=torch.int64, device=device())
+        x = [x0] + [torch.zeros_like(x0) for _ in range(steps)]
+        l = [torch.zeros(tokens, heads, device=device()) for _ in range(steps)]
+        ws = torch.empty(t.tp3d_paged_attn_workspace_bytes(ctx, cache, heads), dtype=torch.uint8, device=device())
+        torch.cuda.synchronize()
+        for i in range(steps):
+            for call in (
+                    lambda: t.tp3d_paged_plan(ctx, page, requests, tokens, lens[i], fresh, free, pages, left[i], table,
+                                              width, q_start, lens[i + 1], slots, pos, left[i + 1]),
+                    lambda: t.tp3d_paged_store(ctx, cache, x[i][:, :kv_heads], x[i][:, kv_heads:], slots),
+                    lambda: t.tp3d_paged_attn(ctx, cache, t.paged_batch(q_start, lens[i + 1], table, tokens, new), x[i],
+                                              x[i + 1], l[i], 1.0, ws)):
+                t.check(call())
+                if drain:
+                    torch.cuda.synchronize()
+        assert t.tp3d_sync_status(ctx) == 0
+        return [table, *lens, *left, *(y.view(torch.int16) for y in x), *l]
+
+    want = run(True)
+    for _ in range(3):
+        for got, w in zip(run(False), want):
+            assert torch.equal(got, w)
