@@ -24,10 +24,10 @@ namespace {
 // faster than HBM delivers them.
 //
 // Work is counted in tiles of 64 or 128 keys of one item (request, key/value
-// head, 16 rows), request by request, head by head; the CTAs take equal contiguous ranges of
-// that sequence, so one long request and many short ones balance alike and
-// nothing about the lengths is needed on the host.  Each of a CTA's warps
-// takes 16 keys of every tile - one page holds them all - through a ring of
+// head, 16 rows), request by request, head by head; the CTAs take equal
+// contiguous ranges of that sequence, so one long request and many short ones
+// balance alike and nothing about the lengths is needed on the host.  Each of a
+// CTA's warps takes 16 keys of every tile - one page holds them all - through a ring of
 // its own, with 16-byte asynchronous copies and no barrier between the warps:
 // a warp refills a stage as soon as it has read it, which keeps two of three
 // stages in flight (keys past the request are zero-filled, so stale contents
