@@ -29,8 +29,10 @@ namespace {
 // balance alike and nothing about the lengths is needed on the host.  Each of a
 // CTA's warps takes 16 keys of every tile - one page holds them all - through a ring of
 // its own, with 16-byte asynchronous copies and no barrier between the warps:
-// a warp refills a stage as soon as it has read it, which keeps two of three
-// stages in flight (keys past the request are zero-filled, so stale contents
+// a warp refills a stage as soon as it has read it, which keeps one of two
+// stages in flight, 64 KiB an SM; with three the same bytes come more slowly (32
+// requests of up to 16384 keys 190 us against 182, one of 131071 91.9 against
+// 87.5, short calls the same) (keys past the request are zero-filled, so stale contents
 // never reach a product).  Each keeps its own running maximum (in base-2
 // units; moved only when exceeded by more than 2^8, which leaves the
 // probabilities far from overflow), row sums and O in registers; they are
@@ -44,39 +46,41 @@ namespace {
 // time, so what runs once is written as rolled loops, and loads are issued in
 // one place.
 //
-// Measured, of a stream of calls: 32 requests of up to 4096 keys, 16 heads of
-// 128 (539 MB): 96.7 us, 5.6 TB/s, 0.84 of the copy rate; DRAM reads are the
-// cache's bytes and no more, issue slots 34 % busy.  32 of up to 16384, grouped:
-// 191 us, 0.93.  A call of one tile: 4.7 us, of which 0.8 is the launch, 0.9
-// the lengths, 2 the table's page and then its keys; a cut item adds 3 for its
-// parts' way through L2.
+// Measured, of a stream of calls: 32 requests of up to 16384 keys, 32 heads on 8,
+// pages of 64 with the heads outside (1185 MB): 182 us, 6.5 TB/s, 0.97 of the
+// copy rate.  32 of up to 4096, 16 heads, pages of 16 with the tokens outside
+// (539 MB): 96 us, 0.84: rows of 256 bytes 4 KiB apart, and the ends of 512
+// items.  DRAM reads are the cache's bytes and no more.  A call of one tile: 4.7
+// us, of which 0.8 is the launch, 0.9 the lengths, 2 the table's page and then
+// its keys; a cut item adds 3 for its parts' way through L2.
 //
 // W warps a CTA, 8 / W CTAs an SM.  Four: one CTA's end of an item falls
 // together with another's loads.  Eight: fewer parts to an item and fewer steps
 // to a part, where the items are too few to give every SM its own.  4 | 8
-// warps: 16 items of 1024 keys 9.8 | 8.4 us, 16 of 3000 13.0 | 10.5, 8 of
-// 131072 95.4 | 92.3; 128 items of 1024 13.5 | 14.8, 512 of 4096 96.6 | 110.
+// warps: 16 items of 1024 keys 9.7 | 8.4 us, 16 of 3000 12.9 | 10.6, 64 of 1024
+// 11.5 | 9.8, 8 of 131072 88.2 | 87.6; 128 items of 1024 13.3 | 15.0, 96 of 2000
+// 15.5 | 20.0, 512 of 4096 96 | 107.
 template <int W>
 struct FewShape {
   static constexpr int kThreads = 32 * W;
   static constexpr int kKeys = 16 * W;  // of a tile
   static constexpr int kPerSm = 8 / W;
-  // tiles of a CTA's range, where there is little work (16 items of 1024 keys, four warps: 9.8 us; with 2 10.3, with
-  // 6 12.6; eight warps: 8.4 us; with 1 9.2, with 3 10.1)
+  // tiles of a CTA's range, where there is little work (16 items of 1024 keys, four warps: 9.7 us; with 2 10.3, with
+  // 6 12.6; eight warps: 8.4 us; with 1 9.1, with 3 10.2)
   static constexpr int kMinTiles = 16 / W;
   // Rows of a request that this kernel takes, in blocks of 16 (items of their
   // own, side by side, so that a block finds the others' keys in L2).  Here | in
   // the kernel for many rows, eight warps: 4 requests of 2000 keys, 4 heads, 24
-  // rows 12.4 | 25.3 us, 48 rows 11.6 | 26.7; one of 65536, 4 heads, 24 rows 41 |
-  // 58, 48 rows 60.9 | 61.1, 64 rows 72.6 | 61.5.  Four warps: 64 of 500, 8 heads
+  // rows 12.5 | 19.0 us, 48 rows 11.6 | 20.5; one of 65536, 4 heads, 24 rows 42 |
+  // 58, 48 rows 61.5 | 61.5, 64 rows 72.6 | 62.2.  Four warps: 64 of 500, 8 heads
   // of 64, 16 rows 21.8 | 38.2, 20 rows 25.3 | 27.4; 32 of 4000, 8 heads, 32 rows
   // 106.7 | 94.8; 16 of 2000, 16 heads, 30 rows 68.8 | 52.9.
   static constexpr int kRows = W == 8 ? 48 : 16;
   static constexpr int kSnap = 8 / W;  // a range boundary this near an item's edge moves there: parts cost more
 };
 constexpr int kFewRows = 16;  // of an item: one mma.sync tile
-constexpr int kFewStages = 3;
-constexpr int kJoinOnce = 16;    // parts of an item joined in one step
+constexpr int kFewStages = 2;  // of a warp's ring
+constexpr int kJoinOnce = 16;    // parts of an item joined in one step (8 heads of 64, 60000 keys: 13.2 us; all 152 at once 30.1)
 constexpr int kFewSlots = 4;     // parts that a CTA has room for in the workspace
 constexpr float kMoveLog2 = 8.0f;
 
@@ -748,7 +752,7 @@ static_assert(kManySmem <= 232448, "shared memory of one CTA");
 // tokens over 3000) 47.1 | 45.9 us; 19 parts (5 tokens, 65536 keys, 8 heads)
 // 122 | 77 us.
 constexpr int kManyByRow = 3;
-constexpr int kManyJoinOnce = 8;  // parts of an item joined in one step
+constexpr int kManyJoinOnce = 8;  // parts of an item joined in one step (500 tokens over 8192, 5 parts: 73.8 us; with 4 78.5)
 constexpr int kManySlots = 4;     // parts that a CTA has room for in the workspace
 TP3D_HD constexpr size_t many_part_floats(int d) { return (size_t)2 * TR * (d + 2); }
 
