@@ -49,10 +49,10 @@ namespace {
 // Measured, of a stream of calls: 32 requests of up to 16384 keys, 32 heads on 8,
 // pages of 64 with the heads outside (1185 MB): 182 us, 6.5 TB/s, 0.97 of the
 // copy rate.  32 of up to 4096, 16 heads, pages of 16 with the tokens outside
-// (539 MB): 96 us, 0.84: rows of 256 bytes 4 KiB apart, and the ends of 512
-// items.  DRAM reads are the cache's bytes and no more.  A call of one tile: 4.7
-// us, of which 0.8 is the launch, 0.9 the lengths, 2 the table's page and then
-// its keys; a cut item adds 3 for its parts' way through L2.
+// (539 MB): 87 us, 0.93: rows of 256 bytes 4 KiB apart.  DRAM reads are the
+// cache's bytes and no more.  A call of one tile: 4.7 us, of which 0.8 is the
+// launch, 0.9 the lengths, 2 the table's page and then its keys; a cut item adds
+// 3 for its parts' way through L2.
 //
 // W warps a CTA, 8 / W CTAs an SM.  Four: one CTA's end of an item falls
 // together with another's loads.  Eight: fewer parts to an item and fewer steps
@@ -77,7 +77,7 @@ struct FewShape {
   // 106.7 | 94.8; 16 of 2000, 16 heads, 30 rows 68.8 | 52.9.
   static constexpr int kRows = W == 8 ? 48 : 16;
   // The end of an item counts as so many tiles in the ranges, about what it costs.  With it | without, four warps:
-  // 32 requests of up to 4096 keys, 16 heads 85 | 94 us; 100 of 700 41.8 | 60.9; 200 of 2000, 8 heads 127 | 145 (1:
+  // 32 requests of up to 4096 keys, 16 heads 85 | 94 us (one box); 100 of 700 41.8 | 60.9; 200 of 2000, 8 heads 127 | 145 (1:
   // 131, 3: 128).  With eight an item has several CTAs.
   static constexpr int kEnd = W == 8 ? 0 : 2;
   static constexpr int kSnap = 8 / W;  // a range boundary this near an item's edge moves there: parts cost more
