@@ -1693,6 +1693,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     if (!sh.join[which]) continue;
+    // the first join ends without a barrier, and its slower warps still read the weights that this one replaces
+    if (which && sh.join[0]) row_warps_meet();
     cur.b = sh.place[which][0];
     cur.h = sh.place[which][1];
     cur.k = sh.place[which][2];

@@ -1,0 +1,66 @@
+"""Attention over the paged cache: what several threads, CTAs and calls do with
+the same memory.  Results are compared bit for bit where only the order in
+which things happen differs, and once with the definition in float64 (the
+tolerances are those of test_gpu_paged.py)."""
+import pytest
+import torch
+
+import tensor_transformer_layer_cube_gb300 as t
+from tests.gpu_util import device
+from tests.test_gpu_paged import Case, compare
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    c = t.tp3d_create(0)
+    yield c
+    t.tp3d_destroy(c)
+
+
+def want64(c):
+    """oracle.paged.attention's results by torch on the GPU, for lengths that would take numpy minutes."""
+    tokens, heads, d = c.q.shape
+    g = heads // c.kv_heads
+    o, absum = (torch.zeros(tokens, heads, d, dtype=torch.float64, device=device()) for _ in range(2))
+    lse = torch.full((tokens, heads), -torch.inf, dtype=torch.float64, device=device())
+    amax = torch.zeros(tokens, heads, dtype=torch.float64, device=device())
+    for b, kv in enumerate(int(x) for x in c.kv):
+        q0, q1 = int(c.q_start[b]), int(c.q_start[b + 1])
+        ids = torch.from_numpy(c.table[b, :-(-kv // c.page)]).to(device())
+        last = kv - (q1 - q0) + torch.arange(q1 - q0, device=device())
+        hidden = torch.arange(kv, device=device()) > last[:, None]
+        for i in range(heads):
+            k, v = (p[ids, :, i // g].flatten(0, 1)[:kv].double() for p in (c.kp, c.vp))
+            q = c.q[q0:q1, i].double()
+            s = (c.scale * (q @ k.T)).masked_fill(hidden, -torch.inf)
+            lse[q0:q1, i] = s.logsumexp(1)
+            p = (s - lse[q0:q1, i, None]).exp()
+            o[q0:q1, i], absum[q0:q1, i] = p @ v, p @ v.abs()
+            amax[q0:q1, i] = c.scale * (q.abs() @ k.abs().T).masked_fill(hidden, 0).amax(1)
+    return [x.cpu().numpy() for x in (o, lse, absum, amax)]
+
+
+# One CTA ends up to two split items after its range: the one that its range begins in and the one that it ends in.
+# Fewer than 256 rows of each pair of tiles are some token's, so the rows of the join are dealt to other threads than
+# those that weigh them.  (heads, keys, rows a head): CTAs of 152 that may end both, parts of their items: 2 with 3 and
+# 4; 3 with 19 and 20, joined in two levels; 15 with 7 and 7; 1 with 8 and 8
+@pytest.mark.parametrize("kv,new,heads", [([8192], [200], 64), ([65536], [200], 8), ([24000], [100], 24),
+                                          ([9000, 7000, 8000], [200, 130, 256], 8)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_two_items_ended_by_one_cta(ctx, kv, new, heads, d):
+    c = Case(kv, new, heads, heads, d, 64, seed=heads, v_mean=0.5)
+    o, l = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    compare(c, o, l, want64(c))
+    # blocks of different lengths beside it hold the SMs for a while: CTAs that start late arrive last at both items
+    x = torch.rand(140, 1 << 22, device=device())
+    side = torch.cuda.Stream()
+    for i in range(40):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            x[:1 + 19 * (i % 8)].softmax(1)
+        o2, l2 = c.run(ctx)
+        assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(l, l2)
+    assert t.tp3d_sync_status(ctx) == 0
