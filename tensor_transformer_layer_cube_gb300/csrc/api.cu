@@ -84,6 +84,11 @@ static tp3d_layout layout_of(int kind, int a, int b) {
   return l;
 }
 
+// cudaMemset of device memory, and cudaMemcpy to it from pageable memory, may
+// return before the device has run them, and a non-blocking stream does not
+// wait for the legacy stream that they run on.  This waits for them.
+static bool legacy_done() { return cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess; }
+
 // The context's scratch, at least `bytes` long.  Growing it waits for the
 // device (an earlier launch may still use the old one) and zeroes the new one.
 tp3d_status ctx_scratch(tp3d_ctx* ctx, size_t bytes, void** out) {
@@ -96,7 +101,7 @@ tp3d_status ctx_scratch(tp3d_ctx* ctx, size_t bytes, void** out) {
     }
     void* p = nullptr;
     TP3D_CUDA_TRY(cudaMalloc(&p, bytes));
-    if (cudaMemset(p, 0, bytes) != cudaSuccess) {
+    if (cudaMemset(p, 0, bytes) != cudaSuccess || !legacy_done()) {
       cudaFree(p);
       return TP3D_ECUDA;
     }
@@ -128,7 +133,7 @@ tp3d_status tp3d_create(int device, tp3d_ctx** out) {
       cudaMalloc(&c->d_err, sizeof(init)) != cudaSuccess ||
       cudaMemcpy(c->d_err, init, sizeof(init), cudaMemcpyHostToDevice) != cudaSuccess ||
       cudaMalloc(&c->d_paged, kPagedCounters * sizeof(unsigned)) != cudaSuccess ||
-      cudaMemset(c->d_paged, 0, kPagedCounters * sizeof(unsigned)) != cudaSuccess) {
+      cudaMemset(c->d_paged, 0, kPagedCounters * sizeof(unsigned)) != cudaSuccess || !legacy_done()) {
     if (c->d_err) cudaFree(c->d_err);
     if (c->d_paged) cudaFree(c->d_paged);
     free(c);
@@ -191,9 +196,14 @@ tp3d_status tp3d_sync_status(tp3d_ctx* ctx, void* stream) {
   if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return TP3D_ECUDA;
   int e = 0;
   if (cudaMemcpy(&e, ctx->d_err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return TP3D_ECUDA;
-  if (e != 0 && cudaMemset(ctx->d_err, 0, sizeof(int)) != cudaSuccess) return TP3D_ECUDA;
-  // a launch that gave up (and perhaps raised something else before) leaves its split items' counts unfinished
-  if (e != 0 && cudaMemset(ctx->d_paged, 0, kPagedCounters * sizeof(unsigned)) != cudaSuccess) return TP3D_ECUDA;
+  if (e == 0) return TP3D_OK;
+  // On the caller's stream, and waited for: the next call may follow at once,
+  // there or elsewhere.  (A launch that gave up, and perhaps raised something
+  // else before, leaves its split items' counts unfinished.)
+  if (cudaMemsetAsync(ctx->d_err, 0, sizeof(int), as_stream(stream)) != cudaSuccess ||
+      cudaMemsetAsync(ctx->d_paged, 0, kPagedCounters * sizeof(unsigned), as_stream(stream)) != cudaSuccess ||
+      cudaStreamSynchronize(as_stream(stream)) != cudaSuccess)
+    return TP3D_ECUDA;
   return static_cast<tp3d_status>(e);
 }
 
@@ -201,7 +211,7 @@ tp3d_status tp3d_set_wait_limit_ns(tp3d_ctx* ctx, uint64_t ns) {
   if (!ctx) return TP3D_EINVAL;
   const unsigned long long lim = ns ? (unsigned long long)ns : kWaitLimitNs;
   if (cudaSetDevice(ctx->device) != cudaSuccess ||
-      cudaMemcpy(ctx->d_err + 2, &lim, sizeof(lim), cudaMemcpyHostToDevice) != cudaSuccess)
+      cudaMemcpy(ctx->d_err + 2, &lim, sizeof(lim), cudaMemcpyHostToDevice) != cudaSuccess || !legacy_done())
     return TP3D_ECUDA;
   return TP3D_OK;
 }

@@ -64,3 +64,48 @@ def test_two_items_ended_by_one_cta(ctx, kv, new, heads, d):
         o2, l2 = c.run(ctx)
         assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(l, l2)
     assert t.tp3d_sync_status(ctx) == 0
+
+
+def with_bad_page(c):
+    """The case's batch with one table entry outside the pool."""
+    table = c.dev[2].clone()
+    table[0, 1] = -1
+    return t.paged_batch(c.dev[0], c.dev[1], table, c.tokens, int(max(c.new))), table
+
+
+@pytest.mark.parametrize("new", [1, 200])
+def test_split_work_right_after_an_error_on_its_stream(ctx, new):
+    # reading the status clears the error and the counters of split items: done when the next call's CTAs count on them
+    c = Case([9000], [new], 4, 4, 128, 64, seed=3)
+    want, wl = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    bad, table = with_bad_page(c)
+    good, o, l = c.batch(), torch.empty_like(want), torch.empty_like(wl)
+    junk = torch.empty_like(want)
+    busy = torch.rand(64, 1 << 20, device=device())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(40):
+        o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        t.check(t.tp3d_paged_attn(ctx, c.cache, bad, c.q, junk, None, c.scale, c.ws, side))
+        busy.softmax(1)  # on the legacy stream, which the side stream does not wait for
+        assert t.STATUS[t.tp3d_sync_status(ctx, side)] == "TP3D_EPAGES"
+        t.check(t.tp3d_paged_attn(ctx, c.cache, good, c.q, o, l, c.scale, c.ws, side))
+        assert t.tp3d_sync_status(ctx, side) == 0
+        assert torch.equal(o.view(torch.int16), want.view(torch.int16)) and torch.equal(l, wl)
+
+
+def test_first_call_of_a_context_on_a_side_stream():
+    # a new context's counters and error word are zero before its first call on a stream that waits for no other
+    c = Case([9000], [200], 4, 4, 128, 64, seed=3)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        x = t.tp3d_create(0)
+        got.append(c.run(x, stream=side))
+        assert t.tp3d_sync_status(x, side) == 0
+        t.tp3d_destroy(x)
+    for o, l in got[1:]:
+        assert torch.equal(o.view(torch.int16), got[0][0].view(torch.int16)) and torch.equal(l, got[0][1])
