@@ -738,10 +738,11 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
 constexpr int kManyThreads = 384;
 constexpr int kManyRegsLow = 120, kManyRegsHigh = 192;  // 128 x 120 + 256 x 192 <= 384 x 168; no spills
 constexpr uint32_t kManyRing = 5;
-constexpr int kNotes = 4;  // items whose values may be under check or in use at once
+constexpr int kNotes = 4;  // pieces whose values may be under check or in use at once
 struct ManyShared {
   unsigned notes[kNotes][64];    // per column (16 bits): first non-finite masked key - first row's last key
   int noted[kNotes][2];          // by value-check warp
+  volatile unsigned ended[8];    // pieces that each row warp has ended: their notes may be begun anew
   int last;
   long long scan[kManyThreads / 32];
   int before, per_head;
@@ -993,6 +994,28 @@ __device__ __forceinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, cons
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
+// The value check goes on to piece p, and may begin its notes, when every row warp has ended
+// piece p - kNotes, whose notes lay in their place.  (A slot whose query tile
+// is empty does not hold the other up: its row warps may be pieces behind.)
+// Bounded as wait_on.
+__device__ __forceinline__ bool notes_free(const volatile unsigned* ended, uint32_t piece, const Ctx& c, int* err,
+                                           int lane) {
+  const auto is = [&] { return __all_sync(0xffffffffu, lane >= 8 || ended[lane & 7] + kNotes > piece) != 0; };
+  bool free = is();
+  const unsigned long long t0 = free ? 0 : globaltimer_ns();
+  while (!free) {
+    __nanosleep(200);
+    if (__any_sync(0xffffffffu, *c.abort_flag || globaltimer_ns() - t0 > wait_limit_ns(err))) break;
+    free = is();
+  }
+  if (!free && lane == 0 && !*c.abort_flag) {
+    *c.abort_flag = 1;
+    raise_error(err, TP3D_ETIMEOUT);
+  }
+  __threadfence_block();
+  return free;
+}
+
 // One key tile of one row: its 128 scores at `s` in tensor memory become P
 // there (per 32 columns: 16 of hi pairs, 16 of lo pairs), the running maximum
 // m (base-2 units) and sum l are updated and, when some row of the warp has to
@@ -1198,6 +1221,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
     *c.abort_flag = 0;
     sh.left[0] = sh.left[1] = sh.join[0] = sh.join[1] = 0;
+    for (int w = 0; w < 8; ++w) sh.ended[w] = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -1386,6 +1410,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       uint32_t ic = 0;
       bool ok = true;
       do {
+        if (!(ok = notes_free(sh.ended, ic, c, A.err, lane))) break;
         const int seen = cur.r.kv - cur.r.n + cur.tok(0);  // the first row's last key
         unsigned* const notes = sh.notes[ic % kNotes] + w * (NV * 4);
         bool noting = false;
@@ -1602,6 +1627,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         warp_arrive(o_empty(sl), lane);
       }
       ++ic;
+      if (lane == 0) {
+        __threadfence_block();
+        sh.ended[warp - 4] = ic;
+      }
     } while (more);
     if (ok && by_row) {
       const ManySplit split(at, units, ctas);

@@ -109,3 +109,23 @@ def test_first_call_of_a_context_on_a_side_stream():
         t.tp3d_destroy(x)
     for o, l in got[1:]:
         assert torch.equal(o.view(torch.int16), got[0][0].view(torch.int16)) and torch.equal(l, got[0][1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_that_are_not_finite_behind_pieces_of_one_query_tile(ctx, d):
+    # notes of values that are not finite, in a CTA that goes on with many pieces whose second query tile is empty: the
+    # first requests have two query tiles, the others one, and most have a NaN or an infinity that only some rows see
+    kv, new = [260, 300, 200] + [40 + i % 50 for i in range(700)], [200, 256, 130] + [17 + i % 7 for i in range(700)]
+    c = Case(kv, new, 4, 4, d, seed=21, v_mean=0.5)
+    clean, cl = c.run(ctx)
+    hit = torch.zeros_like(clean, dtype=torch.bool)
+    for b in range(len(kv)):
+        if b % 3 == 2:
+            continue
+        pos, head, col = kv[b] - 1 - b % 7, b % 4, (b * 5) % d
+        c.vp[int(c.table[b, pos // 16]), pos % 16, head, col] = float("nan") if b % 2 else float("inf")
+        hit[int(c.q_start[b]) + pos - (kv[b] - new[b]):int(c.q_start[b + 1]), head, col] = True
+    for _ in range(20):
+        o, l = c.run(ctx)
+        assert torch.equal(l, cl) and torch.equal(o[~hit], clean[~hit]) and not bool(o[hit].isfinite().any())
+    assert t.tp3d_sync_status(ctx) == 0
