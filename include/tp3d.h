@@ -131,8 +131,10 @@ tp3d_status tp3d_set_wait_limit_ns(tp3d_ctx* ctx, uint64_t ns);
 
 /* Test hook for the timeout path: from now on, the GEMM kernels of this
  * context's calls stop loading operands after `stages` contraction stages of
- * each launch (after letting the loads they issued land), so the tensor-core
- * issuer's next wait can only run out (-1 turns the hook off; the default).
+ * each launch, and each CTA of tp3d_paged_attn's kernel for many rows after
+ * `stages` key and value tiles (after letting the loads they issued land), so
+ * the tensor-core issuer's next wait can only run out (-1 turns the hook off;
+ * the default).
  * Host-side state only; TP3D_EINVAL for stages < -1.                         */
 tp3d_status tp3d_inject_load_stall(tp3d_ctx* ctx, int64_t stages);
 

@@ -17,7 +17,9 @@ struct tp3d_ctx {
   // d_err[2..3] = the bounded waits' limit in nanoseconds (a uint64)
   int* d_err;
   // test hook: the GEMM producers stop loading after this many contraction
-  // stages of each launch (-1: never), so that the issuer's next wait runs out
+  // stages of each launch, those of the paged attention's kernel for many rows
+  // after this many key and value tiles of each CTA (-1: never), so that the
+  // issuer's next wait runs out
   int64_t stall_after;
   // two side streams and their events, for independent launches of one call
   // that run beside the caller's stream (forked from it and joined back into

@@ -400,6 +400,7 @@ tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3
   A.o_head = o_strides.head_stride;
   A.lse = lse;
   A.err = ctx->d_err;
+  A.stall_after = ctx->stall_after;
   return launch_paged_attn(ctx, A, batch->max_new, workspace, as_stream(stream));
 }
 

@@ -26,6 +26,7 @@ struct PagedAttn {
   int64_t o_token, o_head;
   float* lse;  // or null
   int* err;
+  int64_t stall_after;  // test hook: the many-rows kernel's CTAs load this many key and value tiles each (-1: all)
 };
 
 tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* workspace, cudaStream_t s);
