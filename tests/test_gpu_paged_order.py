@@ -129,3 +129,65 @@ def test_values_that_are_not_finite_behind_pieces_of_one_query_tile(ctx, d):
         o, l = c.run(ctx)
         assert torch.equal(l, cl) and torch.equal(o[~hit], clean[~hit]) and not bool(o[hit].isfinite().any())
     assert t.tp3d_sync_status(ctx) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_mixed_steps_that_follow_each_other_at_once(ctx, d):
+    # requests with one token and with many in every step, so both kernels of a call run beside each other and read what
+    # the kernel before them has just written: back to back, and captured and replayed, they give what they give with
+    # the stream drained between any two calls
+    page, requests, heads, kv_heads, steps = 16, 24, 4, 2, 8
+    new = [70 if b % 6 == 0 else 1 for b in range(requests)]
+    width, tokens = -(-70 * steps // page), sum(new)
+    pages = requests * width
+    gen = torch.Generator(device=device()).manual_seed(d)
+    fresh = torch.tensor(new, dtype=torch.int32, device=device())
+    free = torch.randperm(pages, generator=gen, device=device()).int()
+    x0 = torch.empty(tokens, heads, d, dtype=torch.bfloat16, device=device()).normal_(generator=gen)
+
+    def buffers():
+        k, v = (torch.zeros(pages, page, kv_heads, d, dtype=torch.bfloat16, device=device()) for _ in range(2))
+        z = {"dtype": torch.int32, "device": device()}
+        return {"k": k, "v": v, "cache": t.kv_cache(k, v), "table": torch.full((requests, width), -1, **z),
+                "lens": torch.zeros(steps + 1, requests, **z), "left": torch.full((steps + 1, 1), pages, **z),
+                "q_start": torch.zeros(requests + 1, **z), "pos": torch.zeros(tokens, **z),
+                "slots": torch.zeros(tokens, dtype=torch.int64, device=device()),
+                "x": torch.cat([x0[None], torch.zeros(steps, tokens, heads, d, dtype=x0.dtype, device=device())]),
+                "l": torch.zeros(steps, tokens, heads, device=device())}
+
+    def run(s, ws, drain):
+        for i in range(steps):
+            batch = t.paged_batch(s["q_start"], s["lens"][i + 1], s["table"], tokens, 70)
+            for call in (
+                    lambda: t.tp3d_paged_plan(ctx, page, requests, tokens, s["lens"][i], fresh, free, pages, s["left"][i],
+                                              s["table"], width, s["q_start"], s["lens"][i + 1], s["slots"], s["pos"],
+                                              s["left"][i + 1]),
+                    lambda: t.tp3d_paged_store(ctx, s["cache"], s["x"][i, :, :kv_heads], s["x"][i, :, kv_heads:], s["slots"]),
+                    lambda: t.tp3d_paged_attn(ctx, s["cache"], batch, s["x"][i], s["x"][i + 1], s["l"][i], 1.0, ws)):
+                t.check(call())
+                if drain:
+                    torch.cuda.synchronize()
+
+    def same(a, b):
+        return all(torch.equal(a[n].view(torch.uint8), b[n].view(torch.uint8)) for n in ("table", "lens", "left", "x", "l"))
+
+    want, got, blank = buffers(), buffers(), buffers()
+    ws = torch.empty(t.tp3d_paged_attn_workspace_bytes(ctx, want["cache"], heads), dtype=torch.uint8, device=device())
+    run(want, ws, True)
+    assert t.tp3d_sync_status(ctx) == 0
+
+    def reset():
+        for n, x in blank.items():
+            if isinstance(x, torch.Tensor):
+                got[n].copy_(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(got, ws, False)
+    for i in range(12):
+        reset()
+        if i % 2:
+            graph.replay()
+        else:
+            run(got, ws, False)
+        assert t.tp3d_sync_status(ctx) == 0
+        assert same(got, want)
