@@ -33,7 +33,7 @@ struct tp3d_ctx {
   size_t scratch_bytes;
   // arrival counters of the paged attention's split items (zero between calls)
   unsigned* d_paged;
-  int paged_ready;  // head sizes whose paged attention kernels are set up (bits)
+  int paged_ready;  // paged kernels that are set up (bits: attention with heads of 128, of 64, plans of many requests)
   // CUDA graphs of whole layer calls keyed by their arguments (graph.cu), the
   // stream they run on, and the events that order it with the caller's stream
   void* graphs;

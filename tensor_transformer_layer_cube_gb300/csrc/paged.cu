@@ -29,6 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kScanItems = 4;
 constexpr int kScanChunk = kThreads * kScanItems;
 constexpr int kPlanMaxRequests = 16384;
+constexpr int kPlanReady = 4;  // of tp3d_ctx::paged_ready
 
 struct PlanArgs {
   int page_log2, requests;
@@ -319,8 +320,12 @@ tp3d_status tp3d_paged_plan(tp3d_ctx* ctx, int page, int requests, int64_t token
   const PlanArgs P{pl, requests, tokens, cached, fresh, free_pages, free_cap, free_count, block_table, table_width,
                    q_start, kv_len, slots, positions, free_left, ctx->d_err};
   const size_t smem = ((size_t)requests + 1) * 8;
-  if (smem > 48 * 1024)
-    TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  // The limit is the function's, and so every context's and host thread's: set to the largest size once, never lowered.
+  if (smem > 48 * 1024 && !(ctx->paged_ready & kPlanReady)) {
+    TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (kPlanMaxRequests + 1) * 8));
+    ctx->paged_ready |= kPlanReady;
+  }
   return launch_dependent(paged_plan_kernel, blocks(ctx, tokens, 1), kThreads, smem, as_stream(stream), P);
 }
 

@@ -2,6 +2,8 @@
 the same memory.  Results are compared bit for bit where only the order in
 which things happen differs, and once with the definition in float64 (the
 tolerances are those of test_gpu_paged.py)."""
+import threading
+
 import pytest
 import torch
 
@@ -191,3 +193,32 @@ def test_mixed_steps_that_follow_each_other_at_once(ctx, d):
             run(got, ws, False)
         assert t.tp3d_sync_status(ctx) == 0
         assert same(got, want)
+
+
+def test_plans_of_many_requests_from_several_host_threads():
+    # a context and a thread each, batches that need different amounts of shared memory, at the same time
+    def step(requests):
+        z = {"dtype": torch.int32, "device": device()}
+        fresh = torch.ones(requests, **z)
+        return [16, requests, requests, torch.zeros(requests, **z), fresh, torch.arange(requests, **z), requests,
+                torch.full((1,), requests, **z), torch.zeros(requests, 1, **z), 1, torch.zeros(requests + 1, **z),
+                torch.zeros(requests, **z), torch.zeros(requests, dtype=torch.int64, device=device()),
+                torch.zeros(requests, **z), torch.zeros(1, **z)]
+
+    statuses = {}
+
+    def serve(requests):
+        ctx, args, stream = t.tp3d_create(0), step(requests), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        # the C call with its arguments ready, so that the threads spend their time in it
+        plan, raw = t.lib().tp3d_paged_plan, [x if isinstance(x, int) else x.data_ptr() for x in args]
+        got = {plan(ctx, *raw, stream.cuda_stream) for _ in range(20000)}
+        statuses[requests] = {t.STATUS[x] for x in got | {t.tp3d_sync_status(ctx, stream.cuda_stream)}}
+        t.tp3d_destroy(ctx)
+
+    threads = [threading.Thread(target=serve, args=(n,)) for n in (16384, 8000, 12000)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert statuses == {n: {"TP3D_OK"} for n in (16384, 8000, 12000)}
