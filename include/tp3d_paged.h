@@ -117,7 +117,8 @@ tp3d_status tp3d_paged_store(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t 
  * values past kv_b, and whatever else lies in a page, have no effect on the
  * result (NaN and infinities among it); nor has a later token's value on the
  * rows before it in its chunk.  A row that does see a value that is not finite
- * gets NaN or an infinity in its column.  Q and O rows: token t, head i at
+ * gets NaN or an infinity in its column; one whose scores are all -infinity
+ * gets NaN (0 / 0) everywhere and lse = -infinity.  Q and O rows: token t, head i at
  * element t * token_stride + i * head_stride of each; O is written in bf16,
  * lse (or NULL) as float32 [tokens][heads].  Rows from q_start[requests] on
  * are not written.  A block table entry outside the pool raises TP3D_EPAGES;

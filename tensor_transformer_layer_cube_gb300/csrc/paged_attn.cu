@@ -176,6 +176,13 @@ __device__ __forceinline__ uint4 make_finite(const uint4& x, const Note& note) {
   return make_uint4(e[0], e[1], e[2], e[3]);
 }
 
+// What a row's unnormalised O is multiplied by.  A sum of 0 is a row without
+// keys (`last` < 0, the last key it sees), whose O is 0, or one that sees
+// nothing but scores of -infinity: 0 / 0.
+__device__ __forceinline__ float normaliser(float sum, int last) {
+  return sum != 0.0f ? 1.0f / sum : last < 0 ? 0.0f : __int_as_float(0x7fffffff);
+}
+
 // The CTAs' equal contiguous shares of a sequence of units, and the CTA whose
 // share unit u falls in.  In 32 bits: a call of 2^31 tiles or more raises
 // TP3D_EPAGES instead (64-bit division costs a short call a microsecond).
@@ -592,7 +599,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
         const int tok = (c.row0 + r) / A.group;
         const int64_t t = c.q0 + tok;
         const int head = c.h * A.group + (c.row0 + r - tok * A.group);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = normaliser(sum, c.kv - c.n + tok);
         *reinterpret_cast<uint2*>(A.o + t * A.o_token + (int64_t)head * A.o_head + col) =
             make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
         if (A.lse && col == 0)
@@ -1601,7 +1608,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       at = cur;
       more = cur.next(A);
       if (at.j0 == 0 && at.j1 == at.nkv) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = normaliser(l, lim);
         const int64_t row = (int64_t)at.r.q0 + token;
         const int head = at.h * A.group + g;
         bf16* const dst = A.o + row * A.o_token + (int64_t)head * A.o_head;
@@ -1649,7 +1656,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         if (live) {
           __stcg(part + (size_t)2 * TR * D + prow, m);
-          __stcg(part + (size_t)2 * TR * (D + 1) + prow, l);
+          __stcg(part + (size_t)2 * TR * (D + 1) + prow, cnt > 0 ? l : -1.0f);  // -1: no O has been left
         }
         if (by_row) break;
         __syncwarp();
@@ -1689,7 +1696,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         const int64_t row = (int64_t)at.r.q0 + at.tok(sl) + tok;
         const int head = at.h * A.group + g;
         bf16* const dst = A.o + row * A.o_token + (int64_t)head * A.o_head;
-        // the weights of this row's parts first (0: without a key, and perhaps without O)
+        // the weights of this row's parts first (a sum below 0: there is no O)
         constexpr int kOthers = kManyByRow - 1;
         const auto other = [&](int i) { return split.part(parts, pf, i + (i >= own ? 1 : 0)); };
         float om[kOthers], ol[kOthers], top = m, sum = 0.0f;
@@ -1697,26 +1704,26 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         for (int i = 0; i < kOthers; ++i) {
           const bool in = live && i < split.pieces - 1;
           om[i] = in ? __ldcg(other(i) + (size_t)2 * TR * D + prow) : -INFINITY;
-          ol[i] = in ? __ldcg(other(i) + (size_t)2 * TR * (D + 1) + prow) : 0.0f;
+          ol[i] = in ? __ldcg(other(i) + (size_t)2 * TR * (D + 1) + prow) : -1.0f;
         }
 #pragma unroll
         for (int i = 0; i < kOthers; ++i) top = fmaxf(top, om[i]);
         const float tb = top == -INFINITY ? 0.0f : top, of = ex2_approx(m - tb);
 #pragma unroll
         for (int i = 0; i <= kOthers; ++i) {  // in order, this CTA's in its place
-          if (own == i && l != 0.0f) sum = fmaf(of, l, sum);
+          if (own == i && cnt > 0) sum = fmaf(of, l, sum);
           if (i == kOthers) break;
           om[i] = ex2_approx(om[i] - tb);
-          if (ol[i] != 0.0f) sum = fmaf(om[i], ol[i], sum);
+          if (!(ol[i] < 0.0f)) sum = fmaf(om[i], ol[i], sum);
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = normaliser(sum, at.r.kv - at.r.n + at.tok(sl) + tok);
         // 32 columns at a time, all their loads in flight at once
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           float4 v[kOthers][8];
 #pragma unroll
           for (int i = 0; i < kOthers; ++i)
-            if (ol[i] != 0.0f)
+            if (!(ol[i] < 0.0f))
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 v[i][e] = __ldcg(reinterpret_cast<const float4*>(other(i)) + (size_t)(cc * 8 + e) * (2 * TR) + prow);
@@ -1734,10 +1741,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
 #pragma unroll
             for (int i = 0; i <= kOthers; ++i) {
-              if (own == i && l != 0.0f)
+              if (own == i && cnt > 0)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[e] = fmaf(of, __uint_as_float(ov[e]), acc[e]);
-              if (i < kOthers && ol[i] != 0.0f)
+              if (i < kOthers && !(ol[i] < 0.0f))
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float4 x = v[i][half * 4 + e];
@@ -1794,7 +1801,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         return of_groups ? split.group_part(parts, pf, x) : split.part(parts, pf, g * split.gsize + x);
       };
       __threadfence();
-      // the weights of each row's parts (-1: without a key, and perhaps without O), its maximum and sum
+      // the weights of each row's parts (-1: there is no O), its maximum and sum
       {
         const int prow = (int)threadIdx.x - 128;
         float top = -INFINITY, sum = 0.0f;
@@ -1805,8 +1812,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         for (int x = 0; x < n; ++x) {
           const float pl = __ldcg(source(x) + (size_t)2 * TR * (D + 1) + prow);
           const float f = ex2_approx(__ldcg(source(x) + (size_t)2 * TR * D + prow) - tb);
-          weights[(2 + x) * 2 * TR + prow] = pl == 0.0f ? -1.0f : f;
-          if (pl != 0.0f) sum = fmaf(f, pl, sum);
+          weights[(2 + x) * 2 * TR + prow] = pl < 0.0f ? -1.0f : f;
+          if (!(pl < 0.0f)) sum = fmaf(f, pl, sum);
         }
         weights[prow] = top;
         weights[2 * TR + prow] = sum;
@@ -1847,10 +1854,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         const float top = weights[prow], sum = weights[2 * TR + prow];
         if (final) {
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
           const int tok = qr / A.group, head = cur.h * A.group + (qr - tok * A.group);
           const int64_t row = (int64_t)cur.r.q0 + cur.tok(qs) + tok;
-          store_row16(A.o + row * A.o_token + (int64_t)head * A.o_head + col4 * 4, acc, inv);
+          store_row16(A.o + row * A.o_token + (int64_t)head * A.o_head + col4 * 4, acc,
+                      normaliser(sum, cur.r.kv - cur.r.n + cur.tok(qs) + tok));
           if (A.lse && col4 == 0)
             A.lse[row * (int64_t)(A.group * A.c.kv_heads) + head] =
                 sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * kLn2;

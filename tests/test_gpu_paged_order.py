@@ -21,8 +21,9 @@ def ctx():
     t.tp3d_destroy(c)
 
 
-def want64(c):
-    """oracle.paged.attention's results by torch on the GPU, for lengths that would take numpy minutes."""
+def want64(c, dropped=()):
+    """oracle.paged.attention's results by torch on the GPU, for lengths that would take numpy minutes; without the keys
+    at the positions ``dropped``."""
     tokens, heads, d = c.q.shape
     g = heads // c.kv_heads
     o, absum = (torch.zeros(tokens, heads, d, dtype=torch.float64, device=device()) for _ in range(2))
@@ -33,6 +34,7 @@ def want64(c):
         ids = torch.from_numpy(c.table[b, :-(-kv // c.page)]).to(device())
         last = kv - (q1 - q0) + torch.arange(q1 - q0, device=device())
         hidden = torch.arange(kv, device=device()) > last[:, None]
+        hidden[:, [x for x in dropped if x < kv]] = True
         for i in range(heads):
             k, v = (p[ids, :, i // g].flatten(0, 1)[:kv].double() for p in (c.kp, c.vp))
             q = c.q[q0:q1, i].double()
