@@ -339,12 +339,13 @@ def tp3d_layer_bwd(ctx, cfg: tp3d_layer_cfg, params: dict, X, workspace, dY, dX,
 # ---------------------------------------------------------------------------
 
 _dtypes = {}
+_I64 = -64  # of slots; no TP3D type
 
 
 def _dtype_of(x):
     if not _dtypes:
         import torch
-        _dtypes.update({torch.float32: TP3D_F32, torch.bfloat16: TP3D_BF16})
+        _dtypes.update({torch.float32: TP3D_F32, torch.bfloat16: TP3D_BF16, torch.int64: _I64})
     return _dtypes.get(x.dtype, -1)
 
 
@@ -387,7 +388,7 @@ def tp3d_paged_store(ctx, cache: tp3d_kv_cache, K, V, slots, stream=None) -> int
         raise ValueError("tp3d_paged_store: K and V (tokens, kv_heads, head_dim) of the same strides, "
                          "contiguous columns")
     dt = cache.dtype
-    if _dtype_of(K) != dt or _dtype_of(V) != dt or slots.numel() < shape[0] or slots.element_size() != 8 or \
+    if _dtype_of(K) != dt or _dtype_of(V) != dt or slots.numel() < shape[0] or _dtype_of(slots) != _I64 or \
             not slots.is_contiguous():
         raise ValueError("tp3d_paged_store: K and V of the cache's type, an int64 slot for each token")
     return lib().tp3d_paged_store(ctx, ctypes.byref(cache), shape[0], K.data_ptr(), V.data_ptr(), st[0], st[1],
@@ -402,7 +403,7 @@ def tp3d_paged_attn(ctx, cache: tp3d_kv_cache, batch: tp3d_paged_batch, Q, O, ls
     if len(shape) != 3 or O.shape != shape or qs[2] != 1 or os_[2] != 1 or shape[0] < batch.tokens or \
             shape[2] != cache.head_dim or _dtype_of(Q) != dt or _dtype_of(O) != dt:
         raise ValueError("tp3d_paged_attn: Q and O (tokens, heads, head_dim) of the cache's type, contiguous columns")
-    if lse is not None and (not lse.is_contiguous() or lse.shape != shape[:2] or lse.element_size() != 4):
+    if lse is not None and (not lse.is_contiguous() or lse.shape != shape[:2] or _dtype_of(lse) != TP3D_F32):
         raise ValueError("tp3d_paged_attn: lse dense (tokens, heads) float32")
     return lib().tp3d_paged_attn(ctx, ctypes.byref(cache), ctypes.byref(batch), shape[1], scale, Q.data_ptr(),
                                  tp3d_row_strides(qs[0], qs[1]), O.data_ptr(), tp3d_row_strides(os_[0], os_[1]),
