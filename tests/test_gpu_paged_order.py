@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import tensor_transformer_layer_cube_gb300 as t
-from tests.gpu_util import device
+from tests.gpu_util import assert_guards_intact, device, guarded
 from tests.test_gpu_paged import Case, compare
 
 pytestmark = pytest.mark.gpu
@@ -224,3 +224,18 @@ def test_plans_of_many_requests_from_several_host_threads():
     for x in threads:
         x.join()
     assert statuses == {n: {"TP3D_OK"} for n in (16384, 8000, 12000)}
+
+
+@pytest.mark.parametrize("kv,new,heads,kv_heads", [
+    # parts of every kind: two and three to an item, many in two levels, single tokens, both kernels of a call
+    ([9000, 7000], [200, 130], 8, 8), ([30000], [64], 2, 1), ([20000], [1], 16, 2), ([5000, 6000, 300], [1, 300, 1], 8, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_workspace_between_guards(ctx, kv, new, heads, kv_heads, d):
+    c = Case(kv, new, heads, kv_heads, d, 64, seed=d)
+    want, wl = c.run(ctx)
+    whole, ws = guarded(t.tp3d_paged_attn_workspace_bytes(ctx, c.cache, heads), torch.uint8)
+    o, l = torch.empty_like(want), torch.empty_like(wl)
+    t.check(t.tp3d_paged_attn(ctx, c.cache, c.batch(), c.q, o, l, c.scale, ws))
+    assert t.tp3d_sync_status(ctx) == 0
+    assert torch.equal(o.view(torch.int16), want.view(torch.int16)) and torch.equal(l, wl)
+    assert_guards_intact(whole)
