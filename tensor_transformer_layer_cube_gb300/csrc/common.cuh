@@ -31,7 +31,8 @@ struct tp3d_ctx {
   // between calls
   void* scratch;
   size_t scratch_bytes;
-  // arrival counters of the paged attention's split items (zero between calls)
+  // arrival counters of the paged attention's split items, and the word that its
+  // kernel for many rows leaves for the one for few (zero between calls)
   unsigned* d_paged;
   int paged_ready;  // paged kernels that are set up (bits: attention with heads of 128, of 64, plans of many requests)
   // CUDA graphs of whole layer calls keyed by their arguments (graph.cu), the
