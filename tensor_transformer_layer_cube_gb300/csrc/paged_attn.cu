@@ -70,11 +70,13 @@ struct FewShape {
   static constexpr int kMinTiles = 16 / W;
   // Rows of a request that this kernel takes, in blocks of 16 (items of their
   // own, side by side, so that a block finds the others' keys in L2).  Here | in
-  // the kernel for many rows, eight warps: 4 requests of 2000 keys, 4 heads, 24
-  // rows 12.5 | 19.0 us, 48 rows 11.6 | 20.5; one of 65536, 4 heads, 24 rows 42 |
-  // 58, 48 rows 61.5 | 61.5, 64 rows 72.6 | 62.2.  Four warps: 64 of 500, 8 heads
-  // of 64, 16 rows 21.8 | 38.2, 20 rows 25.3 | 27.4; 32 of 4000, 8 heads, 32 rows
-  // 106.7 | 94.8; 16 of 2000, 16 heads, 30 rows 68.8 | 52.9.
+  // the kernel for many rows, eight warps: 4 requests of up to 2000 keys, 4
+  // heads, 24 rows 12.0 | 21.4 us, 48 rows 13.1 | 22.1, 64 rows 18.0 | 22.2; one of
+  // 65536, 4 heads, 24 rows 41.4 | 59.2, 48 rows 60.5 | 62.2, 64 rows 73.0 | 62.5.
+  // Four warps: 64 of up to 500, 8 heads of 64, 16 rows 17.8 | 30.5.  (There more
+  // rows would gain too, which the limit does not use: 20 rows 18.3 | 27.8; 32 of
+  // up to 4000, 8 heads, 32 rows 90.9 | 100.2; 16 of up to 2000, 16 heads, 30
+  // rows 41.2 | 53.1.)
   static constexpr int kRows = W == 8 ? 48 : 16;
   // The end of an item counts as so many tiles in the ranges, about what it costs.  With it | without, four warps:
   // 32 requests of up to 4096 keys, 16 heads 85 | 94 us (one box); 100 of 700 41.8 | 60.9; 200 of 2000, 8 heads 127 | 145 (1:
@@ -744,7 +746,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
 // page and 64 columns.  As in the layer's forward: S = Q K^T in tensor memory,
 // an online softmax per row (one thread each), P written back over S, and
 // O += P V with P read from tensor memory.  Differences:
-//  * P is kept as two bf16 terms (P = hi + lo up to 2^-17 P): over its 32
+//  * P is kept as two bf16 terms (P = hi + lo up to 2^-16 P): over its 32
 //    score columns a chunk leaves 16 columns of hi pairs and 16 of lo pairs,
 //    and O += hi V + lo V.  One bf16 term alone has an error as large as the
 //    output's own rounding.
@@ -757,8 +759,9 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
 //    value that is not finite becomes zero and is noted with its key and
 //    column, since a probability of 0 would not silence it.
 //
-// Measured: 2048 new tokens over 6145, 16 heads of 128 (120 GFLOP): 142 us, 847
-// TFLOP/s, 0.44 of the measured bf16 rate; with the lo terms 1.27 PFLOP/s run.
+// Measured: 2048 new tokens over 6145, 16 heads of 128 (120 GFLOP): 141 us in a
+// captured graph, 146 us as separate calls: 856 and 824 TFLOP/s, 0.45 and 0.43 of
+// the measured bf16 rate; with the lo terms 1.28 and 1.24 PFLOP/s run.
 // For D = 128 the tensor instructions bound it: a pair of tiles takes 48 of them,
 // 128 x 128 x 16 each, about 107 cycles apiece (64 nominal: two 4 KiB operands
 // from shared memory keep its port full), so 5140 of a period of 5250 cycles.
@@ -771,7 +774,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
 // smem: Q0 | Q1 | R0 .. R4 (a ring of K_j V_j ...), 32 KiB each | barriers | notes
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [256+D,256+2D)
 constexpr int kManyThreads = 384;
-constexpr int kManyRegsLow = 120, kManyRegsHigh = 192;  // 128 x 120 + 256 x 192 <= 384 x 168; no spills
+constexpr int kManyRegsLow = 120, kManyRegsHigh = 192;  // 128 x 120 + 256 x 192 <= 384 x 168 (52 and 68 bytes spilled)
 constexpr uint32_t kManyRing = 5;
 constexpr int kNotes = 4;  // pieces whose values may be under check or in use at once
 struct ManyShared {
@@ -789,12 +792,12 @@ struct ManyShared {
 constexpr int kManySmem = 7 * (int)kTile + 512 + (int)sizeof(ManyShared) + 1024;
 static_assert(kManySmem <= 232448, "shared memory of one CTA");
 // Parts of an item joined by row, by the thread that has the CTA's own part in
-// tensor memory; more by element, dealt to all row threads.  Row | element: 2
-// parts (2048 tokens over 6145 keys, 16 heads) 143 | 150 us; 3-4 parts (4 x 200
-// tokens over 3000) 47.1 | 45.9 us; 19 parts (5 tokens, 65536 keys, 8 heads)
-// 122 | 77 us.
+// tensor memory; more by element, dealt to all row threads.  Up to three by row
+// | all by element | up to four by row: 2048 tokens over 6145 keys, 16 heads (2
+// parts) 140.6 | 150.0 | 142.4 us; 4 x up to 200 tokens over 3000 (2 to 4) 47.7 |
+// 56.2 | 48.0; one prompt of 1000 tokens 31.0 | 35.6 | 29.9.
 constexpr int kManyByRow = 3;
-constexpr int kManyJoinOnce = 8;  // parts of an item joined in one step (500 tokens over 8192, 5 parts: 73.8 us; with 4 78.5)
+constexpr int kManyJoinOnce = 8;  // parts of an item joined in one step (500 tokens over 8192, 5 parts: 74.3 us; with 4 80.4)
 constexpr int kManySlots = 4;     // parts that a CTA has room for in the workspace
 TP3D_HD constexpr size_t many_part_floats(int d) { return (size_t)2 * TR * (d + 2); }
 
@@ -870,14 +873,15 @@ __device__ __forceinline__ ManyRequest many_request(const PagedAttn& A, int b) {
 // so that neighbours in the sequence add up to like amounts of work, and a
 // range boundary within `near` tiles of a pair's edge is moved there: leaving a
 // part and joining it costs about as much as kSnap tiles (4 prompts of up to
-// 1024: 42.1 us; with 2 42.8, with 1 46.6).  Where ranges are short, moving by
+// 1024: 43.5 us; with 2 43.7, with 1 47.4; 4 x up to 200 tokens over 3000 47.7;
+// with 2 52.5; 2048 tokens over 6145 140.6; with 2 139.2).  Where ranges are short, moving by
 // as much would leave CTAs without work beside others with twice theirs, so it
 // is two tiles less than a range, one at least.  With that | always by kSnap: 4
-// requests of 2000 keys, 128 rows a head, 4 heads 24.9 | 30.9 us; 8 chunks of
-// up to 100 over 1000, 16 heads of 64 22.1 | 25.5; one prompt of 1000, 16 heads
-// 30.3 | 28.6; 4 x 200 over 3000 the same.
+// requests of 2000 keys, 128 rows a head, 4 heads 26.4 | 30.0 us; 8 chunks of
+// up to 100 over 1000, 16 heads of 64 23.2 | 25.8; one prompt of 1000, 16 heads
+// 31.0 | 28.5; 4 x 200 over 3000 47.7 | 47.3.
 constexpr int kSnap = 4;
-constexpr int kManyMinTiles = 2;  // of a CTA's range, where there is little work (the first case above; with 1 27.2)
+constexpr int kManyMinTiles = 2;  // of a CTA's range, where there is little work (the first case above; with 1 30.3)
 struct ManyCursor {
   ManyRequest r;
   int b, h, i, k, pairs;
