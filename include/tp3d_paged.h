@@ -10,8 +10,14 @@
  *   tp3d_paged_plan   lengths -> pages taken from the free list, block table
  *                     rows, the slot and position of every new token;
  *   (the layer's QKV product, tp3d_linear)
- *   tp3d_paged_store  K and V of the new tokens -> their slots;
- *   tp3d_paged_attn   attention of the new tokens over the cache.
+ *   tp3d_paged_store  K and V of the new tokens -> their slots
+ *                     (tp3d_paged_rope_store: heads normed and turned by
+ *                     position on the way);
+ *   tp3d_paged_attn   attention of the new tokens over the cache
+ *                     (tp3d_paged_attn_window: over a sliding window and a
+ *                     few first tokens).
+ * Between steps pages are shared, given back and moved: tp3d_paged_fork,
+ * tp3d_paged_free, tp3d_paged_compact, and tp3d_paged_copy for the contents.
  * Everything a step depends on stays on the device: no call reads a length
  * back, and a captured step replays with new lengths in the same buffers.
  *
@@ -30,6 +36,7 @@
 #define TP3D_PAGED_H
 
 #include "tp3d.h"
+#include "tp3d_rope.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -109,6 +116,19 @@ tp3d_status tp3d_paged_plan(tp3d_ctx* ctx, int page, int requests, int64_t token
 tp3d_status tp3d_paged_store(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t tokens, const void* K, const void* V,
                              int64_t token_stride, int64_t head_stride, const int64_t* slots, void* stream);
 
+/* tp3d_paged_store with the heads normed and turned (tp3d_rope.h) in the same
+ * pass: query rows Q normed and turned into Q_out (or in place), key rows K
+ * normed, turned and written to their slots, value rows V written to theirs as
+ * they are.  K and V: the cache's heads.  Q rows of a token are written
+ * whatever its slot; slots as in tp3d_paged_store.  rope: of the cache's dtype
+ * (TP3D_EDTYPE) and head_dim (TP3D_ESHAPE).  Other checks as tp3d_qk_rope and
+ * tp3d_paged_store.                                                          */
+tp3d_status tp3d_paged_rope_store(tp3d_ctx* ctx, const tp3d_rope* rope, const tp3d_kv_cache* cache, int64_t tokens,
+                                  int heads, const void* Q, tp3d_row_strides q_strides, const void* K,
+                                  tp3d_row_strides k_strides, const void* V, tp3d_row_strides v_strides,
+                                  const int32_t* positions, const int64_t* slots, void* Q_out,
+                                  tp3d_row_strides qo_strides, void* stream);
+
 /* Attention of the new tokens over the cache, causal: for new token j of
  * request b and query head i (key/value head h = i / (heads / kv_heads)),
  *   O = softmax_k(scale q . k_k) V over the keys k = 0 .. kv_b - n_b + j,
@@ -133,9 +153,6 @@ tp3d_status tp3d_paged_store(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t 
  * aligned, strides positive (TP3D_EINVAL) and multiples of 8 (TP3D_EALIGN).
  * `workspace`: tp3d_paged_attn_workspace_bytes bytes, 256-byte aligned,
  * contents free.                                                             */
-typedef struct {
-  int64_t token_stride, head_stride;
-} tp3d_row_strides;
 tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3d_paged_batch* batch, int heads,
                             float scale, const void* Q, tp3d_row_strides q_strides, void* O,
                             tp3d_row_strides o_strides, float* lse, void* workspace, void* stream);

@@ -9,7 +9,9 @@ Parallelism", §2), in hand-written sm_103a kernels; and (``include/tp3d_plan.h`
 the host-side planners: the cross-mesh resharding planner of that page's
 §3.2 and a pipeline-bubble simulator; and (``include/tp3d_paged.h``) the paged
 key/value cache that serves the layer: block tables and slot maps from request
-lengths, the cache write, and attention of new tokens over the cache.
+lengths, the cache write, and attention of new tokens over the cache; and
+(``include/tp3d_rope.h``) the norm of query and key heads with the rotation by
+position, forward and backward.
 
 This module only marshals arguments: every function has the name of the C
 entry point it calls and returns its status code (0 = TP3D_OK).  Tensor
@@ -41,6 +43,9 @@ __all__ = [
     "TP3D_PIPE_INTERLEAVED",
     "tp3d_kv_cache", "tp3d_paged_batch", "tp3d_row_strides", "kv_cache", "paged_batch", "tp3d_paged_plan",
     "tp3d_paged_store", "tp3d_paged_attn", "tp3d_paged_attn_workspace_bytes",
+    "tp3d_rope", "rope", "rope_turns", "tp3d_rope_turns", "tp3d_qk_rope", "tp3d_qk_rope_bwd",
+    "tp3d_qk_rope_bwd_workspace_bytes", "tp3d_paged_rope_store", "TP3D_ROPE_PLAIN", "TP3D_ROPE_LINEAR",
+    "TP3D_ROPE_BASE", "TP3D_ROPE_PARTS",
 ]
 
 STATUS = {0: "TP3D_OK", 1: "TP3D_EINVAL", 2: "TP3D_ESHAPE", 3: "TP3D_EALIGN", 4: "TP3D_EDTYPE",
@@ -52,6 +57,7 @@ TP3D_SPEC_R, TP3D_SPEC_S0, TP3D_SPEC_S1, TP3D_SPEC_S01 = range(4)
 TP3D_CMR_NAIVE, TP3D_CMR_LOAD_BALANCE, TP3D_CMR_DFS, TP3D_CMR_RANDOM_GREEDY = range(4)
 TP3D_PIPE_GPIPE, TP3D_PIPE_1F1B, TP3D_PIPE_INTERLEAVED = range(3)
 TP3D_SCHEME_1D, TP3D_SCHEME_2D, TP3D_SCHEME_3D = 1, 2, 3
+TP3D_ROPE_PLAIN, TP3D_ROPE_LINEAR, TP3D_ROPE_BASE, TP3D_ROPE_PARTS = range(4)
 
 
 class tp3d_layout(ctypes.Structure):
@@ -90,6 +96,13 @@ class tp3d_paged_batch(ctypes.Structure):
 
 class tp3d_row_strides(ctypes.Structure):
     _fields_ = [("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class tp3d_rope(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("magnitude", ctypes.c_float), ("turns", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
 
 
 class tp3d_rect(ctypes.Structure):
@@ -189,6 +202,18 @@ _SIGS = {
                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "tp3d_paged_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.POINTER(tp3d_kv_cache),
                                                           ctypes.c_int]),
+    "tp3d_rope_turns": (ctypes.c_int, [ctypes.c_int, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double,
+                                       ctypes.c_void_p, ctypes.POINTER(ctypes.c_float)]),
+    "tp3d_qk_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_rope), ctypes.c_int64, ctypes.c_int,
+                                    ctypes.c_int] + [ctypes.c_void_p, tp3d_row_strides] * 2 + [ctypes.c_void_p] +
+                     [ctypes.c_void_p, tp3d_row_strides] * 2 + [ctypes.c_void_p]),
+    "tp3d_qk_rope_bwd": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_rope), ctypes.c_int64, ctypes.c_int,
+                                        ctypes.c_int] + [ctypes.c_void_p, tp3d_row_strides] * 2 + [ctypes.c_void_p] +
+                         [ctypes.c_void_p, tp3d_row_strides] * 4 + [ctypes.c_void_p] * 4),
+    "tp3d_qk_rope_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.POINTER(tp3d_rope)]),
+    "tp3d_paged_rope_store": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_rope), ctypes.POINTER(tp3d_kv_cache),
+                                             ctypes.c_int64, ctypes.c_int] + [ctypes.c_void_p, tp3d_row_strides] * 3 +
+                              [ctypes.c_void_p] * 3 + [tp3d_row_strides, ctypes.c_void_p]),
     "tp3d_layout_rects": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, tp3d_layout, ctypes.POINTER(tp3d_rect),
                                          ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)]),
     "tp3d_mesh_rects": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, tp3d_mesh_spec, ctypes.POINTER(tp3d_rect),
@@ -339,13 +364,13 @@ def tp3d_layer_bwd(ctx, cfg: tp3d_layer_cfg, params: dict, X, workspace, dY, dX,
 # ---------------------------------------------------------------------------
 
 _dtypes = {}
-_I64 = -64  # of slots; no TP3D type
+_I64, _I32 = -64, -32  # of slots and positions; no TP3D types
 
 
 def _dtype_of(x):
     if not _dtypes:
         import torch
-        _dtypes.update({torch.float32: TP3D_F32, torch.bfloat16: TP3D_BF16, torch.int64: _I64})
+        _dtypes.update({torch.float32: TP3D_F32, torch.bfloat16: TP3D_BF16, torch.int64: _I64, torch.int32: _I32})
     return _dtypes.get(x.dtype, -1)
 
 
@@ -412,6 +437,104 @@ def tp3d_paged_attn(ctx, cache: tp3d_kv_cache, batch: tp3d_paged_batch, Q, O, ls
 
 def tp3d_paged_attn_workspace_bytes(ctx, cache: tp3d_kv_cache, heads: int) -> int:
     return lib().tp3d_paged_attn_workspace_bytes(ctx, ctypes.byref(cache), heads)
+
+
+# ---------------------------------------------------------------------------
+# Head norms with the rotation by position (include/tp3d_rope.h).
+# ---------------------------------------------------------------------------
+
+def tp3d_rope_turns(rotary_dim, base, kind, factor, context, turns) -> tuple:
+    """(status, magnitude); ``turns``: a host tensor of int64 words, rotary_dim / 2 of them, or None."""
+    m = ctypes.c_float(0.0)
+    st = lib().tp3d_rope_turns(rotary_dim, base, kind, factor, context, _p(turns), ctypes.byref(m))
+    return st, m.value
+
+
+def rope_turns(rotary_dim: int, base: float = 10000.0, kind: int = TP3D_ROPE_PLAIN, factor: float = 1.0,
+               context: float = 1.0) -> tuple:
+    """(turns, magnitude): the frequencies as a host tensor of int64 words, for ``rope`` once it is on the device.
+    Raises on failure."""
+    import torch
+    turns = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.int64)
+    st, magnitude = tp3d_rope_turns(rotary_dim, base, kind, factor, context, turns)
+    check(st, "tp3d_rope_turns")
+    return turns, magnitude
+
+
+def rope(turns, dtype, head_dim: int, rotary_dim: int, interleaved: bool = False, magnitude: float = 1.0,
+         norm: bool = False, eps: float = 1e-6, q_weight=None, k_weight=None) -> tp3d_rope:
+    """The descriptor of a norm and rotation of heads of ``dtype`` (a torch dtype): device tensors, the frequencies
+    int64 words.  It holds their addresses: keep the tensors."""
+    import torch
+    code = {torch.float32: TP3D_F32, torch.bfloat16: TP3D_BF16}.get(dtype)
+    if code is None:
+        raise ValueError("rope: heads of bfloat16 or float32")
+    if rotary_dim and (turns is None or turns.dtype != torch.int64 or not turns.is_contiguous() or
+                       turns.numel() < rotary_dim // 2):
+        raise ValueError("rope: rotary_dim / 2 contiguous int64 words of turns")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != dtype or not w.is_contiguous() or w.numel() != head_dim):
+            raise ValueError("rope: weights of head_dim contiguous elements of the heads' type")
+    return tp3d_rope(code, head_dim, rotary_dim, int(interleaved), int(norm), eps, magnitude, _p(turns), _p(q_weight),
+                     _p(k_weight))
+
+
+def _rows_of(what, r: tp3d_rope, tokens, *arrays):
+    """Pointer and strides of (token, head, column) tensors, checked: the heads of each pair are the same."""
+    out = []
+    for x, heads in arrays:
+        shape, st = x.shape, x.stride()
+        if len(shape) != 3 or shape[0] != tokens or shape[1] != heads or shape[2] != r.head_dim or st[2] != 1 or \
+                _dtype_of(x) != r.dtype:
+            raise ValueError(f"{what}: (tokens, heads, head_dim) rows of one type, contiguous columns")
+        out += [x.data_ptr(), tp3d_row_strides(st[0], st[1])]
+    return out
+
+
+def _positions(what, positions, tokens):
+    if _dtype_of(positions) != _I32 or not positions.is_contiguous() or positions.numel() < tokens:
+        raise ValueError(f"{what}: a contiguous int32 position for each token")
+    return positions.data_ptr()
+
+
+def tp3d_qk_rope(ctx, rope: tp3d_rope, Q, K, positions, Q_out, K_out, stream=None) -> int:
+    """Q, Q_out (tokens, heads, head_dim), K, K_out (tokens, kv_heads, head_dim); in place where the same tensor."""
+    n, h, kh = Q.shape[0], Q.shape[1], K.shape[1]
+    q, qs, k, ks, qo, qos, ko, kos = _rows_of("tp3d_qk_rope", rope, n, (Q, h), (K, kh), (Q_out, h), (K_out, kh))
+    return lib().tp3d_qk_rope(ctx, ctypes.byref(rope), n, h, kh, q, qs, k, ks,
+                              _positions("tp3d_qk_rope", positions, n), qo, qos, ko, kos, _s(stream))
+
+
+def tp3d_qk_rope_bwd(ctx, rope: tp3d_rope, Q, K, positions, dQ_out, dK_out, dQ, dK, dq_weight, dk_weight, workspace,
+                     stream=None) -> int:
+    """Shapes as in tp3d_qk_rope; Q and K may be None without the norm.  dq_weight, dk_weight: head_dim elements or
+    None."""
+    n, h, kh = dQ_out.shape[0], dQ_out.shape[1], dK_out.shape[1]
+    what, none = "tp3d_qk_rope_bwd", [None, tp3d_row_strides(0, 0)]
+    q = _rows_of(what, rope, n, (Q, h)) if Q is not None else none
+    k = _rows_of(what, rope, n, (K, kh)) if K is not None else none
+    g = _rows_of(what, rope, n, (dQ_out, h), (dK_out, kh), (dQ, h), (dK, kh))
+    for w in (dq_weight, dk_weight):
+        if w is not None and (_dtype_of(w) != rope.dtype or not w.is_contiguous() or w.numel() != rope.head_dim):
+            raise ValueError("tp3d_qk_rope_bwd: weights' gradients of head_dim contiguous elements of the heads' type")
+    return lib().tp3d_qk_rope_bwd(ctx, ctypes.byref(rope), n, h, kh, *q, *k, _positions(what, positions, n), *g,
+                                  _p(dq_weight), _p(dk_weight), _p(workspace), _s(stream))
+
+
+def tp3d_qk_rope_bwd_workspace_bytes(ctx, rope: tp3d_rope) -> int:
+    return lib().tp3d_qk_rope_bwd_workspace_bytes(ctx, ctypes.byref(rope))
+
+
+def tp3d_paged_rope_store(ctx, rope: tp3d_rope, cache: tp3d_kv_cache, Q, K, V, positions, slots, Q_out,
+                          stream=None) -> int:
+    """Q, Q_out (tokens, heads, head_dim), K, V (tokens, kv_heads, head_dim); an int64 slot for each token."""
+    n, h, kh = Q.shape[0], Q.shape[1], cache.kv_heads
+    what = "tp3d_paged_rope_store"
+    q, qs, k, ks, v, vs, qo, qos = _rows_of(what, rope, n, (Q, h), (K, kh), (V, kh), (Q_out, h))
+    if slots.numel() < n or _dtype_of(slots) != _I64 or not slots.is_contiguous():
+        raise ValueError("tp3d_paged_rope_store: an int64 slot for each token")
+    return lib().tp3d_paged_rope_store(ctx, ctypes.byref(rope), ctypes.byref(cache), n, h, q, qs, k, ks, v, vs,
+                                       _positions(what, positions, n), slots.data_ptr(), qo, qos, _s(stream))
 
 
 # ---------------------------------------------------------------------------

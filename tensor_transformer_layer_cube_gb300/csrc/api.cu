@@ -132,8 +132,8 @@ tp3d_status tp3d_create(int device, tp3d_ctx** out) {
   if (cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
       cudaMalloc(&c->d_err, sizeof(init)) != cudaSuccess ||
       cudaMemcpy(c->d_err, init, sizeof(init), cudaMemcpyHostToDevice) != cudaSuccess ||
-      cudaMalloc(&c->d_paged, kPagedCounters * sizeof(unsigned)) != cudaSuccess ||
-      cudaMemset(c->d_paged, 0, kPagedCounters * sizeof(unsigned)) != cudaSuccess || !legacy_done()) {
+      cudaMalloc(&c->d_paged, kPagedWords * sizeof(unsigned)) != cudaSuccess ||
+      cudaMemset(c->d_paged, 0, kPagedWords * sizeof(unsigned)) != cudaSuccess || !legacy_done()) {
     if (c->d_err) cudaFree(c->d_err);
     if (c->d_paged) cudaFree(c->d_paged);
     free(c);
@@ -201,7 +201,7 @@ tp3d_status tp3d_sync_status(tp3d_ctx* ctx, void* stream) {
   // there or elsewhere.  (A launch that gave up, and perhaps raised something
   // else before, leaves its split items' counts unfinished.)
   if (cudaMemsetAsync(ctx->d_err, 0, sizeof(int), as_stream(stream)) != cudaSuccess ||
-      cudaMemsetAsync(ctx->d_paged, 0, kPagedCounters * sizeof(unsigned), as_stream(stream)) != cudaSuccess ||
+      cudaMemsetAsync(ctx->d_paged, 0, kPagedWords * sizeof(unsigned), as_stream(stream)) != cudaSuccess ||
       cudaStreamSynchronize(as_stream(stream)) != cudaSuccess)
     return TP3D_ECUDA;
   return static_cast<tp3d_status>(e);

@@ -31,8 +31,9 @@ struct tp3d_ctx {
   // between calls
   void* scratch;
   size_t scratch_bytes;
-  // arrival counters of the paged attention's split items, and the word that its
-  // kernel for many rows leaves for the one for few (zero between calls)
+  // arrival counters of the paged attention's split items, the word that its
+  // kernel for many rows leaves for the one for few, the arrivals and counts of
+  // rope.cu and paged_pages.cu (zero between calls)
   unsigned* d_paged;
   int paged_ready;  // paged kernels that are set up (bits: attention with heads of 128, of 64, plans of many requests)
   // CUDA graphs of whole layer calls keyed by their arguments (graph.cu), the
@@ -53,7 +54,10 @@ void graph_cache_free(tp3d_ctx* ctx);
 // the context sets another limit (tp3d_set_wait_limit_ns); the drains of an
 // aborting CTA always allow this long.
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;
-constexpr int kPagedCounters = 4096;
+constexpr int kPagedCounters = 4096;  // of the paged attention
+constexpr int kRopeCounter = kPagedCounters;  // arrivals in the sum of the weights' gradients (rope.cu)
+constexpr int kPageWords = kPagedCounters + 32;  // of paged_pages.cu: its flags and counts
+constexpr int kPagedWords = 2 * kPagedCounters;  // all of d_paged
 constexpr int kErrWords = 4;  // ints of the device error area (error code, pad, 64-bit limit)
 
 #define TP3D_CUDA_TRY(expr)                       \

@@ -9,8 +9,6 @@ namespace tp3d {
 
 namespace {
 
-constexpr int kThreads = 256;
-
 // ------------------------------------------------------------------ plan
 // With c_b cached and f_b new tokens, old_b = ceil(c_b / page) and
 // need_b = ceil((c_b + f_b) / page) - old_b, everything a step needs follows
@@ -27,7 +25,7 @@ constexpr int kThreads = 256;
 // of one token 3.4 us on the GPU, 64 prompts (48467 tokens) 3.8 us; the
 // host takes 5.9 us a call.
 constexpr int kScanItems = 4;
-constexpr int kScanChunk = kThreads * kScanItems;
+constexpr int kScanChunk = kPagedThreads * kScanItems;
 constexpr int kPlanMaxRequests = 16384;
 constexpr int kPlanReady = 4;  // of tp3d_ctx::paged_ready
 
@@ -77,11 +75,11 @@ __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int32_t x) 
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs P) {
+__global__ void __launch_bounds__(kPagedThreads) paged_plan_kernel(const PlanArgs P) {
   extern __shared__ int32_t plan_smem[];
   int32_t* sf = plan_smem;                    // exclusive sums of fresh, requests + 1
   int32_t* sp = plan_smem + P.requests + 1;   // exclusive sums of the new pages, requests + 1
-  __shared__ long long warp_f[kThreads / 32], warp_p[kThreads / 32];
+  __shared__ long long warp_f[kPagedThreads / 32], warp_p[kPagedThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool first = blockIdx.x == 0;
   grid_begin();
@@ -123,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs P) 
     __syncthreads();
     long long bf = carry_f + xf - tf, bp = carry_p + xp - tp;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kPagedThreads / 32; ++w) {
       if (w < warp) {
         bf += warp_f[w];
         bp += warp_p[w];
@@ -154,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs P) 
     }
   }
 
-  const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+  const int64_t tid = (int64_t)blockIdx.x * kPagedThreads + threadIdx.x, step = (int64_t)gridDim.x * kPagedThreads;
   for (int64_t i = tid; i < total_p; i += step) {
     const int b = last_at_most(sp, P.requests, (int32_t)i);
     const Lengths l = plan_lengths(P, b);
@@ -196,11 +194,11 @@ struct StoreArgs {
 
 constexpr int kStoreVecs = 4;  // of K and of V each, in flight per thread
 
-__global__ void __launch_bounds__(kThreads) paged_store_kernel(const StoreArgs S) {
+__global__ void __launch_bounds__(kPagedThreads) paged_store_kernel(const StoreArgs S) {
   grid_begin();
   const int64_t rows = S.tokens * S.c.kv_heads, total = rows << S.vec_log2;
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += kStoreVecs * step) {
+  const int64_t step = (int64_t)gridDim.x * kPagedThreads;
+  for (int64_t i0 = (int64_t)blockIdx.x * kPagedThreads + threadIdx.x; i0 < total; i0 += kStoreVecs * step) {
     uint4 k[kStoreVecs], v[kStoreVecs];
     int64_t to[kStoreVecs];
 #pragma unroll
@@ -231,61 +229,6 @@ __global__ void __launch_bounds__(kThreads) paged_store_kernel(const StoreArgs S
       *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(S.c.v) + to[q]) = v[q];
     }
   }
-}
-
-int page_log2(int page) {
-  if (page < 16 || page > 4096 || (page & (page - 1))) return -1;
-  int l = 4;
-  while ((1 << l) < page) ++l;
-  return l;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-tp3d_status check_cache(const tp3d_kv_cache* c) {
-  if (!c || !c->k || !c->v || c->kv_heads < 1 || c->pages < 1) return TP3D_EINVAL;
-  if (c->dtype != TP3D_BF16) return TP3D_EDTYPE;
-  if ((c->head_dim != 64 && c->head_dim != 128) || page_log2(c->page) < 0 || c->pages > INT32_MAX)
-    return TP3D_EUNSUPPORTED;
-  if (c->page_stride < 1 || c->token_stride < 1 || c->head_stride < 1) return TP3D_EINVAL;
-  if ((c->page_stride | c->token_stride | c->head_stride) >> 39) return TP3D_EUNSUPPORTED;  // a tensor map's strides
-  if (!aligned16(c->k) || !aligned16(c->v) || (c->page_stride | c->token_stride | c->head_stride) % 8)
-    return TP3D_EALIGN;
-  return TP3D_OK;
-}
-
-// bytes from a strided (page, token, head) array's first element to its last;
-// strides are the caller's and may be anything, so the sum is kept from
-// wrapping (an array that long overlaps everything above it)
-size_t extent(int64_t pages, int64_t ps, int64_t tokens, int64_t ts, int64_t heads, int64_t hs, int64_t d) {
-  const unsigned __int128 n = ((unsigned __int128)(pages - 1) * (uint64_t)ps +
-                               (unsigned __int128)(tokens - 1) * (uint64_t)ts +
-                               (unsigned __int128)(heads - 1) * (uint64_t)hs + (uint64_t)d) * 2;
-  return n > (unsigned __int128)1 << 62 ? (size_t)1 << 62 : (size_t)n;
-}
-size_t cache_bytes(const tp3d_kv_cache& c) {
-  return extent(c.pages, c.page_stride, c.page, c.token_stride, c.kv_heads, c.head_stride, c.head_dim);
-}
-
-struct Range {
-  const void* p;
-  size_t n;
-};
-// any output overlapping an input or another output
-template <int NO, int NI>
-bool clash(const Range (&out)[NO], const Range (&in)[NI]) {
-  for (int i = 0; i < NO; ++i) {
-    for (int j = 0; j < NI; ++j)
-      if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
-    for (int j = 0; j < i; ++j)
-      if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
-  }
-  return false;
-}
-
-unsigned blocks(const tp3d_ctx* ctx, int64_t threads, int per_sm) {
-  const int64_t n = (threads + kThreads - 1) / kThreads, most = (int64_t)ctx->num_sms * per_sm;
-  return (unsigned)(n < 1 ? 1 : n < most ? n : most);
 }
 
 }  // namespace
@@ -326,7 +269,7 @@ tp3d_status tp3d_paged_plan(tp3d_ctx* ctx, int page, int requests, int64_t token
                                        (kPlanMaxRequests + 1) * 8));
     ctx->paged_ready |= kPlanReady;
   }
-  return launch_dependent(paged_plan_kernel, blocks(ctx, tokens, 1), kThreads, smem, as_stream(stream), P);
+  return launch_dependent(paged_plan_kernel, blocks(ctx, tokens, 1), kPagedThreads, smem, as_stream(stream), P);
 }
 
 tp3d_status tp3d_paged_store(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t tokens, const void* K, const void* V,
@@ -347,7 +290,7 @@ tp3d_status tp3d_paged_store(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t 
   const StoreArgs S{*cache, page_log2(cache->page), cache->head_dim == 128 ? 4 : 3, tokens, token_stride, head_stride,
                     static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), slots, ctx->d_err};
   const int64_t vecs = tokens * cache->kv_heads * (cache->head_dim / 8);
-  return launch_dependent(paged_store_kernel, blocks(ctx, vecs, 8), kThreads, 0, as_stream(stream), S);
+  return launch_dependent(paged_store_kernel, blocks(ctx, vecs, 8), kPagedThreads, 0, as_stream(stream), S);
 }
 
 size_t tp3d_paged_attn_workspace_bytes(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int heads) {

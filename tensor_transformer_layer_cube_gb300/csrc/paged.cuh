@@ -32,6 +32,65 @@ struct PagedAttn {
 tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* workspace, cudaStream_t s);
 size_t paged_attn_workspace(const tp3d_ctx* ctx, int head_dim);
 
+constexpr int kPagedThreads = 256;  // of the kernels that are not attention
+
+inline int page_log2(int page) {
+  if (page < 16 || page > 4096 || (page & (page - 1))) return -1;
+  int l = 4;
+  while ((1 << l) < page) ++l;
+  return l;
+}
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+inline tp3d_status check_cache(const tp3d_kv_cache* c) {
+  if (!c || !c->k || !c->v || c->kv_heads < 1 || c->pages < 1) return TP3D_EINVAL;
+  if (c->dtype != TP3D_BF16) return TP3D_EDTYPE;
+  if ((c->head_dim != 64 && c->head_dim != 128) || page_log2(c->page) < 0 || c->pages > INT32_MAX)
+    return TP3D_EUNSUPPORTED;
+  if (c->page_stride < 1 || c->token_stride < 1 || c->head_stride < 1) return TP3D_EINVAL;
+  if ((c->page_stride | c->token_stride | c->head_stride) >> 39) return TP3D_EUNSUPPORTED;  // a tensor map's strides
+  if (!aligned16(c->k) || !aligned16(c->v) || (c->page_stride | c->token_stride | c->head_stride) % 8)
+    return TP3D_EALIGN;
+  return TP3D_OK;
+}
+
+// bytes from a strided (page, token, head) array's first element to its last;
+// strides are the caller's and may be anything, so the sum is kept from
+// wrapping (an array that long overlaps everything above it)
+inline size_t extent(int64_t pages, int64_t ps, int64_t tokens, int64_t ts, int64_t heads, int64_t hs, int64_t d,
+                     int elem_bytes = 2) {
+  const unsigned __int128 n = ((unsigned __int128)(pages - 1) * (uint64_t)ps +
+                               (unsigned __int128)(tokens - 1) * (uint64_t)ts +
+                               (unsigned __int128)(heads - 1) * (uint64_t)hs + (uint64_t)d) *
+                              (unsigned)elem_bytes;
+  return n > (unsigned __int128)1 << 62 ? (size_t)1 << 62 : (size_t)n;
+}
+inline size_t cache_bytes(const tp3d_kv_cache& c) {
+  return extent(c.pages, c.page_stride, c.page, c.token_stride, c.kv_heads, c.head_stride, c.head_dim);
+}
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+// any output overlapping an input or another output
+template <int NO, int NI>
+bool clash(const Range (&out)[NO], const Range (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < NI; ++j)
+      if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
+inline unsigned blocks(const tp3d_ctx* ctx, int64_t threads, int per_sm) {
+  const int64_t n = (threads + kPagedThreads - 1) / kPagedThreads, most = (int64_t)ctx->num_sms * per_sm;
+  return (unsigned)(n < 1 ? 1 : n < most ? n : most);
+}
+
 #if defined(__CUDACC__)
 
 // Programmatic dependent launch.  The paged kernels follow one another in a
