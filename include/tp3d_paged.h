@@ -163,6 +163,89 @@ tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3
  * for heads of 128, 46 MB for heads of 64.                                   */
 size_t tp3d_paged_attn_workspace_bytes(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int heads);
 
+/* The bookkeeping of a cache's pages, for sharing, giving back and moving them.
+ * One pool serves every layer whose caches use the same block tables: these
+ * calls are made once, tp3d_paged_copy for each layer.
+ *   page          tokens per page, as in tp3d_kv_cache
+ *   rows          rows of the block table, up to 16384 (else
+ *                 TP3D_EUNSUPPORTED), one for each request that can be held
+ *   block_table   rows x table_width int32, dense rows; a negative entry names
+ *                 no page
+ *   pages         pages of the pool
+ *   shares        pages int32: the rows that name a page, less one; 0 for a page
+ *                 with one owner, as tp3d_paged_plan leaves those it hands out,
+ *                 and for a free one
+ *   free_pages    the stack of tp3d_paged_plan, free_cap >= pages entries (else
+ *                 TP3D_ESHAPE)
+ * All 4-byte aligned.  What the device finds not to fit raises TP3D_EPAGES, and
+ * nothing is read or written out of bounds.                                  */
+typedef struct {
+  int32_t page, rows;
+  int64_t pages, table_width, free_cap;
+  int32_t *block_table, *shares, *free_pages;
+} tp3d_page_pool;
+
+/* Forks requests (samples of one prompt, beams): for i < forks, row dst[i] of
+ * the table gets the first len[i] tokens of row src[i].  Whole pages are shared:
+ * their entries are copied and their shares grow by one (entries that name no
+ * page, behind a window, are copied alone).  A partly filled last page, which
+ * both requests will write, is the fork's own: a page from the free list, whose
+ * contents the caller copies,
+ *   copy_from[n] -> copy_to[n], n < *copy_count,
+ * in the order of the forks (tp3d_paged_copy).  The arrays have room for `forks`
+ * entries each; those from *copy_count on are not written.  Entries of row dst[i] past the
+ * len[i] tokens are left as they are: pages that it names there have been given
+ * back before.  *free_left is the free count after the call, as in
+ * tp3d_paged_plan.  A request that is cut back into a page that it shares is
+ * forked to its new length before it is written.
+ * A row out of range, a dst row that is another dst or a src, a length that is
+ * negative or longer than the row, a last page without a valid entry, or too few
+ * free pages raise TP3D_EPAGES, and nothing but *copy_count = 0 and *free_left is
+ * written.  forks <= 16384 (else TP3D_EUNSUPPORTED).                           */
+tp3d_status tp3d_paged_fork(tp3d_ctx* ctx, const tp3d_page_pool* pool, int forks, const int32_t* src,
+                            const int32_t* dst, const int32_t* len, const int32_t* free_count, int32_t* free_left,
+                            int32_t* copy_from, int32_t* copy_to, int32_t* copy_count, void* stream);
+
+/* Gives pages back: columns [first[r], end[r]) of every row r of the table are
+ * set to -1 (nothing where end <= first), and each page that they named loses an
+ * owner.  Pages that have lost their last join the free list above free_count,
+ * the highest first, so that the lowest are taken first again; *free_left is the
+ * new count.  A request that ends gives up [0, ceil(kv / page)); one that is cut
+ * back, the columns past its new length; one with a sliding window (and pages of
+ * first tokens that stay), those behind the window.
+ * Columns out of range (that row then gives up nothing), entries past the pool,
+ * a page that loses more owners than it has (it is freed once), and a free list
+ * that is full raise TP3D_EPAGES.  That a row names no page which is free already
+ * is the caller's to keep.                                                    */
+tp3d_status tp3d_paged_free(tp3d_ctx* ctx, const tp3d_page_pool* pool, const int32_t* first, const int32_t* end,
+                            const int32_t* free_count, int32_t* free_left, void* stream);
+
+/* Draws the used pages together at the pool's start, so that its end can be
+ * given up: with F = *free_count, the n-th (in ascending order) used page past
+ * pages - F moves to the n-th free page below it.  Entries of columns
+ * [0, ceil(kv_len[r] / page)) of each row, and the shares, follow; the free list
+ * becomes pages - 1, ..., pages - F; page_map (pages int32) tells where each used
+ * page is now, -1 for a free one.  The contents move by
+ *   copy_from[n] -> copy_to[n], n < *copy_count,
+ * (tp3d_paged_copy, before anything else is written to the cache); the arrays
+ * have room for pages / 2 entries each.  Used is every page that is not in the
+ * free list, whether a row names it or not.
+ * A free list with an entry out of range or twice, or a free_count out of range,
+ * raises TP3D_EPAGES; the tables and the list are then left as they are, page_map is
+ * the identity and *copy_count 0.  So does a row's length that does not fit (its
+ * entries are left as they are), and an entry past the pool or naming a free page.  */
+tp3d_status tp3d_paged_compact(tp3d_ctx* ctx, const tp3d_page_pool* pool, const int32_t* kv_len,
+                               const int32_t* free_count, int32_t* page_map, int32_t* copy_from, int32_t* copy_to,
+                               int32_t* copy_count, void* stream);
+
+/* Copies whole pages of a cache, keys and values: page copy_from[n] to page
+ * copy_to[n] for n < min(copies, *copy_count), or n < copies with copy_count
+ * NULL.  No page may be written twice, or read and written, in one call (a fork's
+ * and a compaction's lists are like that).  A page outside the pool is skipped
+ * and raises TP3D_EPAGES, as does a count out of [0, copies].                 */
+tp3d_status tp3d_paged_copy(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t copies, const int32_t* copy_from,
+                            const int32_t* copy_to, const int32_t* copy_count, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

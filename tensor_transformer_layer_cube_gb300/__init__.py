@@ -46,6 +46,7 @@ __all__ = [
     "tp3d_rope", "rope", "rope_turns", "tp3d_rope_turns", "tp3d_qk_rope", "tp3d_qk_rope_bwd",
     "tp3d_qk_rope_bwd_workspace_bytes", "tp3d_paged_rope_store", "TP3D_ROPE_PLAIN", "TP3D_ROPE_LINEAR",
     "TP3D_ROPE_BASE", "TP3D_ROPE_PARTS",
+    "tp3d_page_pool", "page_pool", "tp3d_paged_fork", "tp3d_paged_free", "tp3d_paged_compact", "tp3d_paged_copy",
 ]
 
 STATUS = {0: "TP3D_OK", 1: "TP3D_EINVAL", 2: "TP3D_ESHAPE", 3: "TP3D_EALIGN", 4: "TP3D_EDTYPE",
@@ -96,6 +97,12 @@ class tp3d_paged_batch(ctypes.Structure):
 
 class tp3d_row_strides(ctypes.Structure):
     _fields_ = [("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class tp3d_page_pool(ctypes.Structure):
+    _fields_ = [("page", ctypes.c_int32), ("rows", ctypes.c_int32), ("pages", ctypes.c_int64),
+                ("table_width", ctypes.c_int64), ("free_cap", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+                ("shares", ctypes.c_void_p), ("free_pages", ctypes.c_void_p)]
 
 
 class tp3d_rope(ctypes.Structure):
@@ -202,6 +209,12 @@ _SIGS = {
                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "tp3d_paged_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.POINTER(tp3d_kv_cache),
                                                           ctypes.c_int]),
+    "tp3d_paged_fork": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_page_pool), ctypes.c_int] +
+                        [ctypes.c_void_p] * 9),
+    "tp3d_paged_free": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_page_pool)] + [ctypes.c_void_p] * 5),
+    "tp3d_paged_compact": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_page_pool)] + [ctypes.c_void_p] * 7),
+    "tp3d_paged_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_kv_cache), ctypes.c_int64] +
+                        [ctypes.c_void_p] * 4),
     "tp3d_rope_turns": (ctypes.c_int, [ctypes.c_int, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double,
                                        ctypes.c_void_p, ctypes.POINTER(ctypes.c_float)]),
     "tp3d_qk_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_rope), ctypes.c_int64, ctypes.c_int,
@@ -437,6 +450,53 @@ def tp3d_paged_attn(ctx, cache: tp3d_kv_cache, batch: tp3d_paged_batch, Q, O, ls
 
 def tp3d_paged_attn_workspace_bytes(ctx, cache: tp3d_kv_cache, heads: int) -> int:
     return lib().tp3d_paged_attn_workspace_bytes(ctx, ctypes.byref(cache), heads)
+
+
+def page_pool(page: int, block_table, shares, free_pages) -> tp3d_page_pool:
+    """The descriptor of a pool's bookkeeping (int32 device tensors; the table as dense rows, one share count for each
+    page).  It holds their addresses: keep the tensors."""
+    if block_table.dim() != 2 or shares.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("page_pool: block_table (rows, width), shares (pages), free_pages (entries)")
+    _words("page_pool", (block_table, None), (shares, None), (free_pages, None))
+    return tp3d_page_pool(page, block_table.shape[0], shares.numel(), block_table.shape[1], free_pages.numel(),
+                          block_table.data_ptr(), shares.data_ptr(), free_pages.data_ptr())
+
+
+def _words(what, *arrays):
+    """Pointers of contiguous int32 tensors of at least so many elements."""
+    for x, n in arrays:
+        if _dtype_of(x) != _I32 or not x.is_contiguous() or (n is not None and x.numel() < n):
+            raise ValueError(f"{what}: contiguous int32 tensors, one element for each of what they describe")
+    return [x.data_ptr() for x, _ in arrays]
+
+
+def tp3d_paged_fork(ctx, pool: tp3d_page_pool, src, dst, len, free_count, free_left, copy_from, copy_to, copy_count,
+                    stream=None) -> int:
+    """One fork for each element of ``src``."""
+    n = src.numel()
+    return lib().tp3d_paged_fork(ctx, ctypes.byref(pool), n,
+                                 *_words("tp3d_paged_fork", (src, n), (dst, n), (len, n), (free_count, 1),
+                                         (free_left, 1), (copy_from, n), (copy_to, n), (copy_count, 1)), _s(stream))
+
+
+def tp3d_paged_free(ctx, pool: tp3d_page_pool, first, end, free_count, free_left, stream=None) -> int:
+    return lib().tp3d_paged_free(ctx, ctypes.byref(pool),
+                                 *_words("tp3d_paged_free", (first, pool.rows), (end, pool.rows), (free_count, 1),
+                                         (free_left, 1)), _s(stream))
+
+
+def tp3d_paged_compact(ctx, pool: tp3d_page_pool, kv_len, free_count, page_map, copy_from, copy_to, copy_count,
+                       stream=None) -> int:
+    n = pool.pages
+    return lib().tp3d_paged_compact(ctx, ctypes.byref(pool),
+                                    *_words("tp3d_paged_compact", (kv_len, pool.rows), (free_count, 1), (page_map, n),
+                                            (copy_from, n // 2), (copy_to, n // 2), (copy_count, 1)), _s(stream))
+
+
+def tp3d_paged_copy(ctx, cache: tp3d_kv_cache, copies: int, copy_from, copy_to, copy_count=None, stream=None) -> int:
+    at, to = _words("tp3d_paged_copy", (copy_from, copies), (copy_to, copies))
+    count = None if copy_count is None else _words("tp3d_paged_copy", (copy_count, 1))[0]
+    return lib().tp3d_paged_copy(ctx, ctypes.byref(cache), copies, at, to, count, _s(stream))
 
 
 # ---------------------------------------------------------------------------

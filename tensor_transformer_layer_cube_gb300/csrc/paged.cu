@@ -60,21 +60,6 @@ __device__ __forceinline__ Lengths plan_lengths(const PlanArgs& P, int b) {
   return l;
 }
 
-__device__ __forceinline__ int32_t pages_of(int64_t n, int page_log2) {
-  return (int32_t)((n + (1 << page_log2) - 1) >> page_log2);
-}
-
-// the last index i in [0, n) with a[i] <= x (a non-decreasing, a[0] <= x)
-__device__ __forceinline__ int last_at_most(const int32_t* a, int n, int32_t x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 __global__ void __launch_bounds__(kPagedThreads) paged_plan_kernel(const PlanArgs P) {
   extern __shared__ int32_t plan_smem[];
   int32_t* sf = plan_smem;                    // exclusive sums of fresh, requests + 1

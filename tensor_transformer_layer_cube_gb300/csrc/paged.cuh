@@ -128,6 +128,21 @@ tp3d_status launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned 
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...) == cudaSuccess ? TP3D_OK : TP3D_ECUDA;
 }
 
+__device__ __forceinline__ int32_t pages_of(int64_t n, int page_log2) {
+  return (int32_t)((n + (1 << page_log2) - 1) >> page_log2);
+}
+
+// the last index i in [0, n) with a[i] <= x (a non-decreasing, a[0] <= x)
+__device__ __forceinline__ int last_at_most(const int32_t* a, int n, int32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 // A request as the attention kernels see it: rows [q0, q0 + n) of Q, kv keys.
 // Lengths that do not fit are clamped, so that whatever the buffers hold, no
 // access leaves them; a request that was clamped raises TP3D_EPAGES.
