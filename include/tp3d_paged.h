@@ -157,7 +157,21 @@ tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3
                             float scale, const void* Q, tp3d_row_strides q_strides, void* O,
                             tp3d_row_strides o_strides, float* lse, void* workspace, void* stream);
 
-/* Bytes of tp3d_paged_attn's workspace for this cache and head count on the
+/* tp3d_paged_attn with a sliding window and first tokens that stay visible: the
+ * row at position p = kv_b - n_b + j sees the keys k <= p with
+ *   k > p - window  or  k < sinks.
+ * window >= 1, sinks >= 0 (else TP3D_EINVAL); a window longer than any request
+ * is tp3d_paged_attn.  Keys between the first ones and the first new row's window are
+ * not read, and pages that hold nothing else may have been given back: their
+ * table entries are not used.  Everything else is as in tp3d_paged_attn: keys
+ * that a row does not see, their values and scores that are not finite among them,
+ * have no effect on it.                                                      */
+tp3d_status tp3d_paged_attn_window(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3d_paged_batch* batch, int heads,
+                                   float scale, int64_t window, int64_t sinks, const void* Q,
+                                   tp3d_row_strides q_strides, void* O, tp3d_row_strides o_strides, float* lse,
+                                   void* workspace, void* stream);
+
+/* Bytes of tp3d_paged_attn's and tp3d_paged_attn_window's workspace for this cache and head count on the
  * context's device (it does not depend on the batch); 0 for an invalid
  * argument.  Both kernels' parts of split work, for every SM: with 152 SMs 91 MB
  * for heads of 128, 46 MB for heads of 64.                                   */

@@ -52,8 +52,9 @@ def store(pool, new, slots):
     return out
 
 
-def attention(q, k_pool, v_pool, table, q_start, kv_len, scale):
-    """q (token, head, column), pools (page, token, kv head, column).  Returns
+def attention(q, k_pool, v_pool, table, q_start, kv_len, scale, window=None, sinks=0):
+    """q (token, head, column), pools (page, token, kv head, column); with a window a row at position p sees only the
+    keys after p - window and the first ``sinks``.  Returns
     (o, lse, absum, amax): absum = sum_k p_k |v_k| and amax = max_k scale
     sum_c |q_c k_kc| of each row's keys, for error bounds.  Rows of no request
     and rows without keys: o = 0, lse = -inf."""
@@ -69,14 +70,18 @@ def attention(q, k_pool, v_pool, table, q_start, kv_len, scale):
         if q1 == q0 or kv <= 0:
             continue
         pages = [int(x) for x in table[b][:-(-kv // page)]]
-        k = np.concatenate([k_pool[p] for p in pages])[:kv].astype(np.float64)
-        v = np.concatenate([v_pool[p] for p in pages])[:kv].astype(np.float64)
+        # (pages that no row sees may be gone: entries outside the pool)
+        k, v = (np.concatenate([pool[p] if 0 <= p < len(pool) else np.full(pool.shape[1:], np.nan)
+                                for p in pages])[:kv].astype(np.float64) for pool in (k_pool, v_pool))
         for j in range(q1 - q0):
             n = kv - (q1 - q0) + j + 1  # keys this row sees
             if n <= 0:
                 continue
+            sees = slice(0, n)
+            if window is not None and n > window:
+                sees = np.r_[0:min(sinks, n - window), n - window:n]
             for i in range(heads):
-                kk, vv = k[:n, i // g], v[:n, i // g]
+                kk, vv = k[sees, i // g], v[sees, i // g]
                 x = q[q0 + j, i].astype(np.float64)
                 s = scale * (kk @ x)
                 m = s.max()

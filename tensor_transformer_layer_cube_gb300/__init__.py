@@ -46,7 +46,7 @@ __all__ = [
     "tp3d_rope", "rope", "rope_turns", "tp3d_rope_turns", "tp3d_qk_rope", "tp3d_qk_rope_bwd",
     "tp3d_qk_rope_bwd_workspace_bytes", "tp3d_paged_rope_store", "TP3D_ROPE_PLAIN", "TP3D_ROPE_LINEAR",
     "TP3D_ROPE_BASE", "TP3D_ROPE_PARTS",
-    "tp3d_page_pool", "page_pool", "tp3d_paged_fork", "tp3d_paged_free", "tp3d_paged_compact", "tp3d_paged_copy",
+    "tp3d_paged_attn_window", "tp3d_page_pool", "page_pool", "tp3d_paged_fork", "tp3d_paged_free", "tp3d_paged_compact", "tp3d_paged_copy",
 ]
 
 STATUS = {0: "TP3D_OK", 1: "TP3D_EINVAL", 2: "TP3D_ESHAPE", 3: "TP3D_EALIGN", 4: "TP3D_EDTYPE",
@@ -207,6 +207,11 @@ _SIGS = {
                                        ctypes.POINTER(tp3d_paged_batch), ctypes.c_int, ctypes.c_float,
                                        ctypes.c_void_p, tp3d_row_strides, ctypes.c_void_p, tp3d_row_strides,
                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "tp3d_paged_attn_window": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_kv_cache),
+                                              ctypes.POINTER(tp3d_paged_batch), ctypes.c_int, ctypes.c_float,
+                                              ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, tp3d_row_strides,
+                                              ctypes.c_void_p, tp3d_row_strides, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_void_p]),
     "tp3d_paged_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.POINTER(tp3d_kv_cache),
                                                           ctypes.c_int]),
     "tp3d_paged_fork": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(tp3d_page_pool), ctypes.c_int] +
@@ -436,16 +441,28 @@ def tp3d_paged_store(ctx, cache: tp3d_kv_cache, K, V, slots, stream=None) -> int
 def tp3d_paged_attn(ctx, cache: tp3d_kv_cache, batch: tp3d_paged_batch, Q, O, lse, scale, workspace,
                     stream=None) -> int:
     """Q, O: (token, head, column) tensors; lse: dense (token, head) float32 or None."""
+    heads, rows = _attn_rows("tp3d_paged_attn", cache, batch, Q, O, lse)
+    return lib().tp3d_paged_attn(ctx, ctypes.byref(cache), ctypes.byref(batch), heads, scale, *rows, _p(lse),
+                                 _p(workspace), _s(stream))
+
+
+def tp3d_paged_attn_window(ctx, cache: tp3d_kv_cache, batch: tp3d_paged_batch, Q, O, lse, scale, window, sinks,
+                           workspace, stream=None) -> int:
+    """tp3d_paged_attn over a sliding window of ``window`` keys and the first ``sinks`` ones."""
+    heads, rows = _attn_rows("tp3d_paged_attn_window", cache, batch, Q, O, lse)
+    return lib().tp3d_paged_attn_window(ctx, ctypes.byref(cache), ctypes.byref(batch), heads, scale, window, sinks,
+                                        *rows, _p(lse), _p(workspace), _s(stream))
+
+
+def _attn_rows(what, cache, batch, Q, O, lse):
     shape, qs, os_ = Q.shape, Q.stride(), O.stride()
     dt = cache.dtype
     if len(shape) != 3 or O.shape != shape or qs[2] != 1 or os_[2] != 1 or shape[0] < batch.tokens or \
             shape[2] != cache.head_dim or _dtype_of(Q) != dt or _dtype_of(O) != dt:
-        raise ValueError("tp3d_paged_attn: Q and O (tokens, heads, head_dim) of the cache's type, contiguous columns")
+        raise ValueError(f"{what}: Q and O (tokens, heads, head_dim) of the cache's type, contiguous columns")
     if lse is not None and (not lse.is_contiguous() or lse.shape != shape[:2] or _dtype_of(lse) != TP3D_F32):
-        raise ValueError("tp3d_paged_attn: lse dense (tokens, heads) float32")
-    return lib().tp3d_paged_attn(ctx, ctypes.byref(cache), ctypes.byref(batch), shape[1], scale, Q.data_ptr(),
-                                 tp3d_row_strides(qs[0], qs[1]), O.data_ptr(), tp3d_row_strides(os_[0], os_[1]),
-                                 _p(lse), _p(workspace), _s(stream))
+        raise ValueError(f"{what}: lse dense (tokens, heads) float32")
+    return shape[1], (Q.data_ptr(), tp3d_row_strides(qs[0], qs[1]), O.data_ptr(), tp3d_row_strides(os_[0], os_[1]))
 
 
 def tp3d_paged_attn_workspace_bytes(ctx, cache: tp3d_kv_cache, heads: int) -> int:

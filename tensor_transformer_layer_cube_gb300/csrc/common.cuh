@@ -35,7 +35,9 @@ struct tp3d_ctx {
   // kernel for many rows leaves for the one for few, the arrivals and counts of
   // rope.cu and paged_pages.cu (zero between calls)
   unsigned* d_paged;
-  int paged_ready;  // paged kernels that are set up (bits: attention with heads of 128, of 64, plans of many requests)
+  // paged kernels that are set up (bits: attention with heads of 128, of 64, plans of many requests, forks and the
+  // like; from bit 4 the attentions with a window)
+  int paged_ready;
   // CUDA graphs of whole layer calls keyed by their arguments (graph.cu), the
   // stream they run on, and the events that order it with the caller's stream
   void* graphs;

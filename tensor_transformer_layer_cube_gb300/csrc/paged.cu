@@ -283,9 +283,10 @@ size_t tp3d_paged_attn_workspace_bytes(tp3d_ctx* ctx, const tp3d_kv_cache* cache
   return paged_attn_workspace(ctx, cache->head_dim);
 }
 
-tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3d_paged_batch* batch, int heads,
-                            float scale, const void* Q, tp3d_row_strides q_strides, void* O,
-                            tp3d_row_strides o_strides, float* lse, void* workspace, void* stream) {
+// window 0: every key up to the row's own
+static tp3d_status attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3d_paged_batch* batch, int heads,
+                        float scale, int64_t window, int64_t sinks, const void* Q, tp3d_row_strides q_strides, void* O,
+                        tp3d_row_strides o_strides, float* lse, void* workspace, void* stream) {
   if (!ctx || !batch || heads < 1) return TP3D_EINVAL;
   TP3D_TRY(check_cache(cache));
   if (!(scale > 0.0f) || !isfinite(scale)) return TP3D_EINVAL;
@@ -325,6 +326,11 @@ tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3
   A.table = batch->block_table;
   A.width = batch->table_width;
   A.scale = scale;
+  // a window that the tables have no room to pass leaves nothing out
+  if (window < batch->table_width << A.page_log2 && window < kPagedMaxTokens) {
+    A.window = (int32_t)window;
+    A.sinks = (int32_t)(sinks < kPagedMaxTokens ? sinks : kPagedMaxTokens);
+  }
   A.q = static_cast<const __nv_bfloat16*>(Q);
   A.q_token = q_strides.token_stride;
   A.q_head = q_strides.head_stride;
@@ -335,6 +341,20 @@ tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3
   A.err = ctx->d_err;
   A.stall_after = ctx->stall_after;
   return launch_paged_attn(ctx, A, batch->max_new, workspace, as_stream(stream));
+}
+
+tp3d_status tp3d_paged_attn(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3d_paged_batch* batch, int heads,
+                            float scale, const void* Q, tp3d_row_strides q_strides, void* O,
+                            tp3d_row_strides o_strides, float* lse, void* workspace, void* stream) {
+  return attn(ctx, cache, batch, heads, scale, 0, 0, Q, q_strides, O, o_strides, lse, workspace, stream);
+}
+
+tp3d_status tp3d_paged_attn_window(tp3d_ctx* ctx, const tp3d_kv_cache* cache, const tp3d_paged_batch* batch, int heads,
+                                   float scale, int64_t window, int64_t sinks, const void* Q,
+                                   tp3d_row_strides q_strides, void* O, tp3d_row_strides o_strides, float* lse,
+                                   void* workspace, void* stream) {
+  if (window < 1 || sinks < 0) return TP3D_EINVAL;
+  return attn(ctx, cache, batch, heads, scale, window, sinks, Q, q_strides, O, o_strides, lse, workspace, stream);
 }
 
 }  // extern "C"

@@ -20,6 +20,7 @@ struct PagedAttn {
   const int32_t *q_start, *kv_len, *table;
   int64_t width;  // block table columns
   float scale;
+  int32_t window, sinks;  // keys that a row sees up to its own, and first ones that it sees besides (window 0: all)
   const __nv_bfloat16* q;
   int64_t q_token, q_head;
   __nv_bfloat16* o;

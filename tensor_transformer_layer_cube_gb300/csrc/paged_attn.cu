@@ -4,7 +4,9 @@
 // the keys k = 0 .. kv_b - n_b + j:
 //   s_k = scale q . k_k,  m = max s_k,  l = sum exp(s_k - m),
 //   O = sum exp(s_k - m) v_k / l,  lse = m + log l,
-// in one pass over the keys with a running m, l and O.
+// in one pass over the keys with a running m, l and O.  With a window of w
+// keys and f first ones that stay visible, the row at position p sees of these
+// only k > p - w and k < f (WIN in the kernels).
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -98,7 +100,9 @@ struct FewShared {
   int b0;
   int last;
   int poisoned;
-  int poison[128];  // per column: the first key with a non-finite value that some row does not see
+  // per column: the first key with a non-finite value that some row does not see; with a window the rows of the
+  // block that see such a key, a bit each
+  int poison[128];
 };
 
 TP3D_HD constexpr uint32_t few_stage_bytes(int d) { return 16u * 4u * (uint32_t)d; }  // 16 keys, then 16 values
@@ -198,11 +202,33 @@ struct Ranges {
   }
 };
 
+// With a window the keys of a request that none of its new rows sees lie
+// between the first keys and the first row's window: [first, low).  Tiles that
+// hold nothing else are left out of the sequence: of a request's tiles the first
+// `lead` are its first ones, and `gap` are missing behind them.
+struct Gap {
+  int lead = 0, gap = 0;
+  __device__ void set(int first_tiles, int low_tile) {
+    lead = first_tiles < low_tile ? first_tiles : low_tile;
+    gap = low_tile - lead;
+  }
+  // a tile's number among all
+  __device__ int tile(int j) const { return j >= lead ? j + gap : j; }
+  // the position of the first tile there is from tile t on
+  __device__ int at(int t) const { return t < lead ? t : t - gap > lead ? t - gap : lead; }
+};
+// the first key in the window of the row at position p
+__device__ __forceinline__ int window_begin(int64_t p, int window) {
+  return p >= window ? (int)(p - window + 1) : 0;
+}
+
 // A position in a CTA's range: tile `tile`, below `end`, of the `tiles` of
 // (request b, head h, rows from row0), whose first is unit `at`.
-template <int W>
+template <int W, bool WIN>
 struct FewCursor {
   using Shape = FewShape<W>;
+  Gap gap;
+  int low;  // the first key of the first row's window
   int b, h, row0, tile, end, tiles, n, kv, at, u1;  // u1: the range's end (before it is moved)
   int64_t q0;
   // takes request b; tiles = 0 where it is not this kernel's
@@ -213,11 +239,21 @@ struct FewCursor {
     q0 = r.q0;
     const int64_t rows = (int64_t)n * A.group;
     tiles = kv > 0 ? (kv - 1) / Shape::kKeys + 1 : 1;  // a request without keys still has rows to write
+    if (WIN) {
+      low = window_begin((int64_t)kv - n, A.window);
+      const int first = A.sinks < kv ? A.sinks : kv;
+      gap.set((first + Shape::kKeys - 1) / Shape::kKeys, low / Shape::kKeys);
+      tiles -= gap.gap;
+    }
     if (rows == 0 || rows > A.few_rows) {
       tiles = 0;
       if (alone && rows) raise_error(A.err, TP3D_EPAGES);
     }
   }
+  // the first key of the item's tile t
+  __device__ int key(int t) const { return (WIN ? gap.tile(t) : t) * Shape::kKeys; }
+  // keys [k, k + 16) are seen by no row
+  __device__ bool unseen(const PagedAttn& A, int k) const { return WIN && k >= A.sinks && k + 16 <= low; }
   // an item's length in the sequence
   __device__ int span() const { return tiles + Shape::kEnd; }
   // blocks of 16 rows (of a request that is this kernel's)
@@ -273,7 +309,7 @@ __device__ __forceinline__ void see_waited(unsigned* word) {
 }
 
 // `alone`: no other kernel of the call takes the requests with more rows
-template <int D, int W>
+template <int D, int W, bool WIN>
 __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
     paged_attn_few_kernel(const PagedAttn A, bool alone, float* __restrict__ parts, unsigned* __restrict__ counters,
                           unsigned* waited) {
@@ -281,6 +317,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
   constexpr int kThreads = Shape::kThreads, kKeys = Shape::kKeys;
   constexpr int RV = D / 8, NT = D / 8;  // 16-byte vectors of a row, 8-column tiles of O
   constexpr uint32_t kStage = few_stage_bytes(D);
+  constexpr int kNoPoison = WIN ? 0 : INT32_MAX;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const ring_ptr = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
   FewShared<W>& sh = *reinterpret_cast<FewShared<W>*>(ring_ptr + W * kFewStages * kStage);
@@ -300,7 +337,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
   };
 
   // ---- this CTA's range of the tile sequence
-  FewCursor<W> c;
+  FewCursor<W, WIN> c;
   unsigned units = 0, ctas = 0;
   {
     // sums of the tiles over the requests, kThreads at a time; a second
@@ -367,7 +404,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
       }
       if (one) break;
     }
-    if (tid < 128) sh.poison[tid] = INT32_MAX;
+    if (tid < 128) sh.poison[tid] = kNoPoison;
     if (tid == 0) sh.poisoned = 0;
     __syncthreads();
     c.b = sh.b0;
@@ -389,7 +426,8 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
   uint32_t qf[D / 16][4];
   float o[NT][4], m[2], l[2];
   int lim[2];  // the last key that this thread's two rows see
-  FewCursor<W> ld = c;        // the tile to load next; c: to compute next
+  int low[2];  // the first key of their windows
+  FewCursor<W, WIN> ld = c;        // the tile to load next; c: to compute next
   bool begin = true, fetch = true;
   int tile0 = c.tile;      // where this CTA's share of the item begins
   int stage = 0;           // to load into; the next one is the oldest
@@ -401,14 +439,15 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
       if (ld.b != pages_b || (unsigned)(ld.tile - pages_at) >= 32u) {
         pages_b = ld.b;
         pages_at = ld.tile;
-        const int64_t key = (int64_t)(ld.tile + lane) * kKeys + warp * 16;
-        pages = key < ld.kv ? ld_plain(A.table + (int64_t)ld.b * A.width + (key >> A.page_log2)) : -1;
+        const int t = ld.tile + lane;
+        const int64_t key = (int64_t)(WIN ? ld.gap.tile(t) : t) * kKeys + warp * 16;
+        pages = key < ld.kv && !ld.unseen(A, (int)key) ? ld_plain(A.table + (int64_t)ld.b * A.width + (key >> A.page_log2)) : -1;
       }
       const int page = __shfl_sync(0xffffffffu, pages, ld.tile - pages_at);
-      const int key = ld.tile * kKeys + warp * 16, left = ld.kv - key;
+      const int key = ld.key(ld.tile) + warp * 16, left = ld.kv - key;
       if (left > 0) {
         const bool in = page >= 0 && page < A.c.pages;
-        if (!in) raise_error(A.err, TP3D_EPAGES);
+        if (!in && !ld.unseen(A, key)) raise_error(A.err, TP3D_EPAGES);
         // lane -> vector (lane % RV) of rows lane / RV + i * (32 / RV); vector v of row r lies at
         // v ^ (r mod 8), so that the eight rows of an 8 x 8 block fall in different banks
         const int v = lane & (RV - 1), r0 = lane / RV;
@@ -423,7 +462,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
         for (int i = 0; i < RV / 2; ++i) {
           const int r = r0 + i * (32 / RV);
           const uint32_t to = dst + (uint32_t)(r * RV + (v ^ (r & 7))) * 16u;
-          const bool have = in && r < left;
+          const bool have = in && r < left && (!WIN || key + r < A.sinks || key + r >= ld.low);
           cp_async16_zfill(to, have ? ks : static_cast<const bf16*>(A.c.k), have);
           cp_async16_zfill(to + kStage / 2, have ? vs : static_cast<const bf16*>(A.c.v), have);
           ks += hop;
@@ -446,6 +485,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
         const bool in = r < rows;
         const int tok = in ? (c.row0 + r) / A.group : 0, g = in ? c.row0 + r - tok * A.group : 0;
         lim[e] = in ? c.kv - c.n + tok : c.kv - 1;
+        if (WIN) low[e] = window_begin(lim[e], A.window);
         const bf16* src = A.q + (c.q0 + tok) * A.q_token + (int64_t)(c.h * A.group + g) * A.q_head + (lane & 3) * 2;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -463,14 +503,15 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
     cp_wait<kFewStages - 1>();
     __syncwarp();
     const uint32_t sk = ring + (uint32_t)stage * kStage, sv = sk + kStage / 2;
-    const int key0 = c.tile * kKeys + warp * 16;
+    const int key0 = c.key(c.tile) + warp * 16;
     if (key0 < c.kv) {
-      // keys that some row does not see: past kv - n
-      const bool partial = key0 + 15 > c.kv - c.n;
+      // keys that some row does not see: past kv - n; before the last row's window
+      const int last_low = WIN ? window_begin((int64_t)c.kv - 1, A.window) : 0;
+      const bool partial = key0 + 15 > c.kv - c.n || (WIN && key0 < last_low && key0 + 15 >= A.sinks);
       if (partial && c.n > 1) {
         // A probability of 0 does not silence a value that is not finite: such
         // a value becomes 0, and rows that see its key get NaN in its column
-        // at the end.
+        // at the end.  (Keys that no row sees are zeros in the stage.)
 #pragma unroll 1
         for (int i = lane; i < 16 * RV; i += 32) {
           const int r = i / RV, v = i & (RV - 1);
@@ -478,8 +519,20 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
           const uint4 x = ld_shared4(at);
           __nv_bfloat162 seen = __floats2bfloat162_rn(0.0f, 0.0f);
           watch_finite(seen, x);
-          if (key0 + r <= c.kv - c.n || !saw_not_finite(seen)) continue;
-          st_shared4(at, make_finite(x, [&](int e) { atomicMin(&sh.poison[v * 8 + e], key0 + r); }));
+          const int k = key0 + r;
+          if ((k <= c.kv - c.n && (!WIN || k >= last_low || k < A.sinks)) || !saw_not_finite(seen)) continue;
+          int note = k;
+          if (WIN) {
+            note = 0;
+            for (int q = 0; q < rows; ++q) {
+              const int p = c.kv - c.n + (c.row0 + q) / A.group;
+              if (k <= p && (k >= window_begin(p, A.window) || k < A.sinks)) note |= 1 << q;
+            }
+          }
+          st_shared4(at, make_finite(x, [&](int e) {
+                       if (WIN) atomicOr(&sh.poison[v * 8 + e], note);
+                       else atomicMin(&sh.poison[v * 8 + e], note);
+                     }));
           sh.poisoned = 1;
         }
         __syncwarp();
@@ -509,7 +562,10 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float v = s[x][0][e] + s[x][1][e];
-          if (partial && key0 + x * 8 + (lane & 3) * 2 + (e & 1) > lim[e >> 1]) v = -INFINITY;
+          if (partial) {
+            const int k = key0 + x * 8 + (lane & 3) * 2 + (e & 1);
+            if (k > lim[e >> 1] || (WIN && k < low[e >> 1] && k >= A.sinks)) v = -INFINITY;
+          }
           s[x][0][e] = v;
           mt[e >> 1] = fmaxf(mt[e >> 1], v);
         }
@@ -640,7 +696,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
           float* const x = reinterpret_cast<float*>(&acc);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (sh.poison[col + e] <= lr) x[e] = __int_as_float(0x7fffffff);
+            if (WIN ? (sh.poison[col + e] >> r) & 1 : sh.poison[col + e] <= lr) x[e] = __int_as_float(0x7fffffff);
         }
         if (whole) finish(r, col, acc, top, sum);
         else put(at((int)blockIdx.x - c0), r, col, acc, top, sum);
@@ -726,7 +782,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
       begin = true;
       __syncthreads();  // the stages go back to the loads
       if (hurt) {
-        if (tid < 128) sh.poison[tid] = INT32_MAX;
+        if (tid < 128) sh.poison[tid] = kNoPoison;
         if (tid == 0) sh.poisoned = 0;
         __syncthreads();
       }
@@ -832,15 +888,34 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t a, uint32_t b)
 }
 
 // The pairs of query tiles of a request: pair k holds tokens [2 k tt, +2 tt).
+template <bool WIN>
 struct ManyRequest {
   int q0, n, kv, tt;  // tt: tokens of a query tile
+  int window, sinks;  // (first keys: no more than there are keys)
   __device__ int pairs() const { return (n + 2 * tt - 1) / (2 * tt); }
   // key tiles that tokens below `end` see (one at least: rows without keys are written too)
   __device__ int tiles_upto(int end) const {
     const int keys = kv - n + (end < n ? end : n);
     return keys > 0 ? (keys - 1) / TR + 1 : 1;
   }
-  __device__ int tiles(int k) const { return tiles_upto((k + 1) * 2 * tt); }
+  // key tiles that no row of pair k sees, between the first keys and its first row's window
+  __device__ Gap gap(int k) const {
+    Gap g;
+    if (WIN) g.set((sinks + TR - 1) / TR, window_begin((int64_t)kv - n + (int64_t)k * 2 * tt, window) / TR);
+    return g;
+  }
+  // the same of the pairs before pair k.  Pair i's window begins at c + w i, and what it misses are
+  // floor((c + w i) / TR) - lead tiles, from the first pair on where that is positive.
+  __device__ int64_t gaps_before(int k) const {
+    const int w = 2 * tt, lead = (sinks + TR - 1) / TR;
+    const int64_t c = (int64_t)kv - n - window + 1, from = ((int64_t)lead + 1) * TR;
+    const int64_t z = c >= from ? 0 : (from - c + w - 1) / w;
+    if (z >= k) return 0;
+    const int64_t b = c + w * z, left = k - z;
+    return left * (b / TR - lead) + (int64_t)(w / TR) * (left * (left - 1) / 2) +
+           floor_sum((uint32_t)left, (uint32_t)(w % TR), (uint32_t)(b % TR));
+  }
+  __device__ int tiles(int k) const { return tiles_upto((k + 1) * 2 * tt) - gap(k).gap; }
   // key tiles of the pairs before pair k (the last pair's are not among them)
   __device__ int64_t before(int k) const {
     const int w = 2 * tt, ctx = kv - n;
@@ -849,7 +924,7 @@ struct ManyRequest {
     const int b = ctx + (z + 1) * w + TR - 1;
     const int64_t left = k - z;
     return z + (int64_t)(b / TR) * left + (int64_t)(w / TR) * (left * (left - 1) / 2) +
-           floor_sum((uint32_t)left, (uint32_t)(w % TR), (uint32_t)(b % TR));
+           floor_sum((uint32_t)left, (uint32_t)(w % TR), (uint32_t)(b % TR)) - (WIN ? gaps_before(k) : 0);
   }
   __device__ int64_t total() const {
     const int p = pairs();
@@ -857,13 +932,18 @@ struct ManyRequest {
   }
 };
 
-__device__ __forceinline__ ManyRequest many_request(const PagedAttn& A, int b) {
+template <bool WIN>
+__device__ __forceinline__ ManyRequest<WIN> many_request(const PagedAttn& A, int b) {
   const PagedRequest r = paged_request(A, b);
-  ManyRequest m;
+  ManyRequest<WIN> m;
   m.q0 = (int)r.q0;
   m.n = (int64_t)r.n * A.group > A.few_rows ? r.n : 0;  // the others are the kernel above's
   m.kv = r.kv;
   m.tt = TR / A.group;
+  if (WIN) {
+    m.window = A.window;
+    m.sinks = A.sinks < r.kv ? A.sinks : r.kv;
+  }
   return m;
 }
 
@@ -882,8 +962,11 @@ __device__ __forceinline__ ManyRequest many_request(const PagedAttn& A, int b) {
 // 31.0 | 28.5; 4 x 200 over 3000 47.7 | 47.3.
 constexpr int kSnap = 4;
 constexpr int kManyMinTiles = 2;  // of a CTA's range, where there is little work (the first case above; with 1 30.3)
+template <bool WIN>
 struct ManyCursor {
-  ManyRequest r;
+  ManyRequest<WIN> r;
+  Gap gap;          // of the pair
+  int low0, low1;   // the pair's key tiles that some row's window leaves out in part: [low0, low1)
   int b, h, i, k, pairs;
   int j0, j1, nkv;  // nkv: the pair's key tiles
   int u, u1;        // the piece's first unit, the range's end (before it is moved)
@@ -898,6 +981,13 @@ struct ManyCursor {
   __device__ bool enter() {
     k = fold(i, pairs);
     nkv = r.tiles(k);
+    if (WIN) {
+      gap = r.gap(k);
+      const int end = (k + 1) * 2 * r.tt < r.n ? (k + 1) * 2 * r.tt : r.n;
+      const int last_low = window_begin((int64_t)r.kv - r.n + end - 1, r.window);  // of the pair's last row
+      low0 = gap.at(r.sinks / TR);
+      low1 = last_low > r.sinks ? gap.at((last_low - 1) / TR) + 1 : low0;
+    }
     const int end = u1 - (u - j0);
     j1 = end >= nkv ? nkv : end > 0 ? snap(end, nkv) : 0;
     return j1 > j0;
@@ -909,7 +999,7 @@ struct ManyCursor {
       i = 0;
       if (++h == A.c.kv_heads) {
         h = 0;
-        do r = many_request(A, ++b);
+        do r = many_request<WIN>(A, ++b);
         while (r.n == 0);
         pairs = r.pairs();
       }
@@ -925,11 +1015,18 @@ struct ManyCursor {
   // key tiles of slot sl in this piece
   __device__ int count(int sl) const {
     if (sl) return two() ? j1 - j0 : 0;
-    const int n0 = r.tiles_upto(tok(1));
+    const int n0 = r.tiles_upto(tok(1)) - (WIN ? gap.gap : 0);
     return n0 < j1 ? (n0 > j0 ? n0 - j0 : 0) : j1 - j0;
   }
-  // key tile j holds keys that the pair's first row does not see
-  __device__ bool partial(int j) const { return (j + 1) * TR - 1 > r.kv - r.n + tok(0); }
+  __device__ int tile(int j) const { return WIN ? gap.tile(j) : j; }
+  // key tile j holds keys that the pair's first row does not see, being behind it
+  __device__ bool behind(int j) const { return (tile(j) + 1) * TR - 1 > r.kv - r.n + tok(0); }
+  // or that another does not, being before its window
+  __device__ bool partial(int j) const { return behind(j) || (WIN && j >= low0 && j < low1); }
+  // one of key tiles [a, b) is such a tile
+  __device__ bool any_partial(int a, int b) const {
+    return behind(b - 1) || (WIN && (a > low0 ? a : low0) < (b < low1 ? b : low1));
+  }
 };
 
 // How an item cut by range boundaries is joined: its parts are those of CTAs
@@ -937,7 +1034,8 @@ struct ManyCursor {
 // many, and then the groups.
 struct ManySplit {
   int c0, pieces, gsize, groups;
-  __device__ ManySplit(const ManyCursor& cur, unsigned units, unsigned ctas) {
+  template <bool WIN>
+  __device__ ManySplit(const ManyCursor<WIN>& cur, unsigned units, unsigned ctas) {
     const Ranges ranges(units, ctas);
     const int item0 = cur.u - cur.j0;
     c0 = ranges.owner(item0 + cur.near);
@@ -1063,10 +1161,18 @@ __device__ __forceinline__ bool notes_free(const volatile unsigned* ended, uint3
 // Both passes (maximum, then P) read the scores 32 columns at a time in rolled
 // loops: unrolled over the row, the code outgrows the instruction cache and
 // runs slower with half the instructions.  What has a paired fp32 form
-// (.f32x2) uses it.  PART: only columns up to `vis` are seen.
-template <int D, bool PART>
-__device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t half, int lane, float sl2, int vis,
-                                             bool first, float& m, float& l) {
+// (.f32x2) uses it.  PART 1: only columns up to `vis` are seen; 2: of these only
+// the ones from `from` on, and those below `upto`.
+struct Seen {
+  int vis, from, upto;
+  // of columns [c, c + 32), a bit each
+  __device__ uint32_t bits(int c) const { return below(vis + 1 - c) & (~below(from - c) | below(upto - c)); }
+  __device__ static uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+};
+template <int D, int PART>
+__device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t half, int lane, float sl2,
+                                             const Seen& seen, bool first, float& m, float& l) {
+  const int vis = seen.vis;
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
   for (int cc = 0; cc < 4; ++cc) {
@@ -1074,10 +1180,12 @@ __device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t ha
     tmem_ld_32x32b_x32(s + (uint32_t)(cc * 32), v);
     tmem_ld_wait();
     const int left = vis - cc * 32;
+    const uint32_t in = PART == 2 ? seen.bits(cc * 32) : 0u;
+    const auto sees = [&](int e) { return PART == 2 ? (in >> e & 1u) != 0 : !PART || e <= left; };
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-      const float x = !PART || e <= left ? __uint_as_float(v[e]) : -INFINITY;
-      const float y = !PART || e + 1 <= left ? __uint_as_float(v[e + 1]) : -INFINITY;
+      const float x = sees(e) ? __uint_as_float(v[e]) : -INFINITY;
+      const float y = sees(e + 1) ? __uint_as_float(v[e + 1]) : -INFINITY;
       mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], x), y);
     }
   }
@@ -1108,12 +1216,14 @@ __device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t ha
     tmem_ld_32x32b_x32(s + (uint32_t)(cc * 32), v);
     tmem_ld_wait();
     const int left = vis - cc * 32;
+    const uint32_t in = PART == 2 ? seen.bits(cc * 32) : 0u;
+    const auto sees = [&](int e) { return PART == 2 ? (in >> e & 1u) != 0 : !PART || e <= left; };
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       float p0, p1, t0, t1;
       upk2(fma2(pk2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc, nb), p0, p1);
-      p0 = !PART || 2 * e <= left ? ex2_approx(p0) : 0.0f;
-      p1 = !PART || 2 * e + 1 <= left ? ex2_approx(p1) : 0.0f;
+      p0 = sees(2 * e) ? ex2_approx(p0) : 0.0f;
+      p1 = sees(2 * e + 1) ? ex2_approx(p1) : 0.0f;
       const f32x2 P = pk2(p0, p1);
       sum[e & 3] = add2(sum[e & 3], P);
       // hi: the upper halves as they are (truncated to bf16); lo: the exact rest, rounded
@@ -1135,7 +1245,40 @@ __device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t ha
   l += a0 + a1;
 }
 
-template <int D>
+// With a window, which rows see a key is an interval of its own for each key,
+// so the row of new token `token` looks for the values that the check has set to
+// zero itself: at the keys that it sees in the first `cnt` tiles of the piece, of
+// those tiles that were checked.  Returns the columns of [col, col + N) that have
+// one, a bit each.  Only where the check has found a value that is not finite.
+template <bool WIN, int N>
+__device__ __noinline__ uint32_t spoilt(const PagedAttn& A, const ManyCursor<WIN>& at, int cnt, int token, int col) {
+  const int lim = at.r.kv - at.r.n + token, low = window_begin(lim, at.r.window);
+  uint32_t bits = 0;
+  if (token >= at.r.n) return bits;
+#pragma unroll 1
+  for (int j = at.j0; j < at.j0 + cnt; ++j) {
+    if (!at.partial(j)) continue;
+#pragma unroll 1
+    for (int key = at.tile(j) * TR; key < (at.tile(j) + 1) * TR && key <= lim; ++key) {
+      if (key < low && key >= at.r.sinks) continue;
+      const int32_t page = ld_plain(A.table + (int64_t)at.b * A.width + (key >> A.page_log2));
+      if (page < 0 || page >= A.c.pages) continue;
+      const bf16* const v = static_cast<const bf16*>(A.c.v) + page * A.c.page_stride +
+                            (key & (A.c.page - 1)) * A.c.token_stride + at.h * A.c.head_stride + col;
+#pragma unroll
+      for (int q = 0; q < N / 8; ++q) {
+        const uint4 x = ld_plain(reinterpret_cast<const uint4*>(v) + q);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if ((w[e >> 1] >> (16 * (e & 1)) & 0x7f80u) == 0x7f80u) bits |= 1u << (8 * q + e);
+      }
+    }
+  }
+  return bits;
+}
+
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kManyThreads, 1)
     paged_attn_many_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                            const __grid_constant__ CUtensorMap mv, const PagedAttn A, float* __restrict__ parts,
@@ -1164,7 +1307,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 
   // ---- this CTA's range of the tile sequence (as in the kernel above)
   unsigned units = 0, ctas = 0;
-  ManyCursor cur;
+  ManyCursor<WIN> cur;
   {
     const bool one = A.requests <= kManyThreads;
     cur.u = -1;
@@ -1176,7 +1319,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         const int b = base + (int)threadIdx.x;
         long long tiles = 0;
         if (b < A.requests) {
-          const ManyRequest r = many_request(A, b);
+          const ManyRequest<WIN> r = many_request<WIN>(A, b);
           if (r.n > 0) tiles = r.total();
         }
         long long x = tiles;
@@ -1226,7 +1369,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   }
   __syncthreads();
   cur.b = sh.b0;
-  cur.r = many_request(A, cur.b);
+  cur.r = many_request<WIN>(A, cur.b);
   cur.pairs = cur.r.pairs();
   {
     const int per_head = sh.per_head;
@@ -1247,7 +1390,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       hi = lo + step < hi ? lo + step : hi;
     }
     cur.i = lo;
-    const int into = off - begins, n = cur.r.tiles(ManyCursor::fold(lo, cur.pairs));
+    const int into = off - begins, n = cur.r.tiles(ManyCursor<WIN>::fold(lo, cur.pairs));
     cur.j0 = into == 0 ? 0 : cur.snap(into, n);
     cur.u += cur.j0 - into;
     if (!(cur.j0 == n ? cur.following(A) : cur.enter())) return;
@@ -1305,10 +1448,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
         ++ic;
         for (int j = cur.j0; j < cur.j1 && ok; ++j) {
-          // a box outside the request or the pool starts past the last page: TMA fills it with zeros
-          const int key = j * TR + (pi << bl2);
+          // a box outside the request or the pool starts past the last page: TMA fills it with zeros; one whose keys
+          // no row of the pair sees, too (its page may have been given back)
+          const int key = cur.tile(j) * TR + (pi << bl2);
           int32_t page = (int32_t)A.c.pages;
-          if (mine && key < cur.r.kv) {
+          const bool unseen = WIN && key >= cur.r.sinks &&
+                              key + (1 << bl2) <= window_begin((int64_t)cur.r.kv - cur.r.n + cur.tok(0), cur.r.window);
+          if (mine && key < cur.r.kv && !unseen) {
             page = ld_plain(A.table + (int64_t)cur.b * A.width + (key >> A.page_log2));
             if (page < 0 || page >= A.c.pages) {
               raise_error(A.err, TP3D_EPAGES);
@@ -1403,13 +1549,17 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         const int nmax = __shfl_sync(0xffffffffu, cur.j1 - cur.j0, 0);
         // the first key tile of the piece that some row does not see whole
         const int seen = cur.r.kv - cur.r.n + cur.tok(0) + 1;
-        const int part0 = __shfl_sync(0xffffffffu, (seen > 0 ? seen / TR : 0) - cur.j0, 0);
+        const int seen_tiles = seen > 0 ? seen / TR : 0;
+        const int part0 = __shfl_sync(0xffffffffu, (WIN ? cur.gap.at(seen_tiles) : seen_tiles) - cur.j0, 0);
+        // those that some row's window leaves out in part
+        const int low0 = WIN ? __shfl_sync(0xffffffffu, cur.low0 - cur.j0, 0) : 0;
+        const int low1 = WIN ? __shfl_sync(0xffffffffu, cur.low1 - cur.j0, 0) : 0;
         // the value tile of key tile i of the piece, in and (where some row does not see it whole) checked
         auto values = [&](int i, uint32_t& vs) {
           vs = pos.slot;
           wait(r_full(vs), pos.phase);
           pos.next();
-          if (i < part0) return;
+          if (i < part0 && (!WIN || i < low0 || i >= low1)) return;
           wait(v_checked(vs), (vc >> vs) & 1);
           vc ^= 1u << vs;
         };
@@ -1483,11 +1633,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
           if (!noting) {
             noting = true;
-            for (int i = lane; i < NV * 4; i += 32) notes[i] = 0xffffffffu;
+            if (!WIN)
+              for (int i = lane; i < NV * 4; i += 32) notes[i] = 0xffffffffu;
             if (lane == 0) sh.noted[ic % kNotes][w] = 0;
             __syncwarp();
           }
-          const int k0 = j * TR, from = seen + 1 > k0 ? seen + 1 - k0 : 0;
+          // (with a window, any key of the tile: what is not finite becomes zero, and the rows look for it themselves)
+          const int k0 = cur.tile(j) * TR, from = !WIN && seen + 1 > k0 ? seen + 1 - k0 : 0;
           constexpr int RG = 32 / NV;  // rows per step of the warp
           const int v = w * NV + (lane & (NV - 1)), row = lane / NV;
           const uint32_t col = sR(slot) + (uint32_t)(v >> 3) * kChunk;
@@ -1517,7 +1669,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             for (int key = from + row; key < end; key += RG) {
               const unsigned rel = (unsigned)(k0 + key - seen < 0xfffe ? k0 + key - seen : 0xfffe);
               st_shared4(at(key), make_finite(ld_shared4(at(key)), [&](int i) {
-                           note_min(notes + (v - w * NV) * 4 + (i >> 1), i & 1, rel);
+                           if (!WIN) note_min(notes + (v - w * NV) * 4 + (i >> 1), i & 1, rel);
                          }));
             }
             if (lane == 0) sh.noted[ic % kNotes][w] = 1;
@@ -1543,12 +1695,22 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     uint32_t xc = 0;                  // questions about split pieces
     bool ok = true, more = true;
     // of the piece just finished (the last one's are used after the loop)
-    ManyCursor at = cur;
+    ManyCursor<WIN> at = cur;
     float m = -INFINITY, l = 0.0f;
     int cnt = 0;
     bool live = false, hurt = false, by_row = false, last = false;
     // columns whose notes say that this row sees a value that is not finite
     const auto spoil = [&](auto& ov, int col) {
+      if (WIN) {
+        constexpr int N = (int)(sizeof(ov) / 4);
+        const ManyCursor<WIN> piece = at;  // (a copy in memory for the call)
+        const uint32_t bits = spoilt<WIN, N>(A, piece, cnt, piece.tok(sl) + tok, col);
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (bits >> e & 1u) ov[e] = 0x7fffffffu;
+        return;
+      }
       const unsigned* const notes = sh.notes[ic % kNotes];
       const unsigned rel = (unsigned)(at.tok(sl) + tok - at.tok(0));  // the row's last key - the pair's first row's
 #pragma unroll
@@ -1593,12 +1755,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         ++sc;
         tc_fence_after();
         // columns of this tile that the row sees: [0, vis]
-        const int vis = lim - j * TR;
+        const int k0 = cur.tile(j) * TR;
+        const Seen seen{lim - k0, WIN ? window_begin(lim, A.window) - k0 : 0, WIN ? cur.r.sinks - k0 : 0};
         const uint32_t sa = tmem_row(tmem, quarter, s_col), oa = tmem_row(tmem, quarter, o_col);
-        if (__any_sync(0xffffffffu, vis < TR - 1))
-          many_softmax<D, true>(sa, oa, p_half(sl), lane, sl2, vis, j == cur.j0, m, l);
+        if (__any_sync(0xffffffffu, seen.vis < TR - 1 || (WIN && seen.from > 0 && seen.upto < TR)))
+          many_softmax<D, WIN ? 2 : 1>(sa, oa, p_half(sl), lane, sl2, seen, j == cur.j0, m, l);
         else
-          many_softmax<D, false>(sa, oa, p_half(sl), lane, sl2, vis, j == cur.j0, m, l);
+          many_softmax<D, 0>(sa, oa, p_half(sl), lane, sl2, seen, j == cur.j0, m, l);
         tc_fence_before();
         warp_arrive(p_full(sl), lane);
       }
@@ -1608,7 +1771,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         ++oc;
         tc_fence_after();
       }
-      hurt = cnt > 0 && cur.partial(cur.j0 + cnt - 1) && (sh.noted[ic % kNotes][0] | sh.noted[ic % kNotes][1]) != 0;
+      hurt = cnt > 0 && cur.any_partial(cur.j0, cur.j0 + cnt) && (sh.noted[ic % kNotes][0] | sh.noted[ic % kNotes][1]) != 0;
       at = cur;
       more = cur.next(A);
       if (at.j0 == 0 && at.j1 == at.nkv) {
@@ -1789,7 +1952,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     cur.nkv = sh.place[which][3];
     cur.u = sh.place[which][4];
     cur.j0 = 0;
-    cur.r = many_request(A, cur.b);
+    cur.r = many_request<WIN>(A, cur.b);
     const ManySplit split(cur, units, ctas);
     const int g = split.group();
     // the rows of the item that are any token's: slot 0's first live0, slot 1's first live1
@@ -1934,17 +2097,18 @@ tp3d_status row_map(CUtensorMap* m, const void* ptr, int rank, const int64_t* di
 // The kernels' shared-memory limits, set once per context (a context has one
 // device), and the register split checked: setmaxnreg.inc waits until the
 // block's launch registers cover it.
-template <int D>
+template <int D, bool WIN>
 tp3d_status ready(tp3d_ctx* ctx) {
-  const int bit = D == 128 ? 1 : 2;
+  const int bit = (D == 128 ? 1 : 2) << (WIN ? 4 : 0);
   if (ctx->paged_ready & bit) return TP3D_OK;
-  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D, 4, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)few_smem<4>(D)));
-  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_few_kernel<D, 8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)few_smem<8>(D)));
-  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem));
+  TP3D_CUDA_TRY(cudaFuncSetAttribute(paged_attn_many_kernel<D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kManySmem));
   cudaFuncAttributes fa;
-  TP3D_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_attn_many_kernel<D>));
+  TP3D_CUDA_TRY(cudaFuncGetAttributes(&fa, paged_attn_many_kernel<D, WIN>));
   if (fa.numRegs * kManyThreads < 128 * kManyRegsLow + 256 * kManyRegsHigh) return TP3D_EUNSUPPORTED;
   ctx->paged_ready |= bit;
   return TP3D_OK;
@@ -1953,14 +2117,14 @@ tp3d_status ready(tp3d_ctx* ctx) {
 // `after`: right after the other kernel of this call.  It then works beside
 // that one, on the SMs that one leaves: the two write different rows, parts
 // and counters, and it ends only when that one has ended.
-template <int D, int W>
+template <int D, int W, bool WIN>
 tp3d_status launch_few(tp3d_ctx* ctx, const PagedAttn& A, bool after, float* parts, cudaStream_t s) {
-  return launch_dependent(paged_attn_few_kernel<D, W>, (unsigned)(ctx->num_sms * FewShape<W>::kPerSm),
+  return launch_dependent(paged_attn_few_kernel<D, W, WIN>, (unsigned)(ctx->num_sms * FewShape<W>::kPerSm),
                           FewShape<W>::kThreads, few_smem<W>(D), s, A, !after, parts, ctx->d_paged + kManyCounters,
                           ctx->d_paged + kWaitedWord);
 }
 
-template <int D>
+template <int D, bool WIN>
 tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, bool few, float* parts, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   const int64_t qd[3] = {D, (int64_t)A.group * A.c.kv_heads, A.tokens}, qs[2] = {A.q_head, A.q_token};
@@ -1971,17 +2135,17 @@ tp3d_status launch_many(tp3d_ctx* ctx, const PagedAttn& A, bool few, float* part
   const uint32_t cb[4] = {64, (uint32_t)(A.c.page < TR ? A.c.page : TR), 1, 1};
   TP3D_TRY(row_map(&mk, A.c.k, 4, cd, cs, cb));
   TP3D_TRY(row_map(&mv, A.c.v, 4, cd, cs, cb));
-  return launch_dependent(paged_attn_many_kernel<D>, (unsigned)ctx->num_sms, kManyThreads, kManySmem, s, mq, mk, mv, A,
-                          parts, ctx->d_paged, few ? ctx->d_paged + kWaitedWord : nullptr);
+  return launch_dependent(paged_attn_many_kernel<D, WIN>, (unsigned)ctx->num_sms, kManyThreads, kManySmem, s, mq, mk,
+                          mv, A, parts, ctx->d_paged, few ? ctx->d_paged + kWaitedWord : nullptr);
 }
 
-template <int D>
+template <int D, bool WIN>
 tp3d_status launch(tp3d_ctx* ctx, const PagedAttn& A, bool few, bool many, bool wide, void* workspace, cudaStream_t s) {
   float* const few_parts = static_cast<float*>(workspace);
-  TP3D_TRY(ready<D>(ctx));
-  if (many) TP3D_TRY(launch_many<D>(ctx, A, few, few_parts + few_workspace_floats(ctx, D), s));
+  TP3D_TRY((ready<D, WIN>(ctx)));
+  if (many) TP3D_TRY((launch_many<D, WIN>(ctx, A, few, few_parts + few_workspace_floats(ctx, D), s)));
   if (!few) return TP3D_OK;
-  return wide ? launch_few<D, 8>(ctx, A, many, few_parts, s) : launch_few<D, 4>(ctx, A, many, few_parts, s);
+  return wide ? launch_few<D, 8, WIN>(ctx, A, many, few_parts, s) : launch_few<D, 4, WIN>(ctx, A, many, few_parts, s);
 }
 
 }  // namespace
@@ -2002,8 +2166,11 @@ tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* wo
   // (all its rows are computed there all the same, and a launch is saved).
   const bool few = !many || A.requests > 1;
   A.few_rows = few ? few_rows : 0;
-  return A.c.head_dim == 128 ? launch<128>(ctx, A, few, many, wide, workspace, s)
-                             : launch<64>(ctx, A, few, many, wide, workspace, s);
+  if (A.window > 0)
+    return A.c.head_dim == 128 ? launch<128, true>(ctx, A, few, many, wide, workspace, s)
+                               : launch<64, true>(ctx, A, few, many, wide, workspace, s);
+  return A.c.head_dim == 128 ? launch<128, false>(ctx, A, few, many, wide, workspace, s)
+                             : launch<64, false>(ctx, A, few, many, wide, workspace, s);
 }
 
 }  // namespace tp3d
