@@ -36,8 +36,8 @@ struct tp3d_ctx {
   // rope.cu and paged_pages.cu (zero between calls)
   unsigned* d_paged;
   // paged kernels that are set up (bits: attention with heads of 128, of 64, plans of many requests, forks and the
-  // like; from bit 4 the attentions with a window)
-  int paged_ready;
+  // like; from bit 4 the attentions with a window; from bit 8 the rotations' backward passes)
+  unsigned paged_ready;
   // CUDA graphs of whole layer calls keyed by their arguments (graph.cu), the
   // stream they run on, and the events that order it with the caller's stream
   void* graphs;

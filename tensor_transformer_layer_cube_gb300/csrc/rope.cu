@@ -9,12 +9,18 @@
 // can use.
 //
 // Every element is read once and written once, so HBM bounds many tokens and
-// latency few.  A row's columns lie on LANES neighbouring lanes, eight each (16
-// bytes of bf16), so the sums of a row and the partner columns of its pairs
-// are shuffles within a warp.  A warp takes one token and goes over its heads,
-// 32 / LANES at a time: the angles of its columns are computed once for all of
-// them (eight sines and cosines a lane, some 200 instructions, against 100 for each
-// head).  Where tokens are few, several warps share a token's heads.
+// latency few; instructions come close behind, so a pass is made of few.  A row
+// lies on LANES neighbouring lanes, each with two groups of four columns,
+// rotary_dim / 2 apart, so that both columns of a pair are one lane's and
+// neighbouring lanes' groups are neighbours.  A warp's pass takes the same head
+// of 32 / LANES tokens, and its passes go over their query heads, then their key
+// heads (then their values).  With x' the other column of each column's pair, a
+// row of y is
+//   y = s (A x + B x'),  A = m w cos,  B = -+ m w' sin,
+// with the angles computed once for a token and A and B for its heads of one
+// kind.  Passes are loaded several ahead into a ring in shared memory that each
+// lane fills and reads by itself (4 KiB a warp, no barrier), over the ends of
+// tokens.  All passes in a row are cut into equal ranges, one for each warp.
 #include <math.h>
 
 #include "paged.cuh"
@@ -23,9 +29,8 @@ namespace tp3d {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeFlight = 4;  // rows that a lane has in flight
-constexpr int kBackThreads = 512;
+constexpr int kRopeThreads = 256, kBackThreads = 512;
+constexpr int kRingBytes = 4096;  // of a warp
 
 struct RowsIn {
   const void* p;
@@ -37,7 +42,8 @@ struct RowsOut {
 };
 
 struct RopeArgs {
-  int32_t tokens, heads, kv_heads, dim, rot, norm, split;  // split: warps that share a token's heads
+  int32_t tokens, heads, kv_heads, dim, rot, norm;
+  int32_t range;  // passes of a warp
   float eps, magnitude;
   const uint64_t* turns;
   const void *qw, *kw;
@@ -56,96 +62,148 @@ struct RopeArgs {
   unsigned* arrivals;
 };
 
-// eight columns of a row as they lie in memory
+__device__ __forceinline__ void cp_async(uint32_t dst, const __nv_bfloat16* src) {  // four columns
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async(uint32_t dst, const float* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A lane's eight columns of a row, as pairs of fp32: two groups of four.
 template <class T>
-struct Raw;
+struct Row;
 template <>
-struct Raw<__nv_bfloat16> {
-  uint4 a;
-  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = ld_plain(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Row<__nv_bfloat16> {
+  static constexpr uint32_t kBytes = 16, kGroup = 8;  // of a lane in the ring, and from its first group to its second
+  uint4 w;
+  __device__ __forceinline__ void read(uint32_t at) { w = ld_shared4(at); }
+  __device__ __forceinline__ void get(f32x2 (&x)[4]) const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = pk2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
   }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-    uint32_t w[4];
+  __device__ __forceinline__ void set(const f32x2 (&x)[4]) {
+    uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      float a, b;
+      upk2(x[i], a, b);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      v[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    a = make_uint4(w[0], w[1], w[2], w[3]);
+    w = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  __device__ __forceinline__ void write(__nv_bfloat16* p, int second) const {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w.x, w.y);
+    *reinterpret_cast<uint2*>(p + second) = make_uint2(w.z, w.w);
   }
 };
 template <>
-struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-  __device__ __forceinline__ void load(const float* p) {
-    a = ld_plain(reinterpret_cast<const float4*>(p));
-    b = ld_plain(reinterpret_cast<const float4*>(p) + 1);
+struct Row<float> {
+  static constexpr uint32_t kBytes = 32, kGroup = 512;  // the second groups of all lanes behind the first ones
+  uint4 w, v;
+  __device__ __forceinline__ void read(uint32_t at) {
+    w = ld_shared4(at);
+    v = ld_shared4(at + kGroup);
   }
-  __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
+  __device__ __forceinline__ void get(f32x2 (&x)[4]) const {
+    x[0] = pk2(__uint_as_float(w.x), __uint_as_float(w.y));
+    x[1] = pk2(__uint_as_float(w.z), __uint_as_float(w.w));
+    x[2] = pk2(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[3] = pk2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  __device__ __forceinline__ void set(const f32x2 (&x)[4]) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) upk2(x[i], f[2 * i], f[2 * i + 1]);
+    w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    v = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
   }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-    a = make_float4(x[0], x[1], x[2], x[3]);
-    b = make_float4(x[4], x[5], x[6], x[7]);
+  __device__ __forceinline__ void write(float* p, int second) const {
+    *reinterpret_cast<uint4*>(p) = w;
+    *reinterpret_cast<uint4*>(p + second) = v;
   }
 };
 
-// A lane's eight columns from column c: their cosines and sines at one position.
-// Halves: columns c + e turn against those rotary_dim / 2 away, eight angles;
-// interleaved: pairs inside the eight, four.
+// Sine and cosine of an angle in units of 2^-32 turns: an integer number of
+// quarter turns off, what is left (an eighth of a turn at most) goes through the
+// Taylor series, whose next terms are below 2^-28 and 2^-30; to about 2 2^-24.
+__device__ __forceinline__ void sincos_of(uint32_t turn, float& s, float& c) {
+  const uint32_t q = (turn + 0x20000000u) >> 30;
+  const float t = (float)(int32_t)(turn - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float x = t * t;
+  const float a = fmaf(t * x, fmaf(x, fmaf(x, fmaf(x, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), t);
+  const float b = fmaf(
+      x, fmaf(x, fmaf(x, fmaf(x, fmaf(x, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  const float y = q & 1 ? b : a, z = q & 1 ? a : b;
+  s = __uint_as_float(__float_as_uint(y) ^ (q & 2) << 30);
+  c = __uint_as_float(__float_as_uint(z) ^ ((q + 1) & 2) << 30);
+}
+
+// A lane's columns [c, c + 4) and [c + second, + 4), and their rotation.
 template <bool INTER>
 struct Turn {
-  float cs[INTER ? 4 : 8], sn[INTER ? 4 : 8];
-  bool turns;   // these columns are turned
-  int partner;  // the lane of the other columns (halves)
-  __device__ __forceinline__ void place(int rot, int c, int lane) {
-    turns = c < rot;
-    partner = !turns ? lane : c < rot / 2 ? lane + rot / 16 : lane - rot / 16;
-  }
-  // sign -1: the transposed rotation
-  __device__ __forceinline__ void at(const RopeArgs& A, int pos, int c, float sign) {
-    if (!turns) return;
-    const int half = A.rot / 2, j0 = INTER ? c / 2 : c < half ? c : c - half;
-    const float up = INTER || c >= half ? sign : -sign;  // the first column of a pair gets minus the sine
+  int c, second;
+  bool in, turned;     // these are columns of the row; they are turned
+  float cs[4], sn[4];  // cosines and sines of the lane's four pairs, times the magnitude
+  __device__ __forceinline__ void place(const RopeArgs& A, int l) {
+    turned = 8 * l < A.rot;
+    in = 8 * l < A.dim;
+    c = turned ? 4 * l : in ? A.rot / 2 + 4 * l : 0;
+    second = turned ? A.rot / 2 : in ? (A.dim - A.rot) / 2 : 4;
 #pragma unroll
-    for (int e = 0; e < (INTER ? 4 : 8); ++e) {
-      const uint64_t turn = (uint64_t)(int64_t)pos * ld_plain(A.turns + j0 + e);
-      // half turns in [-1, 1]
-      sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 0x1p-31f, &sn[e], &cs[e]);
+    for (int e = 0; e < 4; ++e) cs[e] = 1.0f, sn[e] = 0.0f;
+  }
+  __device__ __forceinline__ void at(const RopeArgs& A, int pos) {
+    if (!turned) return;
+    const uint64_t* const turns = A.turns + (INTER ? c / 2 : c);
+    const int hop = INTER ? A.rot / 4 - 2 : 0;  // from the first group's pairs to the second's
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t turn = (uint64_t)(int64_t)pos * ld_plain(turns + (e < 2 ? e : e + hop));
+      sincos_of((uint32_t)(turn >> 32), sn[e], cs[e]);
       cs[e] *= A.magnitude;
-      sn[e] *= up * A.magnitude;
+      sn[e] *= A.magnitude;
     }
   }
-  // x turned; all lanes of the warp take part
-  __device__ __forceinline__ void apply(float (&x)[8]) const {
-    if (INTER) {
-      if (!turns) return;
+  // The factors of x and x' for weights w; back: of the transposed rotation (and no weights).
+  __device__ __forceinline__ void factors(const float (&w)[8], bool back, f32x2 (&a)[4], f32x2 (&b)[4]) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = fmaf(a, cs[i & 3], -(b * sn[i & 3]));
-        x[2 * i + 1] = fmaf(b, cs[i & 3], a * sn[i & 3]);
+    for (int i = 0; i < 4; ++i) {
+      const int e = 2 * i;
+      if (INTER) {
+        const float s = back ? -sn[i] : sn[i];
+        a[i] = pk2(cs[i] * w[e], cs[i] * w[e + 1]);
+        b[i] = pk2(-s * w[e + 1], s * w[e]);
+      } else {
+        const int o = e ^ 4, p = e & 3;  // the pair's other columns; its place among the four
+        const bool minus = (e < 4) != back;
+        a[i] = pk2(cs[p] * w[e], cs[p + 1] * w[e + 1]);
+        b[i] = pk2((minus ? -sn[p] : sn[p]) * w[o], (minus ? -sn[p + 1] : sn[p + 1]) * w[o + 1]);
       }
+      if (!turned) b[i] = 0;
+    }
+  }
+  // x = a x + b x'.  `all`: every lane's columns are turned; else those that are not only take their weight, since
+  // 0 times an x' that is not finite is none.
+  __device__ __forceinline__ void apply(f32x2 (&x)[4], const f32x2 (&a)[4], const f32x2 (&b)[4], bool all) const {
+    f32x2 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (INTER) {
+        float lo, hi;
+        upk2(x[i], lo, hi);
+        o[i] = pk2(hi, lo);
+      } else {
+        o[i] = x[i ^ 2];
+      }
+    }
+    if (all) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = fma2(x[i], a[i], mul2(o[i], b[i]));
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_sync(0xffffffffu, x[e], partner);
-        if (turns) x[e] = fmaf(x[e], cs[e], o * sn[e]);
-      }
+      for (int i = 0; i < 4; ++i) x[i] = turned ? fma2(x[i], a[i], mul2(o[i], b[i])) : mul2(x[i], a[i]);
     }
   }
 };
@@ -157,95 +215,235 @@ __device__ __forceinline__ float row_sum(float v) {
   for (int o = 1; o < LANES; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-
-template <class T>
-__device__ __forceinline__ void load_weight(float (&w)[8], const void* p, int c, bool in) {
+// The sums over the LANES lanes of a row, of two values: from the first step on
+// even lanes go on with a, odd ones with b.
+template <int LANES>
+__device__ __forceinline__ void row_sums(float& a, float& b, int lane) {
+  const bool odd = lane & 1;
+  float v = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-  if (!p || !in) return;
-  Raw<T> r;
-  r.load(static_cast<const T*>(p) + c);
-  r.get(w);
+  for (int o = 2; o < LANES; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const float u = __shfl_xor_sync(0xffffffffu, v, 1);
+  a = odd ? u : v;
+  b = odd ? v : u;
+}
+__device__ __forceinline__ float sum_of(f32x2 v) {
+  float a, b;
+  upk2(v, a, b);
+  return a + b;
+}
+// 1 / sqrt(mean x^2 + eps) of a row
+template <int LANES>
+__device__ __forceinline__ float inverse_rms(float eps, const f32x2 (&x)[4], float inv_dim) {
+  f32x2 q = mul2(x[0], x[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) q = fma2(x[i], x[i], q);
+  return rsqrtf(fmaf(row_sum<LANES>(sum_of(q)), inv_dim, eps));
 }
 
-template <class T, int LANES, bool INTER, bool STORE>
-__global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_constant__ RopeArgs A) {
-  constexpr int kHeads = 32 / LANES;  // of a pass
-  const int lane = threadIdx.x & 31, sub = lane / LANES, c = (lane & (LANES - 1)) * 8;
-  const bool col = c < A.dim;
-  Turn<INTER> turn;
-  turn.place(A.rot, col ? c : A.dim, lane);
-  grid_begin();
-  float qw[8], kw[8];
-  if (A.norm) {
-    load_weight<T>(qw, A.qw, c, col);
-    load_weight<T>(kw, A.kw, c, col);
+// the weights in shared memory: query heads', then key heads' (kWeights columns each, those past the heads 1)
+constexpr int kWeights = 256;
+template <class T>
+__device__ __forceinline__ void fill_weights(const RopeArgs& A, float* w) {
+  for (int i = threadIdx.x; i < 2 * kWeights; i += blockDim.x) {
+    const T* const p = static_cast<const T*>(i < kWeights ? A.qw : A.kw);
+    const int c = i & (kWeights - 1);
+    w[i] = p && c < A.dim ? (float)ld_plain(p + c) : 1.0f;
   }
-  const float inv_dim = 1.0f / (float)A.dim;
-  const int rows = A.heads + A.kv_heads * (STORE ? 2 : 1);
-  const int passes = (rows + kHeads - 1) / kHeads, mine = (passes + A.split - 1) / A.split;
-  const int tasks = A.tokens * A.split, warps = (int)(gridDim.x * (kRopeThreads / 32));
-  for (int task = (int)(blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5)); task < tasks; task += warps) {
-    const int t = A.split == 1 ? task : task / A.split;
-    const int p0 = (task - t * A.split) * mine, p1 = p0 + mine < passes ? p0 + mine : passes;
-    if (p0 >= p1) continue;
-    const T* const q = static_cast<const T*>(A.q.p) + t * A.q.token + c;
-    const T* const k = static_cast<const T*>(A.k.p) + t * A.k.token + c;
-    const T* const v = STORE ? static_cast<const T*>(A.v.p) + t * A.v.token + c : nullptr;
-    T* const qo = static_cast<T*>(A.qo.p) + t * A.qo.token + c;
-    T* const ko = STORE ? nullptr : static_cast<T*>(A.ko.p) + t * A.ko.token + c;
-    int64_t at = -1;  // of the token in the pools
-    bool ready = false;
-#pragma unroll 1
-    for (int p = p0; p < p1; p += kRopeFlight) {
-      Raw<T> x[kRopeFlight];
+  __syncthreads();
+}
+__device__ __forceinline__ void columns_of(const float* w, int c, int second, float (&x)[8]) {
+  const float4 v = *reinterpret_cast<const float4*>(w + c), u = *reinterpret_cast<const float4*>(w + c + second);
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w, x[4] = u.x, x[5] = u.y, x[6] = u.z, x[7] = u.w;
+}
+
+// What a warp goes over: `range` passes from its first on, pass p of the `all` of
+// each group of neighbouring tokens, group by group.  The first nq of a group are
+// query heads, the next nk key heads, the others values: one kind after the other.
+struct Walk {
+  int nq, nk, all;
+  int group, p, rest;  // rest: passes of the range from this one on
+  __device__ __forceinline__ void begin(const RopeArgs& A, int kinds, int tokens, int warp) {
+    nq = A.heads;
+    nk = A.kv_heads;
+    all = nq + (kinds - 1) * nk;
+    const int64_t groups = ((int64_t)A.tokens + tokens - 1) / tokens;
+    const int64_t first = (int64_t)warp * A.range, left = groups * all - first;
+    rest = left < A.range ? left < 0 ? 0 : (int)left : A.range;
+    group = (int)(first / all);
+    p = (int)(first - (int64_t)group * all);
+  }
+  __device__ __forceinline__ int kind() const { return p < nq ? 0 : p < nq + nk ? 1 : 2; }
+  // the head of pass p, and the passes of its kind from it on
+  __device__ __forceinline__ int head(int kind) const { return p - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk); }
+  __device__ __forceinline__ int left(int kind) const {
+    const int n = (kind == 0 ? nq : kind == 1 ? nq + nk : all) - p;
+    return n < rest ? n : rest;
+  }
+  // n passes on, all of one kind
+  __device__ __forceinline__ void skip(int n) {
+    rest -= n;
+    p += n;
+    if (p == all) {
+      p = 0;
+      ++group;
+    }
+  }
+};
+
+// What a warp loads, ahead of what it computes: a lane's rows of N arrays side by
+// side (dy and x backward), into the stages of its ring.
+template <class T, int N>
+struct Loader {
+  Walk w;
+  const T* src[N];
+  int64_t hop[N];  // from head to head
+  int left;        // passes until the next kind of rows
+  bool in;         // this lane has a column of a token
+  __device__ __forceinline__ void begin(const Walk& at) {
+    w = at;
+    left = 0;
+    in = false;
 #pragma unroll
-      for (int i = 0; i < kRopeFlight; ++i) {
-        const int u = (p + i) * kHeads + sub;
-        x[i].zero();
-        if (p + i >= p1 || u >= rows || !col) continue;
-        x[i].load(u < A.heads ? q + u * A.q.head
-                  : !STORE || u < A.heads + A.kv_heads ? k + (u - A.heads) * A.k.head
-                                                       : v + (u - A.heads - A.kv_heads) * A.v.head);
-      }
-      if (!ready) {  // behind the first rows' loads
-        ready = true;
-        turn.at(A, ld_plain(A.positions + t), c, 1.0f);
-        if (STORE) {
-          const int64_t slot = ld_plain(A.slots + t), page = slot >> A.page_log2;
-          if (slot >= 0 && page >= A.c.pages) raise_error(A.err, TP3D_EPAGES);
-          if (slot >= 0 && page < A.c.pages)
-            at = page * A.c.page_stride + (slot & ((1 << A.page_log2) - 1)) * A.c.token_stride + c;
+    for (int i = 0; i < N; ++i) {
+      src[i] = nullptr;
+      hop[i] = 0;
+    }
+  }
+  // The next pass, into the stage at `to`; nothing behind the last.  rows(kind, i): the i-th array's of a kind.
+  template <bool INTER, class F>
+  __device__ __forceinline__ void fetch(const RopeArgs& A, const Turn<INTER>& turn, int tokens, int sub, uint32_t to,
+                                        const F& rows) {
+    if (left == 0) {
+      in = false;
+      left = INT32_MAX;
+      if (w.rest > 0) {
+        const int kind = w.kind(), t = w.group * tokens + sub;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const RowsIn& r = rows(kind, i);
+          src[i] = static_cast<const T*>(r.p) + t * r.token + w.head(kind) * r.head + turn.c;
+          hop[i] = r.head;
         }
-      }
-#pragma unroll
-      for (int i = 0; i < kRopeFlight; ++i) {
-        if (p + i >= p1) break;
-        const int u = (p + i) * kHeads + sub;
-        const bool value = STORE && u >= A.heads + A.kv_heads;
-        // passes of value rows alone are copied as they are
-        if (!STORE || (p + i) * kHeads < A.heads + A.kv_heads) {
-          float y[8];
-          x[i].get(y);
-          if (A.norm) {
-            float s = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(y[e], y[e], s);
-            s = rsqrtf(fmaf(row_sum<LANES>(s), inv_dim, A.eps));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = y[e] * s * (u < A.heads ? qw[e] : kw[e]);
-          }
-          turn.apply(y);
-          if (!value) x[i].set(y);
-        }
-        if (u >= rows || !col) continue;
-        if (u < A.heads) x[i].store(qo + u * A.qo.head);
-        else if (!STORE) x[i].store(ko + (u - A.heads) * A.ko.head);
-        else if (at >= 0)
-          x[i].store(static_cast<T*>(value ? A.c.v : A.c.k) + at +
-                     (u - A.heads - (value ? A.kv_heads : 0)) * A.c.head_stride);
+        in = turn.in && t < A.tokens;
+        left = w.left(kind);
+        w.skip(left);
       }
     }
+    if (in)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        cp_async(to + i * 32 * Row<T>::kBytes, src[i]);
+        cp_async(to + i * 32 * Row<T>::kBytes + Row<T>::kGroup, src[i] + turn.second);
+      }
+    cp_commit();
+#pragma unroll
+    for (int i = 0; i < N; ++i) src[i] += hop[i];
+    --left;
+  }
+};
+
+template <class T, int LANES, bool INTER, bool NORM, bool STORE>
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_constant__ RopeArgs A) {
+  constexpr int kTokens = 32 / LANES;
+  constexpr uint32_t kStage = 32 * Row<T>::kBytes;  // of a warp
+  constexpr int kStages = kRingBytes / (int)kStage;
+  __shared__ __align__(16) uint8_t ring_all[kRopeThreads / 32 * kRingBytes];
+  __shared__ __align__(16) float weights[2 * kWeights];
+  const int lane = threadIdx.x & 31, sub = lane / LANES;
+  const uint32_t ring = smem_u32(ring_all) + (threadIdx.x >> 5) * kRingBytes + lane * 16u;
+  Turn<INTER> turn;
+  turn.place(A, lane & (LANES - 1));
+  if (!turn.in)  // columns past the row stay zeros
+    for (uint32_t i = 0; i < kRingBytes; i += 512) st_shared4(ring + i, make_uint4(0, 0, 0, 0));
+  const bool all_turned = A.rot == 8 * LANES;
+  grid_begin();
+  Walk at;
+  at.begin(A, STORE ? 3 : 2, kTokens, (int)(blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5)));
+  Loader<T, 1> ld;
+  ld.begin(at);
+  const auto fetch = [&](uint32_t to) {
+    ld.fetch(A, turn, kTokens, sub, to,
+             [&](int kind, int) -> const RowsIn& { return kind == 0 ? A.q : kind == 1 ? A.k : A.v; });
+  };
+#pragma unroll 1
+  for (int s = 0; s < kStages; ++s) fetch(ring + s * kStage);
+  fill_weights<T>(A, weights);
+  const float inv_dim = 1.0f / (float)A.dim;
+  int pos = 0, t = 0;  // of the next group's token, until it is begun
+  int64_t slot = -1;
+  const auto look = [&](int group) {
+    t = group * kTokens + sub;
+    if (t >= A.tokens) return;
+    pos = ld_plain(A.positions + t);
+    if (STORE) slot = ld_plain(A.slots + t);
+  };
+  look(at.group);
+  int token = 0;
+  int64_t pool = -1;  // where the token's rows lie in the pools
+  int begun = -1;     // the group whose angles are here
+  uint32_t stage = 0;
+#pragma unroll 1
+  while (at.rest > 0) {
+    if (begun != at.group) {
+      begun = at.group;
+      token = t;
+      turn.at(A, pos);
+      if (STORE) {
+        const int64_t page = slot >> A.page_log2;
+        const bool live = token < A.tokens && slot >= 0;
+        if (live && page >= A.c.pages) raise_error(A.err, TP3D_EPAGES);
+        pool = live && page < A.c.pages
+                   ? page * A.c.page_stride + (slot & ((1 << A.page_log2) - 1)) * A.c.token_stride
+                   : -1;
+      }
+      if (at.rest > at.all - at.p) look(at.group + 1);
+    }
+    // the passes of one kind
+    const int kind = at.kind(), n = at.left(kind);
+    bool out = turn.in && token < A.tokens;
+    T* dst;
+    int64_t hop;
+    if (STORE && kind > 0) {
+      dst = static_cast<T*>(kind == 1 ? A.c.k : A.c.v) + pool + at.head(kind) * A.c.head_stride + turn.c;
+      hop = A.c.head_stride;
+      out = out && pool >= 0;
+    } else {
+      const RowsOut& o = kind == 0 ? A.qo : A.ko;
+      dst = static_cast<T*>(o.p) + token * o.token + at.head(kind) * o.head + turn.c;
+      hop = o.head;
+    }
+    f32x2 a[4], b[4];
+    {
+      float w[8];
+      columns_of(weights + (kind == 0 ? 0 : kWeights), turn.c, turn.second, w);
+      turn.factors(w, false, a, b);
+    }
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      cp_wait<kStages - 1>();
+      Row<T> x;
+      x.read(ring + stage);
+      if (!STORE || kind < 2) {
+        f32x2 y[4];
+        x.get(y);
+        if (NORM) {
+          // (columns that are not turned: an x' that is not finite makes the whole row so)
+          const f32x2 s = splat2(inverse_rms<LANES>(A.eps, y, inv_dim));
+          turn.apply(y, a, b, true);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], s);
+        } else {
+          turn.apply(y, a, b, all_turned);
+        }
+        x.set(y);
+      }
+      if (out) x.write(dst, turn.second);
+      dst += hop;
+      fetch(ring + stage);
+      stage = (stage + kStage) & (kRingBytes - 1);
+    }
+    at.skip(n);
   }
 }
 
@@ -253,103 +451,132 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
 // weights' gradients, the sums of g x s, kept in registers over a warp's tokens,
 // joined warp by warp in shared memory and CTA by CTA in the workspace, in a
 // fixed order; the last CTA to arrive adds the CTAs' parts.
-template <class T, int LANES, bool INTER>
+template <class T, int LANES, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kBackThreads, 1) rope_back_kernel(const __grid_constant__ RopeArgs A) {
-  constexpr int kHeads = 32 / LANES, kWarps = kBackThreads / 32;
-  extern __shared__ float sums[];  // [warp][q or k][dim]
+  constexpr int kTokens = 32 / LANES, kWarps = kBackThreads / 32;
+  constexpr uint32_t kHalf = 32 * Row<T>::kBytes, kStage = (NORM ? 2 : 1) * kHalf;  // dy, then x
+  constexpr int kStages = kRingBytes / (int)kStage;
+  extern __shared__ __align__(16) uint8_t back_smem[];
+  float* const weights = reinterpret_cast<float*>(back_smem);
+  uint8_t* const ring_all = back_smem + 2 * kWeights * sizeof(float);
+  float* const sums = reinterpret_cast<float*>(ring_all);  // [warp][q or k][dim], when the ring is done with
   __shared__ int last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LANES, c = (lane & (LANES - 1)) * 8;
-  const bool col = c < A.dim;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LANES;
+  const uint32_t ring = smem_u32(ring_all) + warp * kRingBytes + lane * 16u;
   Turn<INTER> turn;
-  turn.place(A.rot, col ? c : A.dim, lane);
+  turn.place(A, lane & (LANES - 1));
+  if (!turn.in)
+    for (uint32_t i = 0; i < kRingBytes; i += 512) st_shared4(ring + i, make_uint4(0, 0, 0, 0));
+  const bool all_turned = A.rot == 8 * LANES;
   grid_begin();
-  float qw[8], kw[8], sq[8], sk[8];
-  if (A.norm) {
-    load_weight<T>(qw, A.qw, c, col);
-    load_weight<T>(kw, A.kw, c, col);
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) sq[e] = sk[e] = 0.0f;
-  const float inv_dim = 1.0f / (float)A.dim;
-  const int rows = A.heads + A.kv_heads;
-  const int passes = (rows + kHeads - 1) / kHeads, mine = (passes + A.split - 1) / A.split;
-  const int tasks = A.tokens * A.split, warps = (int)gridDim.x * kWarps;
-  // consecutive tasks to different CTAs: few tasks fill the SMs evenly
-  for (int task = warp * (int)gridDim.x + (int)blockIdx.x; task < tasks; task += warps) {
-    const int t = A.split == 1 ? task : task / A.split;
-    const int p0 = (task - t * A.split) * mine, p1 = p0 + mine < passes ? p0 + mine : passes;
-    if (p0 >= p1) continue;
-    const T* const q = static_cast<const T*>(A.q.p) + t * A.q.token + c;
-    const T* const k = static_cast<const T*>(A.k.p) + t * A.k.token + c;
-    const T* const dq = static_cast<const T*>(A.dq.p) + t * A.dq.token + c;
-    const T* const dk = static_cast<const T*>(A.dk.p) + t * A.dk.token + c;
-    T* const qo = static_cast<T*>(A.qo.p) + t * A.qo.token + c;
-    T* const ko = static_cast<T*>(A.ko.p) + t * A.ko.token + c;
-    bool ready = false;
-    constexpr int kFlight = kRopeFlight / 2;  // of x and of dy each
+  Walk at;  // neighbouring ranges to different CTAs: few fill the SMs evenly
+  at.begin(A, 2, kTokens, warp * (int)gridDim.x + (int)blockIdx.x);
+  Loader<T, NORM ? 2 : 1> ld;
+  ld.begin(at);
+  const auto fetch = [&](uint32_t to) {
+    ld.fetch(A, turn, kTokens, sub, to, [&](int kind, int i) -> const RowsIn& {
+      return i ? (kind == 0 ? A.q : A.k) : (kind == 0 ? A.dq : A.dk);
+    });
+  };
 #pragma unroll 1
-    for (int p = p0; p < p1; p += kFlight) {
-      Raw<T> x[kFlight], dy[kFlight];
+  for (int s = 0; s < kStages; ++s) fetch(ring + s * kStage);
+  fill_weights<T>(A, weights);
+  const float inv_dim = 1.0f / (float)A.dim;
+  f32x2 sq[4], sk[4], c[4], d[4];
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
-        const int u = (p + i) * kHeads + sub;
-        x[i].zero();
-        dy[i].zero();
-        if (p + i >= p1 || u >= rows || !col) continue;
-        dy[i].load(u < A.heads ? dq + u * A.dq.head : dk + (u - A.heads) * A.dk.head);
-        if (A.norm) x[i].load(u < A.heads ? q + u * A.q.head : k + (u - A.heads) * A.k.head);
-      }
-      if (!ready) {
-        ready = true;
-        turn.at(A, ld_plain(A.positions + t), c, -1.0f);
-      }
+  for (int i = 0; i < 4; ++i) sq[i] = sk[i] = 0;
+  int pos = 0, t = 0;
+  const auto look = [&](int group) {
+    t = group * kTokens + sub;
+    if (t < A.tokens) pos = ld_plain(A.positions + t);
+  };
+  look(at.group);
+  int token = 0, begun = -1;
+  uint32_t stage = 0;
+#pragma unroll 1
+  while (at.rest > 0) {
+    if (begun != at.group) {
+      begun = at.group;
+      token = t;
+      turn.at(A, pos);
+      const float ones[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+      turn.factors(ones, true, c, d);
+      if (at.rest > at.all - at.p) look(at.group + 1);
+    }
+    const int kind = at.kind(), n = at.left(kind);
+    const bool live = token < A.tokens;  // (what lies in the stage of a token past the last is no row)
+    const RowsOut& o = kind == 0 ? A.qo : A.ko;
+    T* dst = static_cast<T*>(o.p) + token * o.token + at.head(kind) * o.head + turn.c;
+    f32x2 w[4], sum[4];
+    {
+      float v[8];
+      columns_of(weights + (kind == 0 ? 0 : kWeights), turn.c, turn.second, v);
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
-        if (p + i >= p1) break;
-        const int u = (p + i) * kHeads + sub;
-        float g[8];
-        dy[i].get(g);
-        turn.apply(g);
-        if (A.norm) {
-          float y[8], s = 0.0f, dot = 0.0f;
-          x[i].get(y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(y[e], y[e], s);
-          s = rsqrtf(fmaf(row_sum<LANES>(s), inv_dim, A.eps));
-          const bool is_q = u < A.heads, is_k = !is_q && u < rows;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[e] *= s;
-            const float dw = g[e] * y[e];
-            sq[e] += is_q ? dw : 0.0f;
-            sk[e] += is_k ? dw : 0.0f;
-            const float w = is_q ? qw[e] : kw[e];
-            dot = fmaf(dw, w, dot);
-            g[e] *= w;
-          }
-          dot = row_sum<LANES>(dot) * inv_dim;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = s * fmaf(-y[e], dot, g[e]);
-        }
-        dy[i].set(g);
-        if (u >= rows || !col) continue;
-        if (u < A.heads) dy[i].store(qo + u * A.qo.head);
-        else dy[i].store(ko + (u - A.heads) * A.ko.head);
+      for (int i = 0; i < 4; ++i) {
+        w[i] = pk2(v[2 * i], v[2 * i + 1]);
+        sum[i] = 0;
       }
     }
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      cp_wait<kStages - 1>();
+      Row<T> x;
+      f32x2 g[4];
+      x.read(ring + stage);
+      x.get(g);
+      turn.apply(g, c, d, all_turned);
+      if (NORM) {
+        f32x2 y[4];
+        x.read(ring + stage + kHalf);
+        x.get(y);
+        // sum x^2 and sum w g x over the row together
+        f32x2 q = mul2(y[0], y[0]), dot = 0, wg[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (e) q = fma2(y[e], y[e], q);
+          wg[e] = mul2(g[e], w[e]);
+          dot = fma2(wg[e], y[e], dot);
+        }
+        float xx = sum_of(q), gx = sum_of(dot);
+        row_sums<LANES>(xx, gx, lane);
+        const float s = rsqrtf(fmaf(xx, inv_dim, A.eps));
+        const f32x2 s2 = splat2(s), minus = splat2(-s * (s * (s * gx)) * inv_dim);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum[e] = fma2(mul2(g[e], s2), y[e], sum[e]);
+          g[e] = fma2(y[e], minus, mul2(wg[e], s2));
+        }
+      }
+      x.set(g);
+      if (turn.in && live) x.write(dst, turn.second);
+      dst += o.head;
+      fetch(ring + stage);
+      stage = (stage + kStage) & (kRingBytes - 1);
+    }
+    if (live) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (kind == 0) sq[e] = add2(sq[e], sum[e]);
+        else sk[e] = add2(sk[e], sum[e]);
+      }
+    }
+    at.skip(n);
   }
   if (!A.parts) return;
+  cp_wait<0>();
+  __syncthreads();  // the ring is the sums' now
   const int width = 2 * A.dim;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int i = 0; i < 4; ++i) {
+    float v[4];
+    upk2(sq[i], v[0], v[1]);
+    upk2(sk[i], v[2], v[3]);
+    const int col = turn.c + (i < 2 ? 0 : turn.second) + 2 * (i & 1);
 #pragma unroll
-    for (int o = LANES; o < 32; o <<= 1) {
-      sq[e] += __shfl_xor_sync(0xffffffffu, sq[e], o);
-      sk[e] += __shfl_xor_sync(0xffffffffu, sk[e], o);
-    }
-    if (sub == 0 && col) {
-      sums[warp * width + c + e] = sq[e];
-      sums[warp * width + A.dim + c + e] = sk[e];
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int o = LANES; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+      if (sub == 0 && turn.in) sums[warp * width + (e >> 1) * A.dim + col + (e & 1)] = v[e];
     }
   }
   __syncthreads();
@@ -359,23 +586,27 @@ __global__ void __launch_bounds__(kBackThreads, 1) rope_back_kernel(const __grid
     for (int w = 0; w < kWarps; ++w) s += sums[w * width + i];
     __stcg(A.parts + (size_t)blockIdx.x * width + i, s);
   }
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicInc(A.arrivals, gridDim.x - 1) == gridDim.x - 1;
+  if (threadIdx.x == 0) last = arrive_last(A.arrivals, gridDim.x);
   __syncthreads();
   if (!last) return;
-  __threadfence();
   // four columns to a thread; group g of `groups` adds every groups-th part, then the groups are added
-  const int quads = width / 4, fit = kBackThreads / quads, groups = fit < kWarps ? fit : kWarps;  // (the size of `sums`)
-  const int g = (int)threadIdx.x / quads, at = (int)threadIdx.x - g * quads;
-  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int quads = width / 4, fit = kBackThreads / quads, groups = fit < kWarps ? fit : kWarps;
+  const int g = (int)threadIdx.x / quads, q = (int)threadIdx.x - g * quads;
   if (g < groups) {
-#pragma unroll 8
-    for (int b = g; b < (int)gridDim.x; b += groups) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(A.parts + (size_t)b * width) + at);
-      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    constexpr int kFlight = 20;  // (all there are with heads of 128)
+    for (int b0 = g; b0 < (int)gridDim.x; b0 += kFlight * groups) {
+      float4 x[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i)
+        if (b0 + i * groups < (int)gridDim.x)
+          x[i] = __ldcg(reinterpret_cast<const float4*>(A.parts + (size_t)(b0 + i * groups) * width) + q);
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i)
+        if (b0 + i * groups < (int)gridDim.x) s.x += x[i].x, s.y += x[i].y, s.z += x[i].z, s.w += x[i].w;
     }
-    reinterpret_cast<float4*>(sums)[g * quads + at] = s;
+    reinterpret_cast<float4*>(sums)[g * quads + q] = s;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < width; i += kBackThreads) {
@@ -474,21 +705,22 @@ RowsOut out(const Rows& r) { return RowsOut{const_cast<void*>(r.p), r.token, r.h
 
 int lanes_of(int dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 
-// Warps for each token: one, unless the tokens leave SMs without `per_sm` warps; then as many as
-// there are passes over its heads.
-int split_of(const tp3d_ctx* ctx, int64_t tokens, int rows, int lanes, int per_sm) {
-  const int64_t passes = (rows + 32 / lanes - 1) / (32 / lanes), want = (int64_t)ctx->num_sms * per_sm;
-  const int64_t s = (want + tokens - 1) / tokens;
-  return (int)(s < 1 ? 1 : s < passes ? s : passes);
+// Cuts the passes (heads of groups of tokens) into equal ranges for `warps` warps; how many get one.
+int64_t cut(RopeArgs& A, int lanes, int heads, int64_t warps) {
+  const int64_t passes = ((int64_t)A.tokens + 32 / lanes - 1) / (32 / lanes) * heads;
+  const int64_t range = (passes + warps - 1) / warps;
+  A.range = (int32_t)range;
+  return (passes + range - 1) / range;
 }
 
 template <class T, int LANES, bool STORE>
 tp3d_status launch_rope_lanes(const tp3d_ctx* ctx, RopeArgs& A, int interleaved, cudaStream_t s) {
-  A.split = split_of(ctx, A.tokens, A.heads + A.kv_heads * (STORE ? 2 : 1), LANES, 16);
-  const int64_t ctas = ((int64_t)A.tokens * A.split + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  const unsigned grid = (unsigned)(ctas < ctx->num_sms * 2 ? ctas : ctx->num_sms * 2);
-  return interleaved ? launch_dependent(rope_kernel<T, LANES, true, STORE>, grid, kRopeThreads, 0, s, A)
-                     : launch_dependent(rope_kernel<T, LANES, false, STORE>, grid, kRopeThreads, 0, s, A);
+  const int per_cta = kRopeThreads / 32;
+  const int64_t used = cut(A, LANES, A.heads + A.kv_heads * (STORE ? 2 : 1), (int64_t)ctx->num_sms * 3 * per_cta);
+  const unsigned grid = (unsigned)((used + per_cta - 1) / per_cta);
+  const auto kernel = interleaved ? (A.norm ? rope_kernel<T, LANES, true, true, STORE> : rope_kernel<T, LANES, true, false, STORE>)
+                                  : (A.norm ? rope_kernel<T, LANES, false, true, STORE> : rope_kernel<T, LANES, false, false, STORE>);
+  return launch_dependent(kernel, grid, kRopeThreads, 0, s, A);
 }
 template <class T, bool STORE>
 tp3d_status launch_rope(const tp3d_ctx* ctx, RopeArgs& A, int interleaved, cudaStream_t s) {
@@ -498,17 +730,24 @@ tp3d_status launch_rope(const tp3d_ctx* ctx, RopeArgs& A, int interleaved, cudaS
   return launch_rope_lanes<T, STORE ? 16 : 32, STORE>(ctx, A, interleaved, s);
 }
 
+constexpr int kBackSmem = 2 * kWeights * (int)sizeof(float) + kBackThreads / 32 * kRingBytes;
+static_assert(kBackThreads / 32 * 2 * kWeights * 4 <= kBackThreads / 32 * kRingBytes, "the sums fit into the ring");
 template <class T, int LANES>
-tp3d_status launch_back_lanes(const tp3d_ctx* ctx, RopeArgs& A, int interleaved, cudaStream_t s) {
-  A.split = split_of(ctx, A.tokens, A.heads + A.kv_heads, LANES, kBackThreads / 32);
-  const int64_t tasks = (int64_t)A.tokens * A.split;
-  const unsigned grid = (unsigned)(tasks < ctx->num_sms ? tasks : ctx->num_sms);
-  const size_t smem = A.parts ? (size_t)(kBackThreads / 32) * 2 * A.dim * sizeof(float) : 0;  // 32 KiB at most
-  return interleaved ? launch_dependent(rope_back_kernel<T, LANES, true>, grid, kBackThreads, smem, s, A)
-                     : launch_dependent(rope_back_kernel<T, LANES, false>, grid, kBackThreads, smem, s, A);
+tp3d_status launch_back_lanes(tp3d_ctx* ctx, RopeArgs& A, int interleaved, cudaStream_t s) {
+  const int64_t used = cut(A, LANES, A.heads + A.kv_heads, (int64_t)ctx->num_sms * (kBackThreads / 32));
+  const unsigned grid = (unsigned)(used < ctx->num_sms ? used : ctx->num_sms);
+  const auto kernel = interleaved ? (A.norm ? rope_back_kernel<T, LANES, true, true> : rope_back_kernel<T, LANES, true, false>)
+                                  : (A.norm ? rope_back_kernel<T, LANES, false, true> : rope_back_kernel<T, LANES, false, false>);
+  const unsigned bit = 1u << (8 + (LANES == 8 ? 0 : LANES == 16 ? 1 : 2) + (sizeof(T) == 4 ? 3 : 0) + (interleaved ? 6 : 0) +
+                        (A.norm ? 12 : 0));
+  if (!(ctx->paged_ready & bit)) {
+    TP3D_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBackSmem));
+    ctx->paged_ready |= bit;
+  }
+  return launch_dependent(kernel, grid, kBackThreads, kBackSmem, s, A);
 }
 template <class T>
-tp3d_status launch_back(const tp3d_ctx* ctx, RopeArgs& A, int interleaved, cudaStream_t s) {
+tp3d_status launch_back(tp3d_ctx* ctx, RopeArgs& A, int interleaved, cudaStream_t s) {
   if (A.tokens == 0)
     return launch_dependent(rope_zero_kernel<T>, 1, 256, 0, s, static_cast<T*>(A.dqw), static_cast<T*>(A.dkw), A.dim);
   switch (lanes_of(A.dim)) {
@@ -518,10 +757,11 @@ tp3d_status launch_back(const tp3d_ctx* ctx, RopeArgs& A, int interleaved, cudaS
   }
 }
 
-// most tokens x warps of a token, and rows: in 32 bits
 tp3d_status check_counts(int64_t tokens, int heads, int kv_heads) {
   if (tokens < 0 || heads < 1 || kv_heads < 1) return TP3D_EINVAL;
   if (tokens > kPagedMaxTokens || heads > 65536 || kv_heads > 65536) return TP3D_EUNSUPPORTED;
+  // (a warp's passes, 1 / 2432 of all on a device of 152 SMs, are counted in 32 bits)
+  if (tokens * ((int64_t)heads + 2 * (int64_t)kv_heads) >> 40) return TP3D_EUNSUPPORTED;
   return TP3D_OK;
 }
 
