@@ -97,8 +97,7 @@ def compact(page, table, shares, free, count, kv_len):
             continue
         for col in range(-(-n // page)):
             e = int(table[r, col])
-            if e >= used:
-                fits &= e in moved
-                table[r, col] = moved.get(e, e)
+            fits &= e < pages and e not in gone
+            table[r, col] = moved.get(e, e)
     free[:count] = np.arange(pages - 1, used - 1, -1)
     return table, shares, free, page_map, copies, fits

@@ -59,7 +59,7 @@ constexpr unsigned long long kWaitLimitNs = 4000000000ull;
 constexpr int kPagedCounters = 4096;  // of the paged attention
 constexpr int kRopeCounter = kPagedCounters;  // arrivals in the sum of the weights' gradients (rope.cu)
 constexpr int kPageWords = kPagedCounters + 32;  // of paged_pages.cu: its flags and counts
-constexpr int kPagedWords = 2 * kPagedCounters;  // all of d_paged
+constexpr int kPagedWords = 24 * 1024;  // all of d_paged
 constexpr int kErrWords = 4;  // ints of the device error area (error code, pad, 64-bit limit)
 
 #define TP3D_CUDA_TRY(expr)                       \

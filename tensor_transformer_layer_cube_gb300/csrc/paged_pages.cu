@@ -21,10 +21,25 @@ namespace {
 
 constexpr int kMaxRows = 16384;
 constexpr int kChunks = 1024;
-constexpr int kWarps = kPagedThreads / 32;
-// in the context's words: counts by chunk (a compaction has two), arrivals, a flag
-constexpr int kCounts = kPageWords, kArrivals = kCounts + 2 * kChunks, kBad = kArrivals + 1;
-static_assert(kBad < kPagedWords, "the context's words");
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+// Counts by chunk, several of each, so that the CTAs' additions do not all meet in
+// a few lines of L2 (31000 pages given back, 304 chunks: 16.0 -> KK us).
+constexpr int kCopies = 8;
+// in the context's words: the counts (a compaction has two kinds), arrivals, whether the free list is bad (zero
+// between calls), and that again (each call writes it before it is read)
+constexpr int kCounts = kPageWords, kArrivals = kCounts + 2 * kCopies * kChunks, kBad = kArrivals + 1, kWasBad = kBad + 1;
+static_assert(kWasBad < kPagedWords, "the context's words");
+// the word to count a page of a chunk in
+__device__ __forceinline__ unsigned* count_word(unsigned* words, int kind, int64_t chunk) {
+  return words + kCounts + (kind * kCopies + (blockIdx.x & (kCopies - 1))) * kChunks + chunk;
+}
+__device__ __forceinline__ long long count_of(const unsigned* words, int kind, int chunk) {
+  unsigned n = 0;
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) n += ld_plain(words + kCounts + (kind * kCopies + i) * kChunks + chunk);
+  return n;
+}
 
 struct Pool {
   int page_log2, rows, chunk_log2;
@@ -62,7 +77,7 @@ template <class F>
 __device__ __forceinline__ long long sum_rows(int n, int32_t* sums, const F& entries) {
   __shared__ long long warp_sum[kWarps];
   long long carry = 0;
-  for (int base = 0; base < n; base += kPagedThreads) {
+  for (int base = 0; base < n; base += kThreads) {
     const int i = base + (int)threadIdx.x;
     long long total;
     const long long at = carry + block_scan(i < n ? entries(i) : 0, warp_sum, total);
@@ -87,47 +102,55 @@ struct ForkArgs {
 
 // Every CTA looks all forks over first, so all of them come to the same answer
 // before any writes: a fork reads rows that are no fork's target.
-__global__ void __launch_bounds__(kPagedThreads) paged_fork_kernel(const ForkArgs F) {
+__global__ void __launch_bounds__(kThreads) paged_fork_kernel(const ForkArgs F) {
   extern __shared__ int32_t smem[];
-  int32_t* const cols = smem;                 // exclusive sums of the entries
-  int32_t* const parts = smem + F.forks;      // exclusive sums of the partly filled pages
+  __shared__ long long warp_sum[kWarps];
+  int32_t* const cols = smem;             // exclusive sums of the entries
+  int32_t* const parts = smem + F.forks;  // exclusive sums of the partly filled pages
   uint32_t* const is_src = reinterpret_cast<uint32_t*>(smem + 2 * F.forks);
   const int row_words = (F.P.rows + 31) / 32;
   uint32_t* const is_dst = is_src + row_words;
   const int64_t cap = F.P.width << F.P.page_log2;
   const int in_page = (1 << F.P.page_log2) - 1;
+  for (int i = threadIdx.x; i < 2 * row_words; i += kThreads) is_src[i] = 0;
   grid_begin();
-  for (int i = threadIdx.x; i < 2 * row_words; i += kPagedThreads) is_src[i] = 0;
   __syncthreads();
   bool bad = false;
-  const auto fits = [&](int i, int& s, int& d, int& len) {
-    s = ld_plain(F.src + i), d = ld_plain(F.dst + i), len = ld_plain(F.len + i);
-    return s >= 0 && s < F.P.rows && d >= 0 && d < F.P.rows && len >= 0 && len <= cap && len <= kPagedMaxTokens;
-  };
-  for (int i = threadIdx.x; i < F.forks; i += kPagedThreads) {
-    int s, d, len;
-    if (!fits(i, s, d, len)) {
-      bad = true;
-      continue;
+  long long carry = 0;  // both sums: 2^41 entries at most below, partly filled pages above
+  constexpr int kPart = 46;
+  for (int base = 0; base < F.forks; base += kThreads) {
+    const int i = base + (int)threadIdx.x;
+    long long mine = 0, total;
+    if (i < F.forks) {
+      const int s = ld_plain(F.src + i), d = ld_plain(F.dst + i), len = ld_plain(F.len + i);
+      if (s >= 0 && s < F.P.rows && d >= 0 && d < F.P.rows && len >= 0 && len <= cap && len <= kPagedMaxTokens) {
+        atomicOr(is_src + (s >> 5), 1u << (s & 31));
+        bad |= (atomicOr(is_dst + (d >> 5), 1u << (d & 31)) >> (d & 31)) & 1u;
+        mine = pages_of(len, F.P.page_log2);
+        if (len & in_page) {
+          const int32_t e = ld_plain(F.P.table + s * F.P.width + (len >> F.P.page_log2));
+          bad |= e < 0 || e >= F.P.pages;
+          mine += 1LL << kPart;
+        }
+      } else {
+        bad = true;
+      }
     }
-    atomicOr(is_src + (s >> 5), 1u << (s & 31));
-    bad |= (atomicOr(is_dst + (d >> 5), 1u << (d & 31)) >> (d & 31)) & 1u;
-    if (len & in_page) {
-      const int32_t e = ld_plain(F.P.table + s * F.P.width + (len >> F.P.page_log2));
-      bad |= e < 0 || e >= F.P.pages;
+    const long long at = carry + block_scan(mine, warp_sum, total);
+    if (i < F.forks) {
+      const long long n = at & ((1LL << kPart) - 1);
+      cols[i] = (int32_t)(n < INT32_MAX ? n : INT32_MAX);
+      parts[i] = (int32_t)(at >> kPart);
     }
+    carry += total;
   }
+  const long long entries = carry & ((1LL << kPart) - 1), fresh = carry >> kPart;
   __syncthreads();
-  for (int i = threadIdx.x; i < row_words; i += kPagedThreads) bad |= (is_src[i] & is_dst[i]) != 0;
-  const long long entries = sum_rows(F.forks, cols, [&](int i) -> long long {
-    int s, d, len;
-    return fits(i, s, d, len) ? pages_of(len, F.P.page_log2) : 0;
-  });
-  const long long fresh = sum_rows(F.forks, parts, [&](int i) -> long long { return (ld_plain(F.len + i) & in_page) != 0; });
+  for (int i = threadIdx.x; i < row_words; i += kThreads) bad |= (is_src[i] & is_dst[i]) != 0;
   const int64_t count0 = ld_plain(F.free_count), count = clamp_count(F.free_count, F.P.free_cap);
   bad |= count != count0 || fresh > count || entries > INT32_MAX;
   bad = __syncthreads_or(bad);  // (and the sums are in)
-  const int64_t tid = (int64_t)blockIdx.x * kPagedThreads + threadIdx.x, step = (int64_t)gridDim.x * kPagedThreads;
+  const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
   if (tid == 0) {
     if (bad) raise_error(F.P.err, TP3D_EPAGES);
     *F.copy_count = bad ? 0 : (int32_t)fresh;
@@ -136,8 +159,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_fork_kernel(const ForkArg
   if (bad) return;
   for (int64_t x = tid; x < entries; x += step) {
     const int i = last_at_most(cols, F.forks, (int32_t)x);
-    int s, d, len;
-    fits(i, s, d, len);
+    const int s = ld_plain(F.src + i), d = ld_plain(F.dst + i), len = ld_plain(F.len + i);
     const int64_t col = x - cols[i];
     int32_t e = ld_plain(F.P.table + s * F.P.width + col);
     if (col < len >> F.P.page_log2) {
@@ -171,7 +193,7 @@ struct FreeArgs {
 // number of owners given up too many brings back.
 constexpr int kGone = 1 << 30;
 
-__global__ void __launch_bounds__(kPagedThreads) paged_free_mark_kernel(const FreeArgs F) {
+__global__ void __launch_bounds__(kThreads) paged_free_mark_kernel(const FreeArgs F) {
   extern __shared__ int32_t smem[];
   grid_begin();
   bool bad = false;
@@ -186,8 +208,8 @@ __global__ void __launch_bounds__(kPagedThreads) paged_free_mark_kernel(const Fr
   if (bad) raise_error(F.P.err, TP3D_EPAGES);
   __syncthreads();
   if (entries > INT32_MAX) return;
-  const int64_t step = (int64_t)gridDim.x * kPagedThreads;
-  for (int64_t x = (int64_t)blockIdx.x * kPagedThreads + threadIdx.x; x < entries; x += step) {
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  for (int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x; x < entries; x += step) {
     const int r = last_at_most(smem, F.P.rows, (int32_t)x);
     int32_t* const at = F.P.table + r * F.P.width + ld_plain(F.first + r) + (x - smem[r]);
     const int32_t e = *at;
@@ -200,30 +222,24 @@ __global__ void __launch_bounds__(kPagedThreads) paged_free_mark_kernel(const Fr
     const int old = atomicSub(F.P.shares + e, 1);
     if (old == 0) {
       atomicSub(F.P.shares + e, kGone);
-      atomicAdd(F.P.words + kCounts + (e >> F.P.chunk_log2), 1u);
+      atomicAdd(count_word(F.P.words, 0, e >> F.P.chunk_log2), 1u);
     } else if (old < 0) {
       raise_error(F.P.err, TP3D_EPAGES);
     }
   }
 }
 
-// Clears `n` of the counts with the last CTA to come, when all have read them.
-__device__ __forceinline__ void clear_words(unsigned* words, int n) {
-  __shared__ int last;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicInc(words + kArrivals, gridDim.x - 1) == gridDim.x - 1;
-  __syncthreads();
-  if (last)
-    for (int i = threadIdx.x; i < n; i += kPagedThreads) words[kCounts + i] = 0;
-}
-
-__global__ void __launch_bounds__(kPagedThreads) paged_free_list_kernel(const FreeArgs F) {
+__global__ void __launch_bounds__(kThreads) paged_free_list_kernel(const FreeArgs F) {
   __shared__ int32_t above[kChunks];  // pages freed in the chunks from the last one down to this, less its own
   __shared__ long long warp_sum[kWarps];
+  __shared__ int last;
   grid_begin();
   const int chunks = (int)((F.P.pages + (1LL << F.P.chunk_log2) - 1) >> F.P.chunk_log2);
-  const long long freed = sum_rows(chunks, above, [&](int i) -> long long { return F.P.words[kCounts + chunks - 1 - i]; });
+  const int64_t size = 1LL << F.P.chunk_log2;
+  const auto page = [&](int i, int64_t base) { return ((int64_t)(chunks - 1 - i) << F.P.chunk_log2) + base - 1 - threadIdx.x; };
+  const auto share = [&](int64_t p) { return p < F.P.pages ? ld_plain(F.P.shares + p) : 0; };
+  int32_t first = share(page(blockIdx.x, size));  // on its way while the counts are added up
+  const long long freed = sum_rows(chunks, above, [&](int i) { return count_of(F.P.words, 0, chunks - 1 - i); });
   __syncthreads();
   const int64_t count0 = ld_plain(F.free_count), count = clamp_count(F.free_count, F.P.free_cap);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -232,12 +248,11 @@ __global__ void __launch_bounds__(kPagedThreads) paged_free_list_kernel(const Fr
     *F.free_left = (int32_t)(left < F.P.free_cap ? left : F.P.free_cap);
   }
   for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
-    const int64_t lo = (int64_t)(chunks - 1 - i) << F.P.chunk_log2;
     int64_t at = count + above[i];
     if ((i + 1 < chunks ? above[i + 1] : freed) == above[i]) continue;
-    for (int64_t base = 1LL << F.P.chunk_log2; base > 0; base -= kPagedThreads) {
-      const int64_t p = lo + base - 1 - threadIdx.x;
-      const bool gone = p < F.P.pages && ld_plain(F.P.shares + p) < -kGone / 2;
+    for (int64_t base = size; base > 0; base -= kThreads) {
+      const int64_t p = page(i, base);
+      const bool gone = (i == blockIdx.x && base == size ? first : share(p)) < -kGone / 2;
       long long total;
       const int64_t to = at + block_scan(gone, warp_sum, total);
       at += total;
@@ -246,7 +261,13 @@ __global__ void __launch_bounds__(kPagedThreads) paged_free_list_kernel(const Fr
       if (to < F.P.free_cap) F.P.free_pages[to] = (int32_t)p;
     }
   }
-  clear_words(F.P.words, chunks);
+  // the last CTA to come, when all have read the counts, clears them
+  __syncthreads();
+  if (threadIdx.x == 0) last = arrive_last(F.P.words + kArrivals, gridDim.x);
+  __syncthreads();
+  if (last)
+    for (int k = 0; k < kCopies; ++k)
+      for (int i = threadIdx.x; i < chunks; i += kThreads) F.P.words[kCounts + k * kChunks + i] = 0;
 }
 
 // ------------------------------------------------------------------ compact
@@ -264,19 +285,19 @@ __device__ __forceinline__ bool good_count(const CompactArgs& C, int64_t& count)
 
 // Marks the free pages, and counts them by chunk: those below `used` (the places
 // to fill), and the others.
-__global__ void __launch_bounds__(kPagedThreads) paged_compact_mark_kernel(const CompactArgs C) {
+__global__ void __launch_bounds__(kThreads) paged_compact_mark_kernel(const CompactArgs C) {
   grid_begin();
   int64_t count;
   bool bad = !good_count(C, count);
-  const int64_t used = C.P.pages - count, step = (int64_t)gridDim.x * kPagedThreads;
+  const int64_t used = C.P.pages - count, step = (int64_t)gridDim.x * kThreads;
   if (!bad)
-    for (int64_t i = (int64_t)blockIdx.x * kPagedThreads + threadIdx.x; i < count; i += step) {
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < count; i += step) {
       const int32_t p = ld_plain(C.P.free_pages + i);
       if (p < 0 || p >= C.P.pages || atomicExch(C.P.shares + p, kIsFree) == kIsFree) {
         bad = true;
         continue;
       }
-      atomicAdd(C.P.words + kCounts + (p < used ? 0 : kChunks) + (p >> C.P.chunk_log2), 1u);
+      atomicAdd(count_word(C.P.words, p < used ? 0 : 1, p >> C.P.chunk_log2), 1u);
     }
   if (bad) {
     raise_error(C.P.err, TP3D_EPAGES);
@@ -284,30 +305,45 @@ __global__ void __launch_bounds__(kPagedThreads) paged_compact_mark_kernel(const
   }
 }
 
-// The two lists, and the map of all pages but those that move.
-__global__ void __launch_bounds__(kPagedThreads) paged_compact_list_kernel(const CompactArgs C) {
+// The two lists, and the map; a page that moves has -2 - n there, for its place n in the lists.
+__global__ void __launch_bounds__(kThreads) paged_compact_list_kernel(const CompactArgs C) {
   __shared__ int32_t holes[kChunks], movers[kChunks];
   __shared__ long long warp_sum[kWarps];
   grid_begin();
   int64_t count;
   good_count(C, count);
-  const bool bad = C.P.words[kBad] != 0;
   const int64_t used = C.P.pages - count, size = 1LL << C.P.chunk_log2;
+  const auto share = [&](int64_t p) { return p < C.P.pages ? ld_plain(C.P.shares + p) : 0; };
+  const int32_t ahead = share(blockIdx.x * size + threadIdx.x);  // on its way while the counts are added up
+  const bool bad = C.P.words[kBad] != 0;
   const int chunks = (int)((C.P.pages + size - 1) >> C.P.chunk_log2);
-  const long long moves = sum_rows(chunks, holes, [&](int i) -> long long { return C.P.words[kCounts + i]; });
-  sum_rows(chunks, movers, [&](int i) -> long long {
-    const int64_t lo = i * size > used ? i * size : used, hi = (i + 1) * size < C.P.pages ? (i + 1) * size : C.P.pages;
-    return hi > lo ? hi - lo - (int64_t)C.P.words[kCounts + kChunks + i] : 0;
-  });
+  long long carry = 0;  // both sums: places to fill below, pages that move above
+  for (int base = 0; base < chunks; base += kThreads) {
+    const int i = base + (int)threadIdx.x;
+    long long mine = 0, total;
+    if (i < chunks) {
+      const int64_t lo = i * size > used ? i * size : used, hi = (i + 1) * size < C.P.pages ? (i + 1) * size : C.P.pages;
+      mine = count_of(C.P.words, 0, i) + ((hi > lo ? hi - lo - count_of(C.P.words, 1, i) : 0) << 32);
+    }
+    const long long at = carry + block_scan(mine, warp_sum, total);
+    if (i < chunks) {
+      holes[i] = (int32_t)(at & 0xffffffffLL);
+      movers[i] = (int32_t)(at >> 32);
+    }
+    carry += total;
+  }
   __syncthreads();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *C.copy_count = bad ? 0 : (int32_t)moves;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *C.copy_count = bad ? 0 : (int32_t)(carry & 0xffffffffLL);
+    C.P.words[kWasBad] = bad;
+  }
   const int64_t most = C.P.pages / 2;
   for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
     int64_t hole_at = holes[i], mover_at = movers[i];
-    for (int64_t base = 0; base < size; base += kPagedThreads) {
+    for (int64_t base = 0; base < size; base += kThreads) {
       const int64_t p = i * size + base + threadIdx.x;
       if (i * size + base >= C.P.pages) break;
-      const bool in = p < C.P.pages, free = in && ld_plain(C.P.shares + p) == kIsFree;
+      const bool in = p < C.P.pages, free = (i == blockIdx.x && base == 0 ? ahead : share(p)) == kIsFree;
       const bool hole = free && p < used, mover = in && !free && p >= used;
       long long total;  // both ranks in one sum
       const long long at = block_scan((hole ? 1LL : 0) + (mover ? 1LL << 32 : 0), warp_sum, total);
@@ -321,27 +357,30 @@ __global__ void __launch_bounds__(kPagedThreads) paged_compact_list_kernel(const
       }
       if (hole && h < most) C.copy_to[h] = (int32_t)p;
       if (mover && m < most) C.copy_from[m] = (int32_t)p;
-      if (in && !mover) C.map[p] = free ? -1 : (int32_t)p;
+      if (in) C.map[p] = mover ? (int32_t)(-2 - m) : free ? -1 : (int32_t)p;
     }
   }
-  clear_words(C.P.words, 2 * kChunks);
 }
 
-// Shares, map and free list follow the moves, and the tables' entries.
-__global__ void __launch_bounds__(kPagedThreads) paged_compact_move_kernel(const CompactArgs C) {
+// Shares, map and free list follow the moves, and the tables' entries.  An entry's
+// reader finds a moved page's word in the map as it was or already with the new
+// page, and comes to the same page by either (relaxed accesses, both of 32 bits).
+__global__ void __launch_bounds__(kThreads) paged_compact_move_kernel(const CompactArgs C) {
   extern __shared__ int32_t smem[];
-  __shared__ int last;
   grid_begin();
-  const bool bad = C.P.words[kBad] != 0;
+  const bool bad = C.P.words[kWasBad] != 0;
   int64_t count;
   good_count(C, count);
-  const int64_t used = C.P.pages - count, cap = C.P.width << C.P.page_log2;
-  const int64_t tid = (int64_t)blockIdx.x * kPagedThreads + threadIdx.x, step = (int64_t)gridDim.x * kPagedThreads;
+  const int64_t cap = C.P.width << C.P.page_log2;
+  const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+  // what the two kernels before this have read is zero again
+  for (int64_t i = tid; i < 2 * kCopies * kChunks; i += step) C.P.words[kCounts + i] = 0;
+  if (tid == 0) C.P.words[kBad] = 0;
   if (!bad) {
     const int32_t moves = ld_plain(C.copy_count);
     for (int64_t i = tid; i < moves; i += step) {
       const int32_t from = ld_plain(C.copy_from + i), to = ld_plain(C.copy_to + i);
-      C.map[from] = to;
+      asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" ::"l"(C.map + from), "r"(to) : "memory");
       C.P.shares[to] = ld_plain(C.P.shares + from);
       C.P.shares[from] = 0;
     }
@@ -358,17 +397,15 @@ __global__ void __launch_bounds__(kPagedThreads) paged_compact_move_kernel(const
       const int r = last_at_most(smem, C.P.rows, (int32_t)x);
       int32_t* const at = C.P.table + r * C.P.width + (x - smem[r]);
       const int32_t e = *at;
-      if (e < used) continue;  // (no page, or one that stays)
-      const int n = moves > 0 && e >= ld_plain(C.copy_from) ? last_at_most(C.copy_from, moves, e) : -1;
-      if (n >= 0 && ld_plain(C.copy_from + n) == e) *at = ld_plain(C.copy_to + n);
-      else wrong = true;
+      if (e < 0) continue;
+      int32_t now = -1;
+      if (e < C.P.pages) asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(now) : "l"(C.map + e) : "memory");
+      if (now < -1) now = -2 - now < moves ? ld_plain(C.copy_to + (-2 - now)) : -1;
+      if (now < 0) wrong = true;
+      else if (now != e) *at = now;
     }
     if (wrong || entries > INT32_MAX) raise_error(C.P.err, TP3D_EPAGES);
   }
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicInc(C.P.words + kArrivals, gridDim.x - 1) == gridDim.x - 1;
-  __syncthreads();
-  if (last && threadIdx.x == 0) C.P.words[kBad] = 0;
 }
 
 // ------------------------------------------------------------------ copy
@@ -383,11 +420,15 @@ struct CopyArgs {
   const int32_t *from, *to, *count;
   int* err;
 };
+// Many more CTAs than there is room for, a tile or a few each: they come and go
+// by themselves, which keeps reads and writes mixed (2333 pages of 64 KiB in K and
+// V: 92 us, 0.97 of the copy rate; in a grid of four to an SM 103, of eight 94).
+constexpr int kCopyThreads = 256, kCopyPerSm = 64;
 constexpr int kCopyVecs = 8;                                          // in flight per thread
-constexpr uint32_t kCopyTile = (uint32_t)kPagedThreads * kCopyVecs;  // 32 KiB
+constexpr uint32_t kCopyTile = (uint32_t)kCopyThreads * kCopyVecs;  // 32 KiB
 
 template <bool WHOLE>
-__global__ void __launch_bounds__(kPagedThreads) paged_copy_kernel(const CopyArgs C) {
+__global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const CopyArgs C) {
   grid_begin();
   int64_t n = C.copies;
   if (C.count) {
@@ -413,7 +454,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_copy_kernel(const CopyArg
     int64_t at[kCopyVecs];
 #pragma unroll
     for (int i = 0; i < kCopyVecs; ++i) {
-      const uint32_t v = v0 + i * kPagedThreads;
+      const uint32_t v = v0 + i * kCopyThreads;
       at[i] = v;
       if (!WHOLE) {
         const uint32_t k = v / C.run, o = k / C.n1;
@@ -423,7 +464,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_copy_kernel(const CopyArg
     }
 #pragma unroll
     for (int i = 0; i < kCopyVecs; ++i)
-      if (v0 + i * kPagedThreads < C.vectors) dst[at[i]] = r[i];
+      if (v0 + i * kCopyThreads < C.vectors) dst[at[i]] = r[i];
   }
 }
 
@@ -437,7 +478,7 @@ tp3d_status check_pool(const tp3d_ctx* ctx, const tp3d_page_pool* p, Pool* out) 
   if (p->free_cap < p->pages) return TP3D_ESHAPE;
   for (const void* x : {p->block_table, p->shares, p->free_pages})
     if (!aligned(x, 4)) return TP3D_EALIGN;
-  int chunk = 8;  // a pass of a CTA at least
+  int chunk = 9;  // a pass of a CTA at least
   while ((p->pages + (1LL << chunk) - 1) >> chunk > kChunks) ++chunk;
   *out = Pool{pl, p->rows, chunk, p->pages, p->table_width, p->free_cap, p->block_table, p->shares, p->free_pages,
               ctx->d_paged, ctx->d_err};
@@ -465,9 +506,13 @@ tp3d_status ready(tp3d_ctx* ctx) {
   return TP3D_OK;
 }
 
-unsigned chunk_blocks(const tp3d_ctx* ctx, const Pool& P) {
-  const int64_t chunks = (P.pages + (1LL << P.chunk_log2) - 1) >> P.chunk_log2;
-  return (unsigned)(chunks < ctx->num_sms ? chunks : ctx->num_sms);
+unsigned grid_of(const tp3d_ctx* ctx, int64_t threads, size_t smem) {
+  const int64_t n = (threads + kThreads - 1) / kThreads, most = (int64_t)ctx->num_sms * (smem > 48 * 1024 ? 1 : 2);
+  return (unsigned)(n < 1 ? 1 : n < most ? n : most);
+}
+unsigned chunk_grid(const tp3d_ctx* ctx, const Pool& P) {
+  const int64_t chunks = (P.pages + (1LL << P.chunk_log2) - 1) >> P.chunk_log2, most = (int64_t)ctx->num_sms * 2;
+  return (unsigned)(chunks < most ? chunks : most);
 }
 
 }  // namespace
@@ -495,7 +540,7 @@ tp3d_status tp3d_paged_fork(tp3d_ctx* ctx, const tp3d_page_pool* pool, int forks
   TP3D_TRY(ready(ctx));
   const ForkArgs F{P, forks, src, dst, len, free_count, free_left, copy_from, copy_to, copy_count};
   const size_t smem = (size_t)forks * 8 + (size_t)((P.rows + 31) / 32) * 8;
-  return launch_dependent(paged_fork_kernel, blocks(ctx, forks * P.width, 1), kPagedThreads, smem, as_stream(stream), F);
+  return launch_dependent(paged_fork_kernel, grid_of(ctx, forks * P.width, smem), kThreads, smem, as_stream(stream), F);
 }
 
 tp3d_status tp3d_paged_free(tp3d_ctx* ctx, const tp3d_page_pool* pool, const int32_t* first, const int32_t* end,
@@ -512,8 +557,8 @@ tp3d_status tp3d_paged_free(tp3d_ctx* ctx, const tp3d_page_pool* pool, const int
   TP3D_TRY(ready(ctx));
   const FreeArgs F{P, first, end, free_count, free_left};
   const cudaStream_t s = as_stream(stream);
-  TP3D_TRY(launch_dependent(paged_free_mark_kernel, blocks(ctx, P.rows * P.width, 1), kPagedThreads, rb, s, F));
-  return launch_dependent(paged_free_list_kernel, chunk_blocks(ctx, P), kPagedThreads, 0, s, F);
+  TP3D_TRY(launch_dependent(paged_free_mark_kernel, grid_of(ctx, P.rows * P.width, rb), kThreads, rb, s, F));
+  return launch_dependent(paged_free_list_kernel, chunk_grid(ctx, P), kThreads, 0, s, F);
 }
 
 tp3d_status tp3d_paged_compact(tp3d_ctx* ctx, const tp3d_page_pool* pool, const int32_t* kv_len,
@@ -532,11 +577,11 @@ tp3d_status tp3d_paged_compact(tp3d_ctx* ctx, const tp3d_page_pool* pool, const 
   TP3D_TRY(ready(ctx));
   const CompactArgs C{P, kv_len, free_count, page_map, copy_from, copy_to, copy_count};
   const cudaStream_t s = as_stream(stream);
-  TP3D_TRY(launch_dependent(paged_compact_mark_kernel, blocks(ctx, P.pages, 1), kPagedThreads, 0, s, C));
-  TP3D_TRY(launch_dependent(paged_compact_list_kernel, chunk_blocks(ctx, P), kPagedThreads, 0, s, C));
+  TP3D_TRY(launch_dependent(paged_compact_mark_kernel, grid_of(ctx, P.pages, 0), kThreads, 0, s, C));
+  TP3D_TRY(launch_dependent(paged_compact_list_kernel, chunk_grid(ctx, P), kThreads, 0, s, C));
   const int64_t entries = P.rows * P.width;
-  return launch_dependent(paged_compact_move_kernel, blocks(ctx, entries > P.pages ? entries : P.pages, 1),
-                          kPagedThreads, rb, s, C);
+  return launch_dependent(paged_compact_move_kernel, grid_of(ctx, entries > P.pages ? entries : P.pages, rb),
+                          kThreads, rb, s, C);
 }
 
 tp3d_status tp3d_paged_copy(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t copies, const int32_t* copy_from,
@@ -584,10 +629,10 @@ tp3d_status tp3d_paged_copy(tp3d_ctx* ctx, const tp3d_kv_cache* cache, int64_t c
   C.to = copy_to;
   C.count = copy_count;
   C.err = ctx->d_err;
-  const int64_t tiles = copies * 2 * ((C.vectors + kCopyTile - 1) / kCopyTile), most = (int64_t)ctx->num_sms * 4;
+  const int64_t tiles = copies * 2 * ((C.vectors + kCopyTile - 1) / kCopyTile), most = (int64_t)ctx->num_sms * kCopyPerSm;
   const unsigned grid = (unsigned)(tiles < most ? tiles : most);
-  return n1 == 1 && n2 == 1 ? launch_dependent(paged_copy_kernel<true>, grid, kPagedThreads, 0, as_stream(stream), C)
-                            : launch_dependent(paged_copy_kernel<false>, grid, kPagedThreads, 0, as_stream(stream), C);
+  return n1 == 1 && n2 == 1 ? launch_dependent(paged_copy_kernel<true>, grid, kCopyThreads, 0, as_stream(stream), C)
+                            : launch_dependent(paged_copy_kernel<false>, grid, kCopyThreads, 0, as_stream(stream), C);
 }
 
 }  // extern "C"
