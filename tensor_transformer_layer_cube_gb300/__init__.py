@@ -442,7 +442,7 @@ def tp3d_paged_attn(ctx, cache: tp3d_kv_cache, batch: tp3d_paged_batch, Q, O, ls
                     stream=None) -> int:
     """Q, O: (token, head, column) tensors; lse: dense (token, head) float32 or None."""
     heads, rows = _attn_rows("tp3d_paged_attn", cache, batch, Q, O, lse)
-    return lib().tp3d_paged_attn(ctx, ctypes.byref(cache), ctypes.byref(batch), heads, scale, *rows, _p(lse),
+    return lib().tp3d_paged_attn(ctx, cache, batch, heads, scale, *rows, _p(lse),
                                  _p(workspace), _s(stream))
 
 
@@ -450,7 +450,7 @@ def tp3d_paged_attn_window(ctx, cache: tp3d_kv_cache, batch: tp3d_paged_batch, Q
                            workspace, stream=None) -> int:
     """tp3d_paged_attn over a sliding window of ``window`` keys and the first ``sinks`` ones."""
     heads, rows = _attn_rows("tp3d_paged_attn_window", cache, batch, Q, O, lse)
-    return lib().tp3d_paged_attn_window(ctx, ctypes.byref(cache), ctypes.byref(batch), heads, scale, window, sinks,
+    return lib().tp3d_paged_attn_window(ctx, cache, batch, heads, scale, window, sinks,
                                         *rows, _p(lse), _p(workspace), _s(stream))
 
 
@@ -462,7 +462,7 @@ def _attn_rows(what, cache, batch, Q, O, lse):
         raise ValueError(f"{what}: Q and O (tokens, heads, head_dim) of the cache's type, contiguous columns")
     if lse is not None and (not lse.is_contiguous() or lse.shape != shape[:2] or _dtype_of(lse) != TP3D_F32):
         raise ValueError(f"{what}: lse dense (tokens, heads) float32")
-    return shape[1], (Q.data_ptr(), tp3d_row_strides(qs[0], qs[1]), O.data_ptr(), tp3d_row_strides(os_[0], os_[1]))
+    return shape[1], (Q.data_ptr(), _strides_of(Q), O.data_ptr(), _strides_of(O))
 
 
 def tp3d_paged_attn_workspace_bytes(ctx, cache: tp3d_kv_cache, heads: int) -> int:
@@ -474,46 +474,55 @@ def page_pool(page: int, block_table, shares, free_pages) -> tp3d_page_pool:
     page).  It holds their addresses: keep the tensors."""
     if block_table.dim() != 2 or shares.dim() != 1 or free_pages.dim() != 1:
         raise ValueError("page_pool: block_table (rows, width), shares (pages), free_pages (entries)")
-    _words("page_pool", (block_table, None), (shares, None), (free_pages, None))
+    _words("page_pool", (0, 0, 0), block_table, shares, free_pages)
     return tp3d_page_pool(page, block_table.shape[0], shares.numel(), block_table.shape[1], free_pages.numel(),
                           block_table.data_ptr(), shares.data_ptr(), free_pages.data_ptr())
 
 
-def _words(what, *arrays):
-    """Pointers of contiguous int32 tensors of at least so many elements."""
-    for x, n in arrays:
-        if _dtype_of(x) != _I32 or not x.is_contiguous() or (n is not None and x.numel() < n):
+_int32 = None
+
+
+def _words(what, sizes, *arrays):
+    """Pointers of contiguous int32 tensors of at least so many elements each."""
+    global _int32
+    if _int32 is None:
+        import torch
+        _int32 = torch.int32
+    out = []
+    for n, x in zip(sizes, arrays):
+        if x.dtype is not _int32 or x.numel() < n or not x.is_contiguous():
             raise ValueError(f"{what}: contiguous int32 tensors, one element for each of what they describe")
-    return [x.data_ptr() for x, _ in arrays]
+        out.append(x.data_ptr())
+    return out
 
 
 def tp3d_paged_fork(ctx, pool: tp3d_page_pool, src, dst, len, free_count, free_left, copy_from, copy_to, copy_count,
                     stream=None) -> int:
     """One fork for each element of ``src``."""
     n = src.numel()
-    return lib().tp3d_paged_fork(ctx, ctypes.byref(pool), n,
-                                 *_words("tp3d_paged_fork", (src, n), (dst, n), (len, n), (free_count, 1),
-                                         (free_left, 1), (copy_from, n), (copy_to, n), (copy_count, 1)), _s(stream))
+    return lib().tp3d_paged_fork(ctx, pool, n,
+                                 *_words("tp3d_paged_fork", (n, n, n, 1, 1, n, n, 1), src, dst, len, free_count,
+                                         free_left, copy_from, copy_to, copy_count), _s(stream))
 
 
 def tp3d_paged_free(ctx, pool: tp3d_page_pool, first, end, free_count, free_left, stream=None) -> int:
-    return lib().tp3d_paged_free(ctx, ctypes.byref(pool),
-                                 *_words("tp3d_paged_free", (first, pool.rows), (end, pool.rows), (free_count, 1),
-                                         (free_left, 1)), _s(stream))
+    n = pool.rows
+    return lib().tp3d_paged_free(ctx, pool, *_words("tp3d_paged_free", (n, n, 1, 1), first, end, free_count, free_left),
+                                 _s(stream))
 
 
 def tp3d_paged_compact(ctx, pool: tp3d_page_pool, kv_len, free_count, page_map, copy_from, copy_to, copy_count,
                        stream=None) -> int:
     n = pool.pages
-    return lib().tp3d_paged_compact(ctx, ctypes.byref(pool),
-                                    *_words("tp3d_paged_compact", (kv_len, pool.rows), (free_count, 1), (page_map, n),
-                                            (copy_from, n // 2), (copy_to, n // 2), (copy_count, 1)), _s(stream))
+    return lib().tp3d_paged_compact(ctx, pool,
+                                    *_words("tp3d_paged_compact", (pool.rows, 1, n, n // 2, n // 2, 1), kv_len,
+                                            free_count, page_map, copy_from, copy_to, copy_count), _s(stream))
 
 
 def tp3d_paged_copy(ctx, cache: tp3d_kv_cache, copies: int, copy_from, copy_to, copy_count=None, stream=None) -> int:
-    at, to = _words("tp3d_paged_copy", (copy_from, copies), (copy_to, copies))
-    count = None if copy_count is None else _words("tp3d_paged_copy", (copy_count, 1))[0]
-    return lib().tp3d_paged_copy(ctx, ctypes.byref(cache), copies, at, to, count, _s(stream))
+    at, to = _words("tp3d_paged_copy", (copies, copies), copy_from, copy_to)
+    count = None if copy_count is None else _words("tp3d_paged_copy", (1,), copy_count)[0]
+    return lib().tp3d_paged_copy(ctx, cache, copies, at, to, count, _s(stream))
 
 
 # ---------------------------------------------------------------------------
@@ -556,46 +565,71 @@ def rope(turns, dtype, head_dim: int, rotary_dim: int, interleaved: bool = False
                      _p(k_weight))
 
 
-def _rows_of(what, r: tp3d_rope, tokens, *arrays):
-    """Pointer and strides of (token, head, column) tensors, checked: the heads of each pair are the same."""
-    out = []
-    for x, heads in arrays:
-        shape, st = x.shape, x.stride()
-        if len(shape) != 3 or shape[0] != tokens or shape[1] != heads or shape[2] != r.head_dim or st[2] != 1 or \
-                _dtype_of(x) != r.dtype:
-            raise ValueError(f"{what}: (tokens, heads, head_dim) rows of one type, contiguous columns")
-        out += [x.data_ptr(), tp3d_row_strides(st[0], st[1])]
-    return out
+_row_strides = {}  # by a tensor's strides
+
+
+def _strides_of(x):
+    """The token and head strides of a (token, head, column) tensor; None where columns are not contiguous."""
+    st = x.stride()
+    r = _row_strides.get(st)
+    if r is None:
+        if len(st) != 3 or st[2] != 1:
+            return None
+        if len(_row_strides) > 1000:
+            _row_strides.clear()
+        r = _row_strides[st] = tp3d_row_strides(st[0], st[1])
+    return r
+
+
+def _rows_of(what, r: tp3d_rope, shape, a, b):
+    """Pointers and strides of two (token, head, column) tensors of one shape, checked."""
+    sa, sb, dt = _row_strides.get(a.stride()) or _strides_of(a), _row_strides.get(b.stride()) or _strides_of(b), r.dtype
+    if len(shape) != 3 or shape[2] != r.head_dim or sa is None or sb is None or a.shape != shape or b.shape != shape or \
+            _dtype_of(a) != dt or _dtype_of(b) != dt:
+        raise ValueError(f"{what}: (tokens, heads, head_dim) rows of one type, contiguous columns, the same heads for what "
+                         "belongs together")
+    return a.data_ptr(), sa, b.data_ptr(), sb
 
 
 def _positions(what, positions, tokens):
-    if _dtype_of(positions) != _I32 or not positions.is_contiguous() or positions.numel() < tokens:
+    if _dtype_of(positions) != _I32 or positions.numel() < tokens or not positions.is_contiguous():
         raise ValueError(f"{what}: a contiguous int32 position for each token")
     return positions.data_ptr()
 
 
 def tp3d_qk_rope(ctx, rope: tp3d_rope, Q, K, positions, Q_out, K_out, stream=None) -> int:
     """Q, Q_out (tokens, heads, head_dim), K, K_out (tokens, kv_heads, head_dim); in place where the same tensor."""
-    n, h, kh = Q.shape[0], Q.shape[1], K.shape[1]
-    q, qs, k, ks, qo, qos, ko, kos = _rows_of("tp3d_qk_rope", rope, n, (Q, h), (K, kh), (Q_out, h), (K_out, kh))
-    return lib().tp3d_qk_rope(ctx, ctypes.byref(rope), n, h, kh, q, qs, k, ks,
-                              _positions("tp3d_qk_rope", positions, n), qo, qos, ko, kos, _s(stream))
+    what, qs, ks = "tp3d_qk_rope", Q.shape, K.shape
+    q, qst, qo, qost = _rows_of(what, rope, qs, Q, Q_out)
+    k, kst, ko, kost = _rows_of(what, rope, ks, K, K_out)
+    n = qs[0]
+    if ks[0] != n:
+        raise ValueError("tp3d_qk_rope: Q and K of the same tokens")
+    return lib().tp3d_qk_rope(ctx, rope, n, qs[1], ks[1], q, qst, k, kst, _positions(what, positions, n), qo, qost, ko,
+                              kost, _s(stream))
 
 
 def tp3d_qk_rope_bwd(ctx, rope: tp3d_rope, Q, K, positions, dQ_out, dK_out, dQ, dK, dq_weight, dk_weight, workspace,
                      stream=None) -> int:
     """Shapes as in tp3d_qk_rope; Q and K may be None without the norm.  dq_weight, dk_weight: head_dim elements or
     None."""
-    n, h, kh = dQ_out.shape[0], dQ_out.shape[1], dK_out.shape[1]
-    what, none = "tp3d_qk_rope_bwd", [None, tp3d_row_strides(0, 0)]
-    q = _rows_of(what, rope, n, (Q, h)) if Q is not None else none
-    k = _rows_of(what, rope, n, (K, kh)) if K is not None else none
-    g = _rows_of(what, rope, n, (dQ_out, h), (dK_out, kh), (dQ, h), (dK, kh))
+    what, qs, ks = "tp3d_qk_rope_bwd", dQ_out.shape, dK_out.shape
+    none = (None, _no_strides)
+    q, qst = _rows_of(what, rope, qs, Q, Q)[:2] if Q is not None else none
+    k, kst = _rows_of(what, rope, ks, K, K)[:2] if K is not None else none
+    gq, gqst, dq, dqst = _rows_of(what, rope, qs, dQ_out, dQ)
+    gk, gkst, dk, dkst = _rows_of(what, rope, ks, dK_out, dK)
+    n = qs[0]
+    if ks[0] != n:
+        raise ValueError("tp3d_qk_rope_bwd: Q and K of the same tokens")
     for w in (dq_weight, dk_weight):
         if w is not None and (_dtype_of(w) != rope.dtype or not w.is_contiguous() or w.numel() != rope.head_dim):
             raise ValueError("tp3d_qk_rope_bwd: weights' gradients of head_dim contiguous elements of the heads' type")
-    return lib().tp3d_qk_rope_bwd(ctx, ctypes.byref(rope), n, h, kh, *q, *k, _positions(what, positions, n), *g,
-                                  _p(dq_weight), _p(dk_weight), _p(workspace), _s(stream))
+    return lib().tp3d_qk_rope_bwd(ctx, rope, n, qs[1], ks[1], q, qst, k, kst, _positions(what, positions, n), gq, gqst,
+                                  gk, gkst, dq, dqst, dk, dkst, _p(dq_weight), _p(dk_weight), _p(workspace), _s(stream))
+
+
+_no_strides = tp3d_row_strides(0, 0)
 
 
 def tp3d_qk_rope_bwd_workspace_bytes(ctx, rope: tp3d_rope) -> int:
@@ -605,13 +639,16 @@ def tp3d_qk_rope_bwd_workspace_bytes(ctx, rope: tp3d_rope) -> int:
 def tp3d_paged_rope_store(ctx, rope: tp3d_rope, cache: tp3d_kv_cache, Q, K, V, positions, slots, Q_out,
                           stream=None) -> int:
     """Q, Q_out (tokens, heads, head_dim), K, V (tokens, kv_heads, head_dim); an int64 slot for each token."""
-    n, h, kh = Q.shape[0], Q.shape[1], cache.kv_heads
-    what = "tp3d_paged_rope_store"
-    q, qs, k, ks, v, vs, qo, qos = _rows_of(what, rope, n, (Q, h), (K, kh), (V, kh), (Q_out, h))
-    if slots.numel() < n or _dtype_of(slots) != _I64 or not slots.is_contiguous():
+    what, qs, ks = "tp3d_paged_rope_store", Q.shape, K.shape
+    q, qst, qo, qost = _rows_of(what, rope, qs, Q, Q_out)
+    k, kst, v, vst = _rows_of(what, rope, ks, K, V)
+    n = qs[0]
+    if ks[0] != n or ks[1] != cache.kv_heads:
+        raise ValueError("tp3d_paged_rope_store: K and V of Q's tokens and the cache's heads")
+    if _dtype_of(slots) != _I64 or slots.numel() < n or not slots.is_contiguous():
         raise ValueError("tp3d_paged_rope_store: an int64 slot for each token")
-    return lib().tp3d_paged_rope_store(ctx, ctypes.byref(rope), ctypes.byref(cache), n, h, q, qs, k, ks, v, vs,
-                                       _positions(what, positions, n), slots.data_ptr(), qo, qos, _s(stream))
+    return lib().tp3d_paged_rope_store(ctx, rope, cache, n, qs[1], q, qst, k, kst, v, vst, _positions(what, positions, n),
+                                       slots.data_ptr(), qo, qost, _s(stream))
 
 
 # ---------------------------------------------------------------------------
