@@ -202,9 +202,7 @@ struct Gap {
   __device__ int at(int t) const { return t < lead ? t : t - gap > lead ? t - gap : lead; }
 };
 // the first key in the window of the row at position p
-__device__ __forceinline__ int window_begin(int64_t p, int window) {
-  return p >= window ? (int)(p - window + 1) : 0;
-}
+__device__ __forceinline__ int window_begin(int p, int window) { return p >= window ? p - window + 1 : 0; }
 
 // A position in a CTA's range: tile `tile`, below `end`, of the `tiles` of
 // (request b, head h, rows from row0), whose first is unit `at`.
@@ -224,7 +222,7 @@ struct FewCursor {
     const int64_t rows = (int64_t)n * A.group;
     tiles = kv > 0 ? (kv - 1) / Shape::kKeys + 1 : 1;  // a request without keys still has rows to write
     if (WIN) {
-      low = window_begin((int64_t)kv - n, A.window);
+      low = window_begin(kv - n, A.window);
       const int first = A.sinks < kv ? A.sinks : kv;
       gap.set((first + Shape::kKeys - 1) / Shape::kKeys, low / Shape::kKeys);
       tiles -= gap.gap;
@@ -490,7 +488,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
     const int key0 = c.key(c.tile) + warp * 16;
     if (key0 < c.kv) {
       // keys that some row does not see: past kv - n; before the last row's window
-      const int last_low = WIN ? window_begin((int64_t)c.kv - 1, A.window) : 0;
+      const int last_low = WIN ? window_begin(c.kv - 1, A.window) : 0;
       const bool partial = key0 + 15 > c.kv - c.n || (WIN && key0 < last_low && key0 + 15 >= A.sinks);
       if (partial && c.n > 1) {
         // A probability of 0 does not silence a value that is not finite: such
@@ -885,7 +883,7 @@ struct ManyRequest {
   // key tiles that no row of pair k sees, between the first keys and its first row's window
   __device__ Gap gap(int k) const {
     Gap g;
-    if (WIN) g.set((sinks + TR - 1) / TR, window_begin((int64_t)kv - n + (int64_t)k * 2 * tt, window) / TR);
+    if (WIN) g.set((sinks + TR - 1) / TR, window_begin(kv - n + k * 2 * tt, window) / TR);
     return g;
   }
   // the same of the pairs before pair k.  Pair i's window begins at c + w i, and what it misses are
@@ -945,6 +943,11 @@ __device__ __forceinline__ ManyRequest<WIN> many_request(const PagedAttn& A, int
 // up to 100 over 1000, 16 heads of 64 23.2 | 25.8; one prompt of 1000, 16 heads
 // 31.0 | 28.5; 4 x 200 over 3000 47.7 | 47.3.
 constexpr int kSnap = 4;
+// With a window pairs are short, and ranges that end at their edges alone
+// unequal.  By two tiles | four | one: 8192 tokens, window 1024, 16 heads of 128
+// 123.2 | 131.8 | 124.1 us; 4 x 384 over 3700, window 511, 32 heads of 64 on 8
+// 42.4 | 45.5 | 39.3; the same ragged, with 12 single tokens 42.5 | 42.6 | 44.5.
+constexpr int kSnapWindow = 2;
 constexpr int kManyMinTiles = 2;  // of a CTA's range, where there is little work (the first case above; with 1 30.3)
 template <bool WIN>
 struct ManyCursor {
@@ -968,7 +971,7 @@ struct ManyCursor {
     if (WIN) {
       gap = r.gap(k);
       const int end = (k + 1) * 2 * r.tt < r.n ? (k + 1) * 2 * r.tt : r.n;
-      const int last_low = window_begin((int64_t)r.kv - r.n + end - 1, r.window);  // of the pair's last row
+      const int last_low = window_begin(r.kv - r.n + end - 1, r.window);  // of the pair's last row
       low0 = gap.at(r.sinks / TR);
       low1 = last_low > r.sinks ? gap.at((last_low - 1) / TR) + 1 : low0;
     }
@@ -1334,7 +1337,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const Ranges R(units, ctas);
           cur.u = R.begin(blockIdx.x);
           const int near = (int)(units / ctas) - 2;
-          cur.near = near < 1 ? 1 : near < kSnap ? near : kSnap;
+          constexpr int most = WIN ? kSnapWindow : kSnap;
+          cur.near = near < 1 ? 1 : near < most ? near : most;
           cur.u1 = R.begin(blockIdx.x + 1);
           if (cur.u >= cur.u1) return;
         }
@@ -1437,7 +1441,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const int key = cur.tile(j) * TR + (pi << bl2);
           int32_t page = (int32_t)A.c.pages;
           const bool unseen = WIN && key >= cur.r.sinks &&
-                              key + (1 << bl2) <= window_begin((int64_t)cur.r.kv - cur.r.n + cur.tok(0), cur.r.window);
+                              key + (1 << bl2) <= window_begin(cur.r.kv - cur.r.n + cur.tok(0), cur.r.window);
           if (mine && key < cur.r.kv && !unseen) {
             page = ld_plain(A.table + (int64_t)cur.b * A.width + (key >> A.page_log2));
             if (page < 0 || page >= A.c.pages) {
