@@ -821,6 +821,7 @@ struct ManyShared {
   volatile unsigned ended[8];    // pieces that each row warp has ended: their notes may be begun anew
   int last;
   long long scan[kManyThreads / 32];
+  unsigned items;  // pairs of all requests (with a window)
   int before, per_head;
   int b0;
   // split pieces joined after the CTA's range (0: one that it goes on behind, 1: its last): row warps that have
@@ -948,6 +949,14 @@ constexpr int kSnap = 4;
 // 123.2 | 131.8 | 124.1 us; 4 x 384 over 3700, window 511, 32 heads of 64 on 8
 // 42.4 | 45.5 | 39.3; the same ragged, with 12 single tokens 42.5 | 42.6 | 44.5.
 constexpr int kSnapWindow = 2;
+// And where pairs are about alike in length and whole ones, dealt out to the CTAs,
+// are done no more than kJoin tiles later than equal ranges, none is cut: a cut
+// costs its CTAs a piece more to begin and to end, a part to leave and one to
+// join.  2048 tokens over 32001, 16 heads of 128, first 4 keys, window 512 37.6 us
+// (cut 45.9), 1024 50.7 (56.6), 2048 72.9 (77.9), 4096 108 (108).  With pairs of
+// several lengths whole ones come out uneven (4 requests of up to 4084 keys,
+// window 1500: 72.8, cut 55.1).
+constexpr float kJoin = 4.0f, kAlike = 0.9f;
 constexpr int kManyMinTiles = 2;  // of a CTA's range, where there is little work (the first case above; with 1 30.3)
 template <bool WIN>
 struct ManyCursor {
@@ -1156,10 +1165,25 @@ struct Seen {
   __device__ uint32_t bits(int c) const { return below(vis + 1 - c) & (~below(from - c) | below(upto - c)); }
   __device__ static uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 };
-template <int D, int PART>
+//
+// With a window a pair's first tiles are seen by some of its rows only.  Where a
+// warp has none of them, the tile's P is zeros; and a row that has not seen a key
+// yet has an O of zeros (or, after scores of -infinity alone, of NaN), so that
+// its first maximum rescales nothing (2048 tokens over 32001, window 6000, 16
+// heads of 128: 139.5 us against 142.6).
+template <int D, int PART, bool WIN>
 __device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t half, int lane, float sl2,
                                              const Seen& seen, bool first, float& m, float& l) {
   const int vis = seen.vis;
+  if (PART == 2 && __all_sync(0xffffffffu, vis < 0 || (vis < seen.from && seen.upto <= 0))) {
+    const uint32_t zeros[32] = {};
+#pragma unroll 1
+    for (int cc = 0; cc < 4; ++cc) tmem_st_32x32b_x32(s + (uint32_t)(cc * 32), zeros);
+    tmem_st_wait();
+    tc_fence_before();
+    warp_arrive(half, lane);
+    return;
+  }
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
   for (int cc = 0; cc < 4; ++cc) {
@@ -1179,7 +1203,7 @@ __device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t ha
   const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
   const bool move = mt > m + kMoveLog2;
   if (__any_sync(0xffffffffu, move)) {
-    if (!first) {
+    if (WIN ? __any_sync(0xffffffffu, move && m > -INFINITY) : !first) {
       const float f = move ? ex2_approx(m - mt) : 1.0f;
       l *= f;
 #pragma unroll 1
@@ -1298,6 +1322,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   {
     const bool one = A.requests <= kManyThreads;
     cur.u = -1;
+    unsigned items = 0;
+    if (WIN && threadIdx.x == 0) sh.items = 0;
 #pragma unroll 1
     for (int round = 0; round < 2; ++round) {
       long long carry = 0;
@@ -1307,7 +1333,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         long long tiles = 0;
         if (b < A.requests) {
           const ManyRequest<WIN> r = many_request<WIN>(A, b);
-          if (r.n > 0) tiles = r.total();
+          if (r.n > 0) {
+            tiles = r.total();
+            if (WIN && round == 0) items += (unsigned)r.pairs();
+          }
         }
         long long x = tiles;
 #pragma unroll
@@ -1339,6 +1368,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const int near = (int)(units / ctas) - 2;
           constexpr int most = WIN ? kSnapWindow : kSnap;
           cur.near = near < 1 ? 1 : near < most ? near : most;
+          if (WIN) {
+            items = __reduce_add_sync(0xffffffffu, items);
+            if (lane == 0) atomicAdd(&sh.items, items);
+            __syncthreads();
+            const float range = (float)units / (float)ctas;
+            const float pair = (float)units / ((float)sh.items * (float)A.c.kv_heads);
+            const float longest = (float)A.window / TR + (float)A.sinks / TR + (float)(2 * (TR / A.group)) / TR + 2.0f;
+            if (pair >= kAlike * longest && ceilf(range / pair) * pair <= range + kJoin) cur.near = INT32_MAX / 2;
+          }
           cur.u1 = R.begin(blockIdx.x + 1);
           if (cur.u >= cur.u1) return;
         }
@@ -1747,9 +1785,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         const Seen seen{lim - k0, WIN ? window_begin(lim, A.window) - k0 : 0, WIN ? cur.r.sinks - k0 : 0};
         const uint32_t sa = tmem_row(tmem, quarter, s_col), oa = tmem_row(tmem, quarter, o_col);
         if (__any_sync(0xffffffffu, seen.vis < TR - 1 || (WIN && seen.from > 0 && seen.upto < TR)))
-          many_softmax<D, WIN ? 2 : 1>(sa, oa, p_half(sl), lane, sl2, seen, j == cur.j0, m, l);
+          many_softmax<D, WIN ? 2 : 1, WIN>(sa, oa, p_half(sl), lane, sl2, seen, j == cur.j0, m, l);
         else
-          many_softmax<D, 0>(sa, oa, p_half(sl), lane, sl2, seen, j == cur.j0, m, l);
+          many_softmax<D, 0, WIN>(sa, oa, p_half(sl), lane, sl2, seen, j == cur.j0, m, l);
         tc_fence_before();
         warp_arrive(p_full(sl), lane);
       }
