@@ -11,6 +11,11 @@
 // chunk while they are marked, and a second kernel, chunk by chunk, ranks them.
 // The marks lie in the share counts, the chunks' counts in words of the context
 // that are zero between calls.
+//
+// On the GPU, in a captured graph: 448 forks of 64 requests of up to 8000 tokens
+// in pages of 16 (112000 entries) 5.3 us, 31000 pages given back 8.9 us in two
+// launches, a pool of 9233 pages compacted 9.1 us in three, without the copies.  A
+// call from Python takes 4 to 7 us of the host.
 #include <initializer_list>
 
 #include "paged.cuh"

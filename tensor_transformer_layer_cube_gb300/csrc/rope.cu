@@ -21,6 +21,13 @@
 // kind.  Passes are loaded several ahead into a ring in shared memory that each
 // lane fills and reads by itself (4 KiB a warp, no barrier), over the ends of
 // tokens.  All passes in a row are cut into equal ranges, one for each warp.
+//
+// Measured, of a stream of calls: 16385 tokens of 32 heads of 128 on 8, with the
+// store (403 MB) 69.5 us, 0.85 of the copy rate; 4095 tokens of 12 heads of 96 on
+// 4 in fp32, half of each turned (50 MB) 11.6 us, 0.64; 64 tokens of 16 heads of
+// 128 with the store 7.5 us, of which the GPU's part is 3.8.  A pass is 90
+// instructions; with rows of one token in a pass, their pairs on different lanes
+// and the angles by CUDA's function it was 195, and the times 95.8, 13.4 and 9.9.
 #include <math.h>
 
 #include "paged.cuh"
@@ -450,7 +457,10 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
 // Backward: g = R(p)^T dy; with the norm dx = s (w g - x s^2 mean(w g x)) and the
 // weights' gradients, the sums of g x s, kept in registers over a warp's tokens,
 // joined warp by warp in shared memory and CTA by CTA in the workspace, in a
-// fixed order; the last CTA to arrive adds the CTAs' parts.
+// fixed order; the last CTA to arrive adds the CTAs' parts.  Both sums of a row
+// come out of five shuffles.  4096 tokens of 16 heads of 128 (101 MB): 25.4 us,
+// 0.58 of the copy rate; without the weights' gradients 4 less, which are the
+// parts' way through L2 (16384 tokens 71 and 67 us, 0.83).
 template <class T, int LANES, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kBackThreads, 1) rope_back_kernel(const __grid_constant__ RopeArgs A) {
   constexpr int kTokens = 32 / LANES, kWarps = kBackThreads / 32;
