@@ -134,7 +134,7 @@ struct Row<float> {
 
 // Sine and cosine of an angle in units of 2^-32 turns: an integer number of
 // quarter turns off, what is left (an eighth of a turn at most) goes through the
-// Taylor series, whose next terms are below 2^-28 and 2^-30; to about 2 2^-24.
+// Taylor series, whose next terms are below 2^-29 and 2^-33; to about 2 2^-24.
 __device__ __forceinline__ void sincos_of(uint32_t turn, float& s, float& c) {
   const uint32_t q = (turn + 0x20000000u) >> 30;
   const float t = (float)(int32_t)(turn - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
     pos = ld_plain(A.positions + t);
     if (STORE) slot = ld_plain(A.slots + t);
   };
-  look(at.group);
+  if (at.rest > 0) look(at.group);
   int token = 0;
   int64_t pool = -1;  // where the token's rows lie in the pools
   int begun = -1;     // the group whose angles are here
@@ -435,9 +435,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
         f32x2 y[4];
         x.get(y);
         if (NORM) {
-          // (columns that are not turned: an x' that is not finite makes the whole row so)
           const f32x2 s = splat2(inverse_rms<LANES>(A.eps, y, inv_dim));
-          turn.apply(y, a, b, true);
+          turn.apply(y, a, b, all_turned);
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], s);
         } else {
@@ -500,7 +499,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) rope_back_kernel(const __grid
     t = group * kTokens + sub;
     if (t < A.tokens) pos = ld_plain(A.positions + t);
   };
-  look(at.group);
+  if (at.rest > 0) look(at.group);
   int token = 0, begun = -1;
   uint32_t stage = 0;
 #pragma unroll 1
@@ -550,11 +549,12 @@ __global__ void __launch_bounds__(kBackThreads, 1) rope_back_kernel(const __grid
         float xx = sum_of(q), gx = sum_of(dot);
         row_sums<LANES>(xx, gx, lane);
         const float s = rsqrtf(fmaf(xx, inv_dim, A.eps));
-        const f32x2 s2 = splat2(s), minus = splat2(-s * (s * (s * gx)) * inv_dim);
+        const f32x2 s2 = splat2(s), minus = splat2(-s * gx * inv_dim);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sum[e] = fma2(mul2(g[e], s2), y[e], sum[e]);
-          g[e] = fma2(y[e], minus, mul2(wg[e], s2));
+          y[e] = mul2(y[e], s2);
+          sum[e] = fma2(g[e], y[e], sum[e]);
+          g[e] = mul2(fma2(y[e], minus, wg[e]), s2);
         }
       }
       x.set(g);

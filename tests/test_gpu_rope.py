@@ -225,6 +225,34 @@ def test_values_that_are_not_finite_stay_in_their_rows(ctx, value):
             c.check(got, c.q, c.qw)
 
 
+def test_an_infinite_value_with_the_norm(ctx):
+    # 1 / sqrt(infinity) is 0: the value itself and the column that it turns against are 0 times infinity, the others 0
+    c = Case(9, 2, 1, 64, 32, BF16)
+    c.q[3, 1, 5] = c.q[4, 0, 60] = c.q[5, 0, 17] = float("inf")
+    got, k = c.new(2), c.new(1)
+    t.check(t.tp3d_qk_rope(ctx, c.rope, c.q, c.k, c.positions, got, k))
+    assert t.tp3d_sync_status(ctx) == 0
+    for row, cols in (((3, 1), [5, 21]), ((4, 0), [60]), ((5, 0), [17, 1])):
+        want = torch.zeros(64, dtype=torch.bool, device=device())
+        want[cols] = True
+        assert torch.equal(got[row].isnan(), want) and bool((got[row][~want] == 0).all())
+    c.check(k, c.k, c.kw)
+
+
+def test_gradients_of_very_small_rows(ctx):
+    # s of 10^15 and more, whose powers fp32 does not hold
+    c = Case(33, 2, 2, 64, 64, F32, eps=0.0, weights=False)
+    c.q *= 1e-16
+    c.k *= 1e15
+    rng = np.random.default_rng(11)
+    gq, gk = random(rng, F32, 33, 2, 64) * 1e-10, random(rng, F32, 33, 2, 64)
+    dq, dk = c.new(2), c.new(2)
+    t.check(t.tp3d_qk_rope_bwd(ctx, c.rope, c.q, c.k, c.positions, gq, gk, dq, dk, None, None, None))
+    assert t.tp3d_sync_status(ctx) == 0
+    c.check_back(dq, None, c.q, gq, None)
+    c.check_back(dk, None, c.k, gk, None)
+
+
 def test_bits_of_columns_that_are_not_turned(ctx):
     c = Case(16, 2, 1, 64, 16, BF16, norm=False)
     bits = torch.arange(16 * 2 * 64, dtype=torch.int32).mul(31).to(torch.int16).to(device()).view(16, 2, 64)
