@@ -70,7 +70,8 @@ typedef struct {
   const void *q_weight, *k_weight;
 } tp3d_rope;
 
-/* (token, head) rows of head_dim contiguous columns; strides in elements.    */
+/* (token, head) rows of head_dim contiguous columns, strides in elements; that
+ * the rows of an output do not overlap is the caller's to keep.              */
 typedef struct {
   int64_t token_stride, head_stride;
 } tp3d_row_strides;

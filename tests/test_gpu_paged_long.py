@@ -174,3 +174,62 @@ def test_long_conversations(ctx, page, heads, kv_heads, d, window, sinks, inter)
         s.end(r)
     s.check_books()
     assert int(s.count) == s.pages
+
+
+def test_two_servers_at_once(ctx):
+    # a context each, on streams of their own: what they say is what each says alone
+    other = t.tp3d_create(0)
+    try:
+        shape = (8, 160, 40, 16, 4, 2, 64, 40, 5, False)
+        alone = Server(ctx, *shape)
+        pair = [Server(ctx, *shape), Server(other, *shape)]
+        streams = [torch.cuda.Stream() for _ in pair]
+        torch.cuda.synchronize()
+        n, h, kh, d = 3000, alone.heads, alone.kv_heads, alone.d
+        rng = np.random.default_rng(3)
+        x = values(rng, (n, (h + kh) * d)).to(device())
+        g = values(rng, (n, (h + kh) * d)).to(device())
+        pos = i32(rng.integers(0, 5000, n))
+
+        class Work:
+            # gradients, whose sums share the context's words, then pages taken and given back
+            def __init__(self, s):
+                self.s = s
+                self.q, self.k = x[:, :h * d].view(n, h, d), x[:, h * d:].view(n, kh, d)
+                self.gq, self.gk = g[:, :h * d].view(n, h, d), g[:, h * d:].view(n, kh, d)
+                self.dq, self.dk = torch.empty_like(self.q.contiguous()), torch.empty_like(self.k.contiguous())
+                self.dw = [torch.empty(d, dtype=torch.bfloat16, device=device()) for _ in range(2)]
+                self.ws = torch.empty(t.tp3d_qk_rope_bwd_workspace_bytes(s.ctx, s.rope), dtype=torch.uint8, device=device())
+                self.zero, self.fresh, self.ends = i32([0] * 8), i32([80] * 8), i32([5] * 8)
+                self.q_start, self.kv, self.at = i32([0] * 9), i32([0] * 8), i32([0] * 640)
+                self.slots, self.left = torch.zeros(640, dtype=torch.int64, device=device()), [i32([0]) for _ in range(2)]
+
+            def step(self, stream):
+                s = self.s
+                t.check(t.tp3d_qk_rope_bwd(s.ctx, s.rope, self.q, self.k, pos, self.gq, self.gk, self.dq, self.dk, *self.dw,
+                                           self.ws, stream))
+                t.check(t.tp3d_paged_plan(s.ctx, s.page, 8, 640, self.zero, self.fresh, s.free, s.pages, s.count, s.table,
+                                          s.width, self.q_start, self.kv, self.slots, self.at, self.left[0], stream))
+                t.check(t.tp3d_paged_free(s.ctx, s.pool, self.zero, self.ends, self.left[0], self.left[1], stream))
+
+            def said(self):
+                return [self.dq, self.dk, *self.dw, self.s.free, self.s.shares, self.s.table, self.left[1]]
+
+        one, both = Work(alone), [Work(s) for s in pair]
+        for _ in range(20):
+            one.step(torch.cuda.current_stream())
+        want = one.said()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for w, stream in zip(both, streams):
+                w.step(stream)
+        torch.cuda.synchronize()
+        got = [w.said() for w in both]
+        for s in pair:
+            assert t.tp3d_sync_status(s.ctx) == 0
+        for one in got:
+            for a, b in zip(one, want):
+                assert torch.equal(a, b)
+        assert int(want[-1]) == alone.pages
+    finally:
+        t.tp3d_destroy(other)
