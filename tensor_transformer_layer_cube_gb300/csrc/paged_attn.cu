@@ -892,9 +892,9 @@ struct ManyRequest {
   __device__ int64_t gaps_before(int k) const {
     const int w = 2 * tt, lead = (sinks + TR - 1) / TR;
     const int64_t c = (int64_t)kv - n - window + 1, from = ((int64_t)lead + 1) * TR;
-    const int64_t z = c >= from ? 0 : (from - c + w - 1) / w;
-    if (z >= k) return 0;
-    const int64_t b = c + w * z, left = k - z;
+    if (from - c > (int64_t)(k - 1) * w) return 0;
+    const int z = c >= from ? 0 : (int)((unsigned)(from - c + w - 1) / (unsigned)w);  // (in 32 bits: k w is)
+    const int64_t b = c + (int64_t)w * z, left = k - z;
     return left * (b / TR - lead) + (int64_t)(w / TR) * (left * (left - 1) / 2) +
            floor_sum((uint32_t)left, (uint32_t)(w % TR), (uint32_t)(b % TR));
   }
@@ -1157,33 +1157,15 @@ __device__ __forceinline__ bool notes_free(const volatile unsigned* ended, uint3
 // Both passes (maximum, then P) read the scores 32 columns at a time in rolled
 // loops: unrolled over the row, the code outgrows the instruction cache and
 // runs slower with half the instructions.  What has a paired fp32 form
-// (.f32x2) uses it.  PART 1: only columns up to `vis` are seen; 2: of these only
-// the ones from `from` on, and those below `upto`.
-struct Seen {
-  int vis, from, upto;
-  // of columns [c, c + 32), a bit each
-  __device__ uint32_t bits(int c) const { return below(vis + 1 - c) & (~below(from - c) | below(upto - c)); }
-  __device__ static uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-};
+// (.f32x2) uses it.  PART: only columns up to `vis` are seen.
 //
-// With a window a pair's first tiles are seen by some of its rows only.  Where a
-// warp has none of them, the tile's P is zeros; and a row that has not seen a key
-// yet has an O of zeros (or, after scores of -infinity alone, of NaN), so that
-// its first maximum rescales nothing (2048 tokens over 32001, window 6000, 16
-// heads of 128: 139.5 us against 142.6).
-template <int D, int PART, bool WIN>
-__device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t half, int lane, float sl2,
-                                             const Seen& seen, bool first, float& m, float& l) {
-  const int vis = seen.vis;
-  if (PART == 2 && __all_sync(0xffffffffu, vis < 0 || (vis < seen.from && seen.upto <= 0))) {
-    const uint32_t zeros[32] = {};
-#pragma unroll 1
-    for (int cc = 0; cc < 4; ++cc) tmem_st_32x32b_x32(s + (uint32_t)(cc * 32), zeros);
-    tmem_st_wait();
-    tc_fence_before();
-    warp_arrive(half, lane);
-    return;
-  }
+// With a window a pair's first tiles are seen by some of its rows only, and a row
+// that has not seen a key yet has an O of zeros (or, after scores of -infinity
+// alone, of NaN): its first maximum rescales nothing (2048 tokens over 32001,
+// window 6000, 16 heads of 128: 139.5 us against 142.6).
+template <int D, bool PART, bool WIN>
+__device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t half, int lane, float sl2, int vis,
+                                             bool first, float& m, float& l) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
   for (int cc = 0; cc < 4; ++cc) {
@@ -1191,12 +1173,10 @@ __device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t ha
     tmem_ld_32x32b_x32(s + (uint32_t)(cc * 32), v);
     tmem_ld_wait();
     const int left = vis - cc * 32;
-    const uint32_t in = PART == 2 ? seen.bits(cc * 32) : 0u;
-    const auto sees = [&](int e) { return PART == 2 ? (in >> e & 1u) != 0 : !PART || e <= left; };
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-      const float x = sees(e) ? __uint_as_float(v[e]) : -INFINITY;
-      const float y = sees(e + 1) ? __uint_as_float(v[e + 1]) : -INFINITY;
+      const float x = !PART || e <= left ? __uint_as_float(v[e]) : -INFINITY;
+      const float y = !PART || e + 1 <= left ? __uint_as_float(v[e + 1]) : -INFINITY;
       mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], x), y);
     }
   }
@@ -1227,14 +1207,12 @@ __device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t ha
     tmem_ld_32x32b_x32(s + (uint32_t)(cc * 32), v);
     tmem_ld_wait();
     const int left = vis - cc * 32;
-    const uint32_t in = PART == 2 ? seen.bits(cc * 32) : 0u;
-    const auto sees = [&](int e) { return PART == 2 ? (in >> e & 1u) != 0 : !PART || e <= left; };
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       float p0, p1, t0, t1;
       upk2(fma2(pk2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc, nb), p0, p1);
-      p0 = sees(2 * e) ? ex2_approx(p0) : 0.0f;
-      p1 = sees(2 * e + 1) ? ex2_approx(p1) : 0.0f;
+      p0 = !PART || 2 * e <= left ? ex2_approx(p0) : 0.0f;
+      p1 = !PART || 2 * e + 1 <= left ? ex2_approx(p1) : 0.0f;
       const f32x2 P = pk2(p0, p1);
       sum[e & 3] = add2(sum[e & 3], P);
       // hi: the upper halves as they are (truncated to bf16); lo: the exact rest, rounded
@@ -1254,6 +1232,32 @@ __device__ __forceinline__ void many_softmax(uint32_t s, uint32_t o, uint32_t ha
   float a0, a1;
   upk2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
   l += a0 + a1;
+}
+
+// With a window, the scores of a tile that a row does not see become -infinity
+// where they lie, and the softmax is that of whole tiles: of a warp's four groups
+// of 32 columns mostly one is seen in part, and a second softmax's instructions
+// would have to be fetched for every tile at a window's edge (XX).  Seen are the columns up to `vis` and from
+// `from` on, and those below `upto`.
+struct Seen {
+  int vis, from, upto;
+  // of columns [c, c + 32), a bit each
+  __device__ uint32_t bits(int c) const { return below(vis + 1 - c) & (~below(from - c) | below(upto - c)); }
+  __device__ static uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+};
+__device__ __forceinline__ void hide_unseen(uint32_t s, const Seen& seen) {
+#pragma unroll 1
+  for (int cc = 0; cc < 4; ++cc) {
+    const uint32_t in = seen.bits(cc * 32);
+    if (__all_sync(0xffffffffu, in == ~0u)) continue;
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(s + (uint32_t)(cc * 32), v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = in >> e & 1u ? v[e] : 0xff800000u;
+    tmem_st_32x32b_x32(s + (uint32_t)(cc * 32), v);
+  }
+  tmem_st_wait();
 }
 
 // With a window, which rows see a key is an interval of its own for each key,
@@ -1605,6 +1609,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         for (int i = 0; i < nmax; ++i) {
           const bool more = i + 1 < nmax;
           if (i < cnt[0]) issue_pv(0, vs, i == 0);
+          if (i + 1 == cnt[0]) {  // its rows go on to their output while the other slot ends
+            commit(o_full(0));
+            ++oc[0];
+          }
           const int aborted = *c.abort_flag;
           if (more) {
             ks = pos.slot;
@@ -1627,11 +1635,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
         }
         if (!ok) break;
-        for (int sl = 0; sl < 2; ++sl)
-          if (cnt[sl] > 0) {
-            commit(o_full(sl));
-            ++oc[sl];
-          }
+        if (cnt[1] > 0) {
+          commit(o_full(1));
+          ++oc[1];
+        }
       } while (cur.next(A));
       commit(final_bar);
       drain(final_bar, 0);
@@ -1782,12 +1789,17 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         tc_fence_after();
         // columns of this tile that the row sees: [0, vis]
         const int k0 = cur.tile(j) * TR;
-        const Seen seen{lim - k0, WIN ? window_begin(lim, A.window) - k0 : 0, WIN ? cur.r.sinks - k0 : 0};
+        const int vis = lim - k0;
         const uint32_t sa = tmem_row(tmem, quarter, s_col), oa = tmem_row(tmem, quarter, o_col);
-        if (__any_sync(0xffffffffu, seen.vis < TR - 1 || (WIN && seen.from > 0 && seen.upto < TR)))
-          many_softmax<D, WIN ? 2 : 1, WIN>(sa, oa, p_half(sl), lane, sl2, seen, j == cur.j0, m, l);
-        else
-          many_softmax<D, 0, WIN>(sa, oa, p_half(sl), lane, sl2, seen, j == cur.j0, m, l);
+        if (WIN) {
+          const Seen seen{vis, window_begin(lim, A.window) - k0, cur.r.sinks - k0};
+          if (__any_sync(0xffffffffu, vis < TR - 1 || (seen.from > 0 && seen.upto < TR))) hide_unseen(sa, seen);
+          many_softmax<D, false, WIN>(sa, oa, p_half(sl), lane, sl2, vis, j == cur.j0, m, l);
+        } else if (__any_sync(0xffffffffu, vis < TR - 1)) {
+          many_softmax<D, true, WIN>(sa, oa, p_half(sl), lane, sl2, vis, j == cur.j0, m, l);
+        } else {
+          many_softmax<D, false, WIN>(sa, oa, p_half(sl), lane, sl2, vis, j == cur.j0, m, l);
+        }
         tc_fence_before();
         warp_arrive(p_full(sl), lane);
       }
