@@ -25,7 +25,7 @@
 // Measured, of a stream of calls: 16385 tokens of 32 heads of 128 on 8, with the
 // store (403 MB) 69.5 us, 0.85 of the copy rate; 4095 tokens of 12 heads of 96 on
 // 4 in fp32, half of each turned (50 MB) 11.6 us, 0.64; 64 tokens of 16 heads of
-// 128 with the store 7.5 us, of which the GPU's part is 3.8.  A pass is 90
+// 128 with the store 7.5 us, of which the GPU's part is 3.8.  A pass is 102
 // instructions; with rows of one token in a pass, their pairs on different lanes
 // and the angles by CUDA's function it was 195, and the times 95.8, 13.4 and 9.9.
 #include <math.h>
