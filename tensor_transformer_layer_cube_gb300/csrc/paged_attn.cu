@@ -2197,6 +2197,28 @@ tp3d_status launch(tp3d_ctx* ctx, const PagedAttn& A, bool few, bool many, bool 
   return wide ? launch_few<D, 8, WIN>(ctx, A, many, few_parts, s) : launch_few<D, 4, WIN>(ctx, A, many, few_parts, s);
 }
 
+// Whether a windowed call is little enough work for the kernel for few rows to
+// take all of its requests, whatever rows they have.  There each block of 16
+// rows reads every key that its request's rows see (the other blocks' from L2),
+// so its time grows with blocks x keys over the SMs; the other kernel has one
+// read for 256 rows but begins later, and an item that it cuts into many parts
+// costs it their join, more the fewer items there are.  The window bounds the
+// keys of every request, so the host knows both.  Here | there, heads of 128, us:
+//   1 item   64 rows 11.8 | 17.7 (window 1167), 512 14.7 | 32.6, 1024 26.6 | 38.0 (2048), 2048 61.2 | 45.3 (4096)
+//   8 items  128 rows 18.7 | 23.4 (1167), 256 32.9 | 37.4 (2048), 256 50.1 | 43.5 (4096), 512 44.5 | 36.3 (1167)
+//   16       64 rows 18.6 | 22.5 (1167), 128 25.2 | 26.5 (1167), 128 33.1 | 29.5 (2048), 192 17.3 | 15.6 (128)
+//   32       64 rows 9.9 | 14.5 (128), 64 18.4 | 21.2 (512), 64 25.4 | 23.1 (1167)
+// Rows far beyond one another's windows do not see most of those keys: 2048 rows of 512 tokens, window 128, 22.1 | 18.1.
+// A window as wide as the tables leaves nothing out and goes the way of the call without one, to the same results.
+bool short_window(const tp3d_ctx* ctx, const PagedAttn& A, int64_t most_new) {
+  const int64_t items = (int64_t)A.requests * A.c.kv_heads, blocks = items * ((most_new * A.group + 15) / 16);
+  const int64_t keys = (int64_t)A.window + A.sinks + most_new;
+  if (A.window == 0 || most_new > 2 * (int64_t)A.window || keys >= A.width * A.c.page) return false;
+  if (items <= 0 || blocks * 8 > ctx->num_sms * 7) return false;  // measured up to 128
+  const int64_t per_sm = (1 << 14) / items;
+  return blocks * keys <= ctx->num_sms * (per_sm < 2048 ? per_sm : 2048);
+}
+
 }  // namespace
 
 size_t paged_attn_workspace(const tp3d_ctx* ctx, int d) {
@@ -2208,8 +2230,9 @@ tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* wo
     return TP3D_EUNSUPPORTED;
   // items (requests x key/value heads) that leave half of the SMs without one: see FewShape
   const bool wide = (int64_t)A.requests * A.c.kv_heads * 2 <= ctx->num_sms;
-  const int few_rows = wide ? FewShape<8>::kRows : FewShape<4>::kRows;
-  const int64_t most = (max_new > 0 && max_new < A.tokens ? max_new : A.tokens) * A.group;
+  const int64_t most_new = max_new > 0 && max_new < A.tokens ? max_new : A.tokens, most = most_new * A.group;
+  int few_rows = wide ? FewShape<8>::kRows : FewShape<4>::kRows;
+  if (short_window(ctx, A, most_new)) few_rows = (int)most;
   const bool many = most > few_rows;
   // One request that may have many rows goes to that kernel whatever it has
   // (all its rows are computed there all the same, and a launch is saved).

@@ -138,6 +138,44 @@ def test_work_split_along_the_keys(ctx, kv, new, heads, kv_heads, window, sinks)
         assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(l, l2)
 
 
+@pytest.mark.parametrize("kv,new,heads,kv_heads,d,window,sinks", [
+    ([3000], [64], 1, 1, 128, 40, 0), ([5000], [250], 8, 2, 64, 1000, 3), ([3001], [17], 48, 1, 128, 100, 20),
+    ([2500, 2000], [131, 131], 4, 2, 128, 300, 0), ([2600, 65, 0, 1900], [65, 64, 3, 1], 8, 2, 64, 513, 16),
+    ([900] * 9, [33] * 9, 8, 4, 128, 127, 1), ([40000], [513], 8, 4, 64, 257, 300), ([40000], [300], 3, 1, 128, 2000, 0),
+    ([9000, 8000], [200, 100], 2, 2, 128, 100, 5), ([9000, 8000], [201, 100], 2, 2, 128, 100, 5)])
+@pytest.mark.parametrize("max_new", [0, 600])
+def test_short_windows_over_long_contexts(ctx, kv, new, heads, kv_heads, d, window, sinks, max_new):
+    # little work for each SM: about where a call of many rows moves to the kernel for few, on either side
+    c = Window(kv, new, heads, kv_heads, d, window, sinks, 32, seed=len(kv) + window, v_mean=0.5)
+    want = None
+    for _ in range(2):
+        o, l = c.run(ctx, max_new or max(new))
+        assert t.tp3d_sync_status(ctx) == 0
+        compare(c, o, l)
+        assert want is None or (torch.equal(o, want[0]) and torch.equal(l, want[1]))
+        want = o, l
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_in_short_windows(ctx, value):
+    # blocks of 16 rows side by side: each row leaves out what it alone does not see
+    c = Window([2000, 1500], [90, 40], 4, 2, 128, 60, 3, 32, seed=5)
+    at = [(0, 1915), (0, 1990), (0, 2), (0, 1000), (1, 1470)]
+    for n, (b, pos) in enumerate(at):
+        page = int(c.table[b, pos // 32])
+        if page >= 0:
+            c.vp[page, pos % 32, :, 7 * n] = value
+    o, l = c.run(ctx)
+    assert t.tp3d_sync_status(ctx) == 0
+    for b, (q0, n) in enumerate(zip(c.q_start, c.new)):
+        for k, (r, pos) in enumerate(at):
+            if r == b:
+                sees = c.sees(b, pos)
+                column = o[int(q0):int(q0) + int(n), :, 7 * k]
+                assert bool((~torch.isfinite(column[sees])).all()) and bool(torch.isfinite(column[~sees]).all())
+    assert bool(torch.isfinite(l).all())
+
+
 @pytest.mark.parametrize("requests", [129, 1000])
 @pytest.mark.parametrize("long_every", [0, 7])
 def test_many_requests(ctx, requests, long_every):
