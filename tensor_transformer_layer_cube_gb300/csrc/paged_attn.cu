@@ -80,6 +80,12 @@ struct FewShape {
   // up to 4000, 8 heads, 32 rows 90.9 | 100.2; 16 of up to 2000, 16 heads, 30
   // rows 41.2 | 53.1.)
   static constexpr int kRows = W == 8 ? 48 : 16;
+  // With a window, where the host knows how many keys a row sees: blocks beside one another in either shape, and two of
+  // them pay with four warps too, for heads of 64 at any window, for heads of 128 at short ones.  Here | there, 32
+  // rows: 128 items, heads of 64, 8.4 | 13.9 us (window 128), 25.7 | 32.3 (1167), 61.8 | 72.7 (4096); 512 items 25.1 |
+  // 33.4, 78.6 | 93.3, 223 | 238; heads of 128, 128 items 10.8 | 15.2, 34.1 | 38.0, 83.2 | 84.7, 512 items 35.4 | 36.9, 110
+  // | 107, 330 | 275.  48 rows lose but for very short windows: 128 items of 64 13.9 | 14.1, 22.9 | 20.0 (512).
+  static constexpr int kRowsWindow = 32, kKeysWindow = 1280;
   // The end of an item counts as so many tiles in the ranges, about what it costs.  With it | without, four warps:
   // 32 requests of up to 4096 keys, 16 heads 85 | 94 us (one box); 100 of 700 41.8 | 60.9; 200 of 2000, 8 heads 127 | 145 (1:
   // 131, 3: 128).  With eight an item has several CTAs.
@@ -209,6 +215,7 @@ __device__ __forceinline__ int window_begin(int p, int window) { return p >= win
 template <int W, bool WIN>
 struct FewCursor {
   using Shape = FewShape<W>;
+  static constexpr bool kBlocks = WIN || Shape::kRows > 16;  // a request may have several
   Gap gap;
   int low;  // the first key of the first row's window
   int b, h, row0, tile, end, tiles, n, kv, at, u1;  // u1: the range's end (before it is moved)
@@ -239,7 +246,7 @@ struct FewCursor {
   // an item's length in the sequence
   __device__ int span() const { return tiles + Shape::kEnd; }
   // blocks of 16 rows (of a request that is this kernel's)
-  __device__ int blocks(const PagedAttn& A) const { return Shape::kRows > 16 ? (n * A.group + 15) / 16 : 1; }
+  __device__ int blocks(const PagedAttn& A) const { return kBlocks ? (n * A.group + 15) / 16 : 1; }
   // where a boundary `off` tiles into an item comes to lie
   __device__ int snap(int off) const {
     const int rest = tiles - off;
@@ -256,7 +263,7 @@ struct FewCursor {
     at += span();
     if (at >= u1) return false;
     row0 += 16;
-    if (Shape::kRows > 16 && row0 < n * A.group) return share();
+    if (kBlocks && row0 < n * A.group) return share();
     row0 = 0;
     if (++h == A.c.kv_heads) {
       h = 0;
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(FewShape<W>::kThreads, FewShape<W>::kPerSm)
     c.take(A, alone);
     const int off = u0 - sh.before;
     const int item = off / c.span(), blocks = c.blocks(A);
-    c.h = Shape::kRows > 16 ? item / blocks : item;
+    c.h = c.kBlocks ? item / blocks : item;
     c.row0 = (item - c.h * blocks) * 16;
     const int into = off - item * c.span();
     c.at = u0 - into;
@@ -2197,6 +2204,14 @@ tp3d_status launch(tp3d_ctx* ctx, const PagedAttn& A, bool few, bool many, bool 
   return wide ? launch_few<D, 8, WIN>(ctx, A, many, few_parts, s) : launch_few<D, 4, WIN>(ctx, A, many, few_parts, s);
 }
 
+// The most keys that the rows of a request see between them, or 0 where the
+// window is as wide as the tables: that leaves nothing out and goes the way of
+// the call without one, to the same results.
+int64_t window_keys(const PagedAttn& A, int64_t most_new) {
+  const int64_t keys = (int64_t)A.window + A.sinks + most_new;
+  return A.window > 0 && keys < A.width * A.c.page ? keys : 0;
+}
+
 // Whether a windowed call is little enough work for the kernel for few rows to
 // take all of its requests, whatever rows they have.  There each block of 16
 // rows reads every key that its request's rows see (the other blocks' from L2),
@@ -2209,11 +2224,10 @@ tp3d_status launch(tp3d_ctx* ctx, const PagedAttn& A, bool few, bool many, bool 
 //   16       64 rows 18.6 | 22.5 (1167), 128 25.2 | 26.5 (1167), 128 33.1 | 29.5 (2048), 192 17.3 | 15.6 (128)
 //   32       64 rows 9.9 | 14.5 (128), 64 18.4 | 21.2 (512), 64 25.4 | 23.1 (1167)
 // Rows far beyond one another's windows do not see most of those keys: 2048 rows of 512 tokens, window 128, 22.1 | 18.1.
-// A window as wide as the tables leaves nothing out and goes the way of the call without one, to the same results.
 bool short_window(const tp3d_ctx* ctx, const PagedAttn& A, int64_t most_new) {
   const int64_t items = (int64_t)A.requests * A.c.kv_heads, blocks = items * ((most_new * A.group + 15) / 16);
-  const int64_t keys = (int64_t)A.window + A.sinks + most_new;
-  if (A.window == 0 || most_new > 2 * (int64_t)A.window || keys >= A.width * A.c.page) return false;
+  const int64_t keys = window_keys(A, most_new);
+  if (keys == 0 || most_new > 2 * (int64_t)A.window) return false;
   if (items <= 0 || blocks * 8 > ctx->num_sms * 7) return false;  // measured up to 128
   const int64_t per_sm = (1 << 14) / items;
   return blocks * keys <= ctx->num_sms * (per_sm < 2048 ? per_sm : 2048);
@@ -2232,7 +2246,11 @@ tp3d_status launch_paged_attn(tp3d_ctx* ctx, PagedAttn& A, int max_new, void* wo
   const bool wide = (int64_t)A.requests * A.c.kv_heads * 2 <= ctx->num_sms;
   const int64_t most_new = max_new > 0 && max_new < A.tokens ? max_new : A.tokens, most = most_new * A.group;
   int few_rows = wide ? FewShape<8>::kRows : FewShape<4>::kRows;
-  if (short_window(ctx, A, most_new)) few_rows = (int)most;
+  if (short_window(ctx, A, most_new))
+    few_rows = most > few_rows ? (int)most : few_rows;
+  else if (!wide && window_keys(A, most_new) > 0 &&
+           (A.c.head_dim == 64 || (int64_t)A.window + A.sinks <= FewShape<4>::kKeysWindow))
+    few_rows = FewShape<4>::kRowsWindow;
   const bool many = most > few_rows;
   // One request that may have many rows goes to that kernel whatever it has
   // (all its rows are computed there all the same, and a launch is saved).

@@ -156,6 +156,20 @@ def test_short_windows_over_long_contexts(ctx, kv, new, heads, kv_heads, d, wind
         want = o, l
 
 
+@pytest.mark.parametrize("heads,kv_heads,d,new", [(16, 4, 64, 8), (16, 4, 128, 8), (4, 4, 64, 33), (28, 4, 128, 3), (4, 4, 128, 17)])
+@pytest.mark.parametrize("window,sinks", [(10, 0), (100, 3), (700, 16), (1290, 5), (1400, 0)])
+def test_short_chunks_of_many_requests(ctx, heads, kv_heads, d, new, window, sinks):
+    # two blocks of 16 rows (the second one cut short, or none) in a call of many items, and lengths beside the limit
+    rng = np.random.default_rng(new)
+    kv = np.concatenate([rng.integers(0, 2000, 36), [1500, new, new + 1, 0]])
+    fresh = np.minimum(kv, np.concatenate([rng.integers(0, new + 1, 36), [new, new, new, 0]]))
+    c = Window(kv, fresh, heads, kv_heads, d, window, sinks, 16, seed=new + window, v_mean=0.5)
+    for most in (None, 0):
+        o, l = c.run(ctx, most)
+        assert t.tp3d_sync_status(ctx) == 0
+        compare(c, o, l)
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 def test_values_that_are_not_finite_in_short_windows(ctx, value):
     # blocks of 16 rows side by side: each row leaves out what it alone does not see
