@@ -5,8 +5,7 @@
 // Row x of one head at position p: n = x s w with s = 1 / sqrt(mean x^2 + eps),
 // y = R(p) n.  R turns pairs of columns by p f_j; with the frequency as a 64-bit
 // fraction F of a turn, the angle is p F mod 2^64: an integer product that
-// drops whole turns by itself, of which the upper 32 bits are as many as fp32
-// can use.
+// drops whole turns by itself, rounded to fp32 when whole quarter turns are off.
 //
 // Every element is read once and written once, so HBM bounds many tokens and
 // latency few; instructions come close behind, so a pass is made of few.  A row
@@ -132,12 +131,18 @@ struct Row<float> {
   }
 };
 
-// Sine and cosine of an angle in units of 2^-32 turns: an integer number of
-// quarter turns off, what is left (an eighth of a turn at most) goes through the
-// Taylor series, whose next terms are below 2^-29 and 2^-33; to about 2 2^-24.
-__device__ __forceinline__ void sincos_of(uint32_t turn, float& s, float& c) {
-  const uint32_t q = (turn + 0x20000000u) >> 30;
-  const float t = (float)(int32_t)(turn - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+// Sine and cosine of an angle in units of 2^-64 turns: a whole number of quarter
+// turns off, what is left (an eighth of a turn at most) goes through the Taylor
+// series, whose next terms are below 2^-29 and 2^-33.  Either is off by 5 2^-24 of
+// itself at most, small ones too: a slow pair's sine is as small as its angle, and
+// stands alone where the pair's other column is small.  (The upper 32 bits alone
+// leave 5.6e-6 off by 2.5e-4 of itself, and cost as much: 4095 tokens in fp32 11.9 us
+// both, and with one conversion of all 64 bits 12.4.)
+__device__ __forceinline__ void sincos_of(uint64_t turn, float& s, float& c) {
+  const uint32_t hi = (uint32_t)(turn >> 32), lo = (uint32_t)turn, q = (hi + 0x20000000u) >> 30;
+  // the halves as signed numbers, so that neither takes much of the other away; by 2 pi / 2^32 and 2 pi / 2^64
+  const float t = fmaf((float)(int32_t)(hi - (q << 30) + (lo >> 31)), 1.4629180792671596e-9f,
+                       (float)(int32_t)lo * 3.4061215800865545e-19f);
   const float x = t * t;
   const float a = fmaf(t * x, fmaf(x, fmaf(x, fmaf(x, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), t);
   const float b = fmaf(
@@ -167,8 +172,7 @@ struct Turn {
     const int hop = INTER ? A.rot / 4 - 2 : 0;  // from the first group's pairs to the second's
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint64_t turn = (uint64_t)(int64_t)pos * ld_plain(turns + (e < 2 ? e : e + hop));
-      sincos_of((uint32_t)(turn >> 32), sn[e], cs[e]);
+      sincos_of((uint64_t)(int64_t)pos * ld_plain(turns + (e < 2 ? e : e + hop)), sn[e], cs[e]);
       cs[e] *= A.magnitude;
       sn[e] *= A.magnitude;
     }
