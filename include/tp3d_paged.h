@@ -213,9 +213,13 @@ typedef struct {
  * tp3d_paged_plan.  A request that is cut back into a page that it shares is
  * forked to its new length before it is written.
  * A row out of range, a dst row that is another dst or a src, a length that is
- * negative or longer than the row, a last page without a valid entry, or too few
- * free pages raise TP3D_EPAGES, and nothing but *copy_count = 0 and *free_left is
- * written.  forks <= 16384 (else TP3D_EUNSUPPORTED).                           */
+ * negative or longer than the row, a last page without a valid entry, a free
+ * count out of range, too few free pages, or one to be taken that is outside the
+ * pool raise TP3D_EPAGES, and nothing but *copy_count = 0 and *free_left (the free
+ * count, kept within [0, free_cap]) is written.  An entry of a whole page that is
+ * past the pool raises TP3D_EPAGES too, but becomes -1 in row dst[i] and holds up
+ * nothing else.  That the free list names no page twice, and none that a row
+ * names, is the caller's to keep.  forks <= 16384 (else TP3D_EUNSUPPORTED).    */
 tp3d_status tp3d_paged_fork(tp3d_ctx* ctx, const tp3d_page_pool* pool, int forks, const int32_t* src,
                             const int32_t* dst, const int32_t* len, const int32_t* free_count, int32_t* free_left,
                             int32_t* copy_from, int32_t* copy_to, int32_t* copy_count, void* stream);

@@ -17,7 +17,8 @@ def fork(page, table, shares, free, count, src, dst, length):
         bad |= not (0 <= s < rows and 0 <= d < rows and 0 <= n <= width * page)
         if not bad and n % page:
             bad |= not 0 <= table[s, n // page] < len(shares)
-    bad |= sum(n % page > 0 for _, _, n in whole) > left
+    fresh = sum(n % page > 0 for _, _, n in whole)
+    bad |= fresh > left or not all(0 <= int(p) < len(shares) for p in free[max(left - fresh, 0):left])
     if bad:
         return table, shares, left, [], False
     fits = True
