@@ -110,6 +110,7 @@ class tp3d_rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("magnitude", ctypes.c_float), ("turns", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
                 ("k_weight", ctypes.c_void_p)]
+    on_host = False  # rope() was given tensors of the host, which no kernel can use
 
 
 class tp3d_rect(ctypes.Structure):
@@ -531,6 +532,9 @@ def tp3d_paged_copy(ctx, cache: tp3d_kv_cache, copies: int, copy_from, copy_to, 
 
 def tp3d_rope_turns(rotary_dim, base, kind, factor, context, turns) -> tuple:
     """(status, magnitude); ``turns``: a host tensor of int64 words, rotary_dim / 2 of them, or None."""
+    if turns is not None and (_dtype_of(turns) != _I64 or turns.device.type != "cpu" or not turns.is_contiguous() or
+                              turns.numel() < rotary_dim // 2):
+        raise ValueError("tp3d_rope_turns: rotary_dim / 2 contiguous int64 words in host memory")
     m = ctypes.c_float(0.0)
     st = lib().tp3d_rope_turns(rotary_dim, base, kind, factor, context, _p(turns), ctypes.byref(m))
     return st, m.value
@@ -561,8 +565,17 @@ def rope(turns, dtype, head_dim: int, rotary_dim: int, interleaved: bool = False
     for w in (q_weight, k_weight):
         if w is not None and (w.dtype != dtype or not w.is_contiguous() or w.numel() != head_dim):
             raise ValueError("rope: weights of head_dim contiguous elements of the heads' type")
-    return tp3d_rope(code, head_dim, rotary_dim, int(interleaved), int(norm), eps, magnitude, _p(turns), _p(q_weight),
-                     _p(k_weight))
+    r = tp3d_rope(code, head_dim, rotary_dim, int(interleaved), int(norm), eps, magnitude, _p(turns), _p(q_weight),
+                  _p(k_weight))
+    used = ([turns] if rotary_dim else []) + ([q_weight, k_weight] if norm else [])
+    r.on_host = any(x is not None and not x.is_cuda for x in used)
+    return r
+
+
+def _on_device(what, rope):
+    """Last of a call's checks: the descriptor's tensors, of which the kernels get the addresses."""
+    if rope.on_host:
+        raise TypeError(f"{what}: turns and weights in device memory (rope_turns makes a host tensor)")
 
 
 _row_strides = {}  # by a tensor's strides
@@ -605,8 +618,9 @@ def tp3d_qk_rope(ctx, rope: tp3d_rope, Q, K, positions, Q_out, K_out, stream=Non
     n = qs[0]
     if ks[0] != n:
         raise ValueError("tp3d_qk_rope: Q and K of the same tokens")
-    return lib().tp3d_qk_rope(ctx, rope, n, qs[1], ks[1], q, qst, k, kst, _positions(what, positions, n), qo, qost, ko,
-                              kost, _s(stream))
+    at = _positions(what, positions, n)
+    _on_device(what, rope)
+    return lib().tp3d_qk_rope(ctx, rope, n, qs[1], ks[1], q, qst, k, kst, at, qo, qost, ko, kost, _s(stream))
 
 
 def tp3d_qk_rope_bwd(ctx, rope: tp3d_rope, Q, K, positions, dQ_out, dK_out, dQ, dK, dq_weight, dk_weight, workspace,
@@ -625,8 +639,10 @@ def tp3d_qk_rope_bwd(ctx, rope: tp3d_rope, Q, K, positions, dQ_out, dK_out, dQ, 
     for w in (dq_weight, dk_weight):
         if w is not None and (_dtype_of(w) != rope.dtype or not w.is_contiguous() or w.numel() != rope.head_dim):
             raise ValueError("tp3d_qk_rope_bwd: weights' gradients of head_dim contiguous elements of the heads' type")
-    return lib().tp3d_qk_rope_bwd(ctx, rope, n, qs[1], ks[1], q, qst, k, kst, _positions(what, positions, n), gq, gqst,
-                                  gk, gkst, dq, dqst, dk, dkst, _p(dq_weight), _p(dk_weight), _p(workspace), _s(stream))
+    at = _positions(what, positions, n)
+    _on_device(what, rope)
+    return lib().tp3d_qk_rope_bwd(ctx, rope, n, qs[1], ks[1], q, qst, k, kst, at, gq, gqst, gk, gkst, dq, dqst, dk, dkst,
+                                  _p(dq_weight), _p(dk_weight), _p(workspace), _s(stream))
 
 
 _no_strides = tp3d_row_strides(0, 0)
@@ -647,8 +663,10 @@ def tp3d_paged_rope_store(ctx, rope: tp3d_rope, cache: tp3d_kv_cache, Q, K, V, p
         raise ValueError("tp3d_paged_rope_store: K and V of Q's tokens and the cache's heads")
     if _dtype_of(slots) != _I64 or slots.numel() < n or not slots.is_contiguous():
         raise ValueError("tp3d_paged_rope_store: an int64 slot for each token")
-    return lib().tp3d_paged_rope_store(ctx, rope, cache, n, qs[1], q, qst, k, kst, v, vst, _positions(what, positions, n),
-                                       slots.data_ptr(), qo, qost, _s(stream))
+    at = _positions(what, positions, n)
+    _on_device(what, rope)
+    return lib().tp3d_paged_rope_store(ctx, rope, cache, n, qs[1], q, qst, k, kst, v, vst, at, slots.data_ptr(), qo, qost,
+                                       _s(stream))
 
 
 # ---------------------------------------------------------------------------
