@@ -232,9 +232,10 @@ tp3d_status tp3d_paged_fork(tp3d_ctx* ctx, const tp3d_page_pool* pool, int forks
  * back, the columns past its new length; one with a sliding window (and pages of
  * first tokens that stay), those behind the window.
  * Columns out of range (that row then gives up nothing), entries past the pool,
- * a page that loses more owners than it has (it is freed once), and a free list
- * that is full raise TP3D_EPAGES.  That a row names no page which is free already
- * is the caller's to keep.                                                    */
+ * a page that loses more owners than it has (it is freed once), a free_count out
+ * of range (kept within [0, free_cap]), and a free list that is full raise
+ * TP3D_EPAGES.  That a row names no page which is free already is the caller's to
+ * keep.                                                                       */
 tp3d_status tp3d_paged_free(tp3d_ctx* ctx, const tp3d_page_pool* pool, const int32_t* first, const int32_t* end,
                             const int32_t* free_count, int32_t* free_left, void* stream);
 

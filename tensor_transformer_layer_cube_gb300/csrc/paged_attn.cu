@@ -85,6 +85,11 @@ struct FewShape {
   // rows: 128 items, heads of 64, 8.4 | 13.9 us (window 128), 25.7 | 32.3 (1167), 61.8 | 72.7 (4096); 512 items 25.1 |
   // 33.4, 78.6 | 93.3, 223 | 238; heads of 128, 128 items 10.8 | 15.2, 34.1 | 38.0, 83.2 | 84.7, 512 items 35.4 | 36.9, 110
   // | 107, 330 | 275.  48 rows lose but for very short windows: 128 items of 64 13.9 | 14.1, 22.9 | 20.0 (512).
+  // With heads of 128 the limit does not win everywhere.  Over 80 to 512 items, 20 to 32 rows and windows of 128 to
+  // 1280, lengths alike and not, the time here is 0.61 to 1.16 of that there, 0.87 in the mean, above 1.03 at 79 of
+  // 1096 points: where the ends of tiles and ranges fall badly, 112 to 144 items with windows of 384 to 704 0.65 to 1.16 (0.97 in the mean; 128
+  // items, 32 rows, window 512: 25.2 | 22.6, 448 with unequal lengths 0.86), 256 of 512 37.4 | 36.2, 384 and 512 items
+  // of 128 to 256 0.86 to 1.12.  No limit on items and window tells these from their neighbours.
   static constexpr int kRowsWindow = 32, kKeysWindow = 1280;
   // The end of an item counts as so many tiles in the ranges, about what it costs.  With it | without, four warps:
   // 32 requests of up to 4096 keys, 16 heads 85 | 94 us (one box); 100 of 700 41.8 | 60.9; 200 of 2000, 8 heads 127 | 145 (1:

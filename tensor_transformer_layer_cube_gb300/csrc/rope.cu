@@ -23,7 +23,7 @@
 //
 // Measured, of a stream of calls: 16385 tokens of 32 heads of 128 on 8, with the
 // store (403 MB) 69.5 us, 0.85 of the copy rate; 4095 tokens of 12 heads of 96 on
-// 4 in fp32, half of each turned (50 MB) 11.6 us, 0.64; 64 tokens of 16 heads of
+// 4 in fp32, half of each turned (50 MB) 12.0 us, 0.62; 64 tokens of 16 heads of
 // 128 with the store 7.5 us, of which the GPU's part is 3.8.  A pass is 102
 // instructions; with rows of one token in a pass, their pairs on different lanes
 // and the angles by CUDA's function it was 195, and the times 95.8, 13.4 and 9.9.
@@ -136,8 +136,8 @@ struct Row<float> {
 // series, whose next terms are below 2^-29 and 2^-33.  Either is off by 5 2^-24 of
 // itself at most, small ones too: a slow pair's sine is as small as its angle, and
 // stands alone where the pair's other column is small.  (The upper 32 bits alone
-// leave 5.6e-6 off by 2.5e-4 of itself, and cost as much: 4095 tokens in fp32 11.9 us
-// both, and with one conversion of all 64 bits 12.4.)
+// leave 5.6e-6 off by 2.5e-4 of itself.  4095 tokens in fp32 12.0 us, with those alone
+// 11.9, with one conversion of all 64 bits 12.4.)
 __device__ __forceinline__ void sincos_of(uint64_t turn, float& s, float& c) {
   const uint32_t hi = (uint32_t)(turn >> 32), lo = (uint32_t)turn, q = (hi + 0x20000000u) >> 30;
   // the halves as signed numbers, so that neither takes much of the other away; by 2 pi / 2^32 and 2 pi / 2^64
